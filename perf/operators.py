@@ -236,8 +236,7 @@ def _plan_attn(case):
     from all_gather_gemm_amd import attention
     return attention.DecodeAttention(case["q_heads"], case["kv_heads"], case["dim"],
                                      dtype=case["dtype"], storage=case["storage"],
-                                     max_batch=case["batch"], window=case["window"],
-                                     soft_cap=case["cap"])
+                                     window=case["window"], soft_cap=case["cap"])
 
 
 def _inputs(case, seed):
