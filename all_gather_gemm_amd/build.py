@@ -15,7 +15,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libagmm.so")
 RESOURCES = os.path.join(HERE, "kernel_resources.json")
-SOURCES = ["agmm_kernels.hip", "agmm_static.hip", "agmm_api.cpp"]
+SOURCES = ["agmm_kernels.hip", "agmm_static.hip", "agmm_api.cpp", "agmm_rope_kv.hip",
+           "agmm_attn.hip", "agmm_attn_api.cpp"]
 LLVM_BIN = "/opt/rocm/llvm/bin"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

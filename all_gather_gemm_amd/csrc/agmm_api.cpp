@@ -517,6 +517,10 @@ void release_streams(agmm_handle* h) {
 
 }  // namespace
 
+namespace agmm {
+void set_last_hip_error(int e) { g_last_hip = e; }
+}  // namespace agmm
+
 extern "C" {
 
 void ag_matmul_desc_init(agmm_desc* d) {

@@ -1,0 +1,601 @@
+// gfx950 kernel of the attention of one new token over a paged key-value cache (agmm_attn.h).
+//
+// Mathematics, for one sequence and one kv head with its G q heads: S = K Q^T (tokens x G), a
+// softmax over the tokens with a running maximum m and sum l in 32 bits, O^T = V^T P^T. Each cached
+// byte is used for G <= 16 q heads, 4 G flop per 16-bit value, so the bound is the memory
+// bandwidth and the kernel is built around keeping loads in flight:
+//
+//  - Matrix instructions of 16 tokens x 16 q heads read K straight from global memory: a lane's
+//    operand is 8 values of one token's row, which is 16 contiguous bytes. The order of the inner
+//    dimension is free as long as Q has the same, so 8-bit and 4-bit rows are read 16 bytes a lane
+//    too. Nothing passes through LDS on the way.
+//  - S^T's accumulator layout (lane = q head, 4 consecutive tokens) is, for a pair of 16-token
+//    tiles, the operand layout of P^T for 32 tokens in the order {4 g .. 4 g + 3, 16 + 4 g ..}, so
+//    P never moves between lanes.
+//  - V^T needs 8 tokens of one element in a lane. A lane loads 8 elements (16 bytes) of each of its
+//    8 tokens, 16 lanes covering whole rows, and transposes 8 x 8 in registers with v_perm_b32;
+//    matrix instruction e takes element 8 c + e of chunk c, so lane c's accumulators end up holding
+//    32 consecutive elements of the output.
+//  - Codes are turned into the 16-bit type, scale included, by one v_cvt_scalef32_pk per pair.
+//  - The maximum is raised only when a tile's exceeds it by 2^8 or more, so the accumulators are
+//    rescaled a few times a sequence; weights are kept up to 2^15 (a maximum of 2^7 plus the 2^8),
+//    where the fp16 operand has its full precision and room below.
+//
+// Work: the tiles (128 tokens) of all sequences and heads, in that order, are cut into equal runs, one
+// for each workgroup, from the lengths on the device. A run may begin and end inside a sequence's
+// head; such a head's pieces are joined by the last workgroup to finish one, in the order of the
+// pieces (16 at a time, and then the groups of 16), so results do not depend on timing.
+#include "agmm_attn_device.h"
+
+namespace agmm {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kWaveTokens = 32;
+static_assert(kWaves * kWaveTokens == kAttnTile, "a workgroup's tile is one step of its waves");
+constexpr int kJoin = 16;            // pieces joined at once
+constexpr float kHead = 7.0f;        // weights are 2^(s - m + kHead)
+constexpr float kUnhead = 0x1p-7f;   // 2^-kHead
+constexpr float kRaise = 8.0f;       // raise the maximum when a tile's is above it by this
+
+// Sum or maximum over the 4 lane groups of 16 (lanes l, l ^ 16, l ^ 32, l ^ 48).
+__device__ inline float across_max(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ inline float across_sum(float x) {
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
+// Loads of a tile of 32 tokens by one wave, as they come from memory.
+template <int ST, int DP>
+struct Raw {
+  static constexpr int kSteps = DP / 32;  // matrix instructions over the head for 16 tokens
+  // K: loads a lane makes for one token, and words in each
+  static constexpr int kWords = ST == AG_KV_MXFP4 && DP == 64 ? 2 : 4;
+  static constexpr int kLoads = ST == AG_KV_16BIT ? DP / 32
+                                : ST == AG_KV_MXFP8 ? DP / 64 : (DP == 64 ? 1 : DP / 128);
+  static constexpr int kPer = kSteps / kLoads;  // matrix instructions a load feeds
+  static constexpr int kScales = ST == AG_KV_16BIT ? 0 : (DP == 256 ? 2 : 1);  // scale words a row
+  // V: chunks of 8 elements a lane takes of each token, and words in a chunk
+  static constexpr int kChunks = DP == 256 ? 2 : 1;
+  static constexpr int kVWords = ST == AG_KV_16BIT ? 4 : ST == AG_KV_MXFP8 ? 2 : 1;
+
+  uint32_t k[2][kLoads][kWords];
+  uint32_t ks[2][kScales ? kScales : 1];
+  uint32_t v[8][kChunks][kVWords];
+  uint32_t vs[8][kScales ? kChunks : 1];
+  uint32_t valid;  // bit j: token j of this lane's 8 is attended to
+
+  // First element of a lane's operand in matrix instruction `step`, lane group g.
+  __device__ static inline int first(int step, int g) {
+    const int load = step / kPer, part = step % kPer;
+    return load * 32 * kPer + g * 8 * kPer + part * 8;
+  }
+};
+
+template <int N>
+__device__ inline void load_words(uint32_t (&w)[N], const char* p) {
+  if constexpr (N == 4) {
+    const u32x4 t = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = t[i];
+  } else if constexpr (N == 2) {
+    const u32x2 t = *reinterpret_cast<const u32x2*>(p);
+    w[0] = t[0];
+    w[1] = t[1];
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+template <int DT, int ST, int DP>
+struct Wave {
+  typedef Raw<ST, DP> R;
+  static constexpr int kAcc = 8 * R::kChunks;
+
+  u32x4 q[R::kSteps];
+  f32x4 acc[kAcc];
+  float m, l;  // of this lane's q head; l of this lane's tokens alone
+
+  __device__ inline void start(const AttnParams& p, int64_t b, int head0, int n) {
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    const uint16_t* row = p.q + b * p.q_batch + (int64_t)(head0 + (col < n ? col : 0)) * p.q_head;
+#pragma unroll
+    for (int i = 0; i < R::kSteps; ++i) {
+      const int e = R::first(i, g);
+      q[i] = u32x4{0, 0, 0, 0};
+      if (col < n && e < p.c.head_dim) q[i] = load16(row + e);
+    }
+#pragma unroll
+    for (int i = 0; i < kAcc; ++i) acc[i] = f32x4{0, 0, 0, 0};
+    m = -INFINITY;
+    l = 0.0f;
+  }
+
+  // Issues the loads of 32 tokens whose places (data and scale offsets, -1: not attended to) are
+  // in `at`; nothing is read for the others, and their values count as zeros.
+  __device__ static inline void load(R& r, const AttnParams& p, const int64_t (*at)[2],
+                                     int64_t head, int64_t s_head) {
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    const int hd = p.c.head_dim;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int64_t off = at[16 * t + col][0], soff = at[16 * t + col][1];
+#pragma unroll
+      for (int i = 0; i < R::kLoads; ++i) {
+#pragma unroll
+        for (int w = 0; w < R::kWords; ++w) r.k[t][i][w] = 0;
+        const int e = R::first(i * R::kPer, g);
+        if (off >= 0 && e < hd) {
+          const int64_t byte = ST == AG_KV_16BIT ? 2 * e : ST == AG_KV_MXFP8 ? e : e / 2;
+          load_words<R::kWords>(r.k[t][i], p.c.k + off + head + byte);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < R::kScales; ++i) {
+        r.ks[t][i] = 0;
+        // (the bytes behind the row's last block hold anything: 255 would make its zeros NaN)
+        if (off >= 0 && 128 * i < hd)
+          r.ks[t][i] = *reinterpret_cast<const uint32_t*>(p.c.ks + soff + s_head + 4 * i) &
+                       (hd - 128 * i >= 128 ? ~0u : (1u << (hd - 128 * i) / 4) - 1u);
+      }
+    }
+    r.valid = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int t = (j < 4 ? 0 : 16) + 4 * g + (j & 3);
+      const int64_t off = at[t][0], soff = at[t][1];
+      r.valid |= (off >= 0 ? 1u : 0u) << j;
+#pragma unroll
+      for (int c = 0; c < R::kChunks; ++c) {
+        const int e = 128 * c + 8 * col;
+#pragma unroll
+        for (int w = 0; w < R::kVWords; ++w) r.v[j][c][w] = 0;
+        if (R::kScales) r.vs[j][c] = 0;
+        if (off >= 0 && e < hd) {
+          const int64_t byte = ST == AG_KV_16BIT ? 2 * e : ST == AG_KV_MXFP8 ? e : e / 2;
+          load_words<R::kVWords>(r.v[j][c], p.c.v + off + head + byte);
+          if (R::kScales)
+            r.vs[j][c] = *reinterpret_cast<const uint8_t*>(p.c.vs + soff + s_head + e / 32);
+        }
+      }
+    }
+  }
+
+  // The K operand of matrix instruction `step` for token tile t.
+  __device__ static inline u32x4 key(const R& r, int t, int step, int g) {
+    const int i = step / R::kPer, part = step % R::kPer;
+    if constexpr (ST == AG_KV_16BIT) {
+      return u32x4{r.k[t][i][0], r.k[t][i][1], r.k[t][i][2], r.k[t][i][3]};
+    } else {
+      const int block = R::first(step, 0) / 32 + (g * R::kPer * 8) / 32;
+      const uint32_t word = R::kScales == 2 && block >= 4 ? r.ks[t][R::kScales - 1] : r.ks[t][0];
+      const float s = scale_of((word >> (8 * (block & 3))) & 255u);
+      if constexpr (ST == AG_KV_MXFP8)
+        return from_fp8x8<DT>(r.k[t][i][2 * part], r.k[t][i][2 * part + 1], s);
+      else
+        return from_fp4x8<DT>(r.k[t][i][part], s);
+    }
+  }
+
+  __device__ inline void step(const R& r, const AttnParams& p) {
+    const int lane = threadIdx.x & 63, g = lane >> 4;
+    f32x4 st[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      st[t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < R::kSteps; ++i) st[t] = T16<DT>::mfma(key(r, t, i, g), q[i], st[t]);
+    }
+    // scores in base 2; the capped ones by tanh x = 1 - 2 / (e^2x + 1)
+    float s[8], top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float x = st[j >> 2][j & 3];
+      if (p.cap != 0.0f) {
+        const float e = __builtin_amdgcn_exp2f(x * p.inv_cap);
+        x = p.cap - 2.0f * p.cap / (e + 1.0f);
+      } else {
+        x *= p.scale;
+      }
+      s[j] = (r.valid >> j) & 1u ? x : -INFINITY;
+      top = fmaxf(top, s[j]);
+    }
+    top = across_max(top);
+    if (__any(top > m + kRaise)) {
+      const float raised = fmaxf(m, top);
+      const float f = raised == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
+#pragma unroll
+      for (int i = 0; i < kAcc; ++i)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) acc[i][w] *= f;
+      l *= f;
+      m = raised;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m - kHead;
+    u32x4 hi, lo;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = __builtin_amdgcn_exp2f(s[2 * j] - ref);
+      const float b = __builtin_amdgcn_exp2f(s[2 * j + 1] - ref);
+      l += a + b;
+      if (DT == AGMM_F16) {
+        hi[j] = T16<DT>::pack(a, b);  // 11 bits of a weight
+      } else {
+        // bf16 weights keep 8 bits: what cutting them there leaves goes into a second operand, 16 in
+        // all. That part is kept above 0 (by 2^-126), since 0 times an infinite value is NaN.
+        const uint32_t ab = __builtin_bit_cast(uint32_t, a), bb = __builtin_bit_cast(uint32_t, b);
+        hi[j] = __builtin_amdgcn_perm(bb, ab, 0x07060302u);
+        lo[j] = T16<DT>::pack(fmaxf(a - T16<DT>::hi(ab), 0x1p-126f), fmaxf(b - T16<DT>::hi(bb), 0x1p-126f));
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < R::kChunks; ++c) {
+      u32x4 v[8];  // 8 tokens x 8 elements
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (ST == AG_KV_16BIT)
+          v[j] = u32x4{r.v[j][c][0], r.v[j][c][1], r.v[j][c][2], r.v[j][c][3]};
+        else if constexpr (ST == AG_KV_MXFP8)
+          v[j] = from_fp8x8<DT>(r.v[j][c][0], r.v[j][c][1], scale_of(r.vs[j][c]));
+        else
+          v[j] = from_fp4x8<DT>(r.v[j][c][0], scale_of(r.vs[j][c]));
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        u32x4 a;  // 8 tokens of element e
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          a[j] = __builtin_amdgcn_perm(v[2 * j + 1][e / 2], v[2 * j][e / 2],
+                                       e % 2 ? 0x07060302u : 0x05040100u);
+        acc[8 * c + e] = T16<DT>::mfma(a, hi, acc[8 * c + e]);
+        if (DT == AGMM_BF16) acc[8 * c + e] = T16<DT>::mfma(a, lo, acc[8 * c + e]);
+      }
+    }
+  }
+};
+
+// A partial result: 16 rows of DP sums, the rows' maxima (base 2, less kHead), the rows' sums.
+template <int DP>
+constexpr int kPartial = 16 * DP + 32;
+
+struct Place {  // what the workgroup works on: tokens [first, end) of sequence b
+  int64_t first, end;
+};
+__device__ inline Place tokens_of(const AttnParams& p, int b) {
+  const int n = min(max(p.lens[b], 0), p.capacity);
+  const int64_t len = max(p.lens[b], 0);
+  const int64_t first = p.window > 0 ? max((int64_t)0, len - p.window) : 0;
+  return Place{min(first, (int64_t)n), n};
+}
+__device__ inline uint32_t tiles_of(const AttnParams& p, int b) {
+  const Place w = tokens_of(p, b);
+  return (uint32_t)((w.end - w.first + kAttnTile - 1) / kAttnTile);
+}
+
+__device__ inline uint32_t wave_sum(uint32_t x) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) x += (uint32_t)__shfl_xor((int)x, d);
+  return x;
+}
+// Sum over the lanes up to and with this one.
+__device__ inline uint32_t wave_scan(uint32_t x) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t y = (uint32_t)__shfl_up((int)x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
+template <int DP>
+struct Shared {
+  int64_t at[kWaves][kWaveTokens][2];
+  float m[kWaves][16], l[kWaves][16];
+  float acc[kWaves][16][DP + 4];
+  uint32_t last;
+};
+
+__device__ inline void write_out(uint16_t* w, uint32_t a, uint32_t b) {
+  typedef u32x2 u32x2_any __attribute__((aligned(2)));
+  *reinterpret_cast<u32x2_any*>(w) = u32x2{a, b};
+}
+
+// Elements e .. e + 3 of a row: o over the row's sum l, and the row's lse with element 0.
+template <int DT>
+__device__ inline void finish(const AttnParams& p, int64_t b, int head, int e, f32x4 o, float m,
+                              float l) {
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // 0: nothing was attended to
+  write_out(p.out + b * p.o_batch + (int64_t)head * p.o_head + e,
+            T16<DT>::pack(o[0] * inv, o[1] * inv), T16<DT>::pack(o[2] * inv, o[3] * inv));
+  if (e == 0 && p.lse)
+    p.lse[b * p.q_heads + head] =
+        l == 0.0f ? -INFINITY
+                  : (m + __builtin_amdgcn_logf(l * kUnhead)) * 0.69314718055994531f;
+}
+
+// Joins `count` partial results for n q heads: of workgroups wg0, wg0 + stride, ..., the one of
+// workgroup `begin`, where the head's tiles begin, in slot 1 and the others in slot 0. final: the
+// output; else a partial result again, in the place of the first.
+template <int DT, int DP>
+__device__ void join(const AttnParams& p, uint32_t wg0, uint32_t stride, uint32_t count,
+                     uint32_t begin, int64_t b, int head0, int n, bool final) {
+  auto slot = [&](uint32_t i) {
+    const uint32_t wg = wg0 + i * stride;
+    return p.partials + (int64_t)(2 * wg + (wg == begin ? 1 : 0)) * kPartial<DP>;
+  };
+  constexpr int kRounds = 16 * DP / 4 / (kWaves * 64);
+  const int d4 = p.c.head_dim / 4;
+  f32x4 o[kRounds];
+  float m[kRounds], l[kRounds];
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    const int idx = k * kWaves * 64 + threadIdx.x;
+    const int row = idx / d4, e = (idx - row * d4) * 4;
+    m[k] = -INFINITY;
+    l[k] = 0.0f;
+    o[k] = f32x4{0, 0, 0, 0};
+    if (row >= n) continue;
+    for (uint32_t i = 0; i < count; ++i) m[k] = fmaxf(m[k], slot(i)[16 * DP + row]);
+    for (uint32_t i = 0; i < count; ++i) {
+      const float* s = slot(i);
+      const float mi = s[16 * DP + row];
+      if (mi == -INFINITY) continue;
+      const float f = __builtin_amdgcn_exp2f(mi - m[k]);
+      l[k] += f * s[16 * DP + 16 + row];
+      o[k] += *reinterpret_cast<const f32x4*>(s + row * DP + e) * f;
+    }
+    if (final) finish<DT>(p, b, head0 + row, e, o[k], m[k], l[k]);
+  }
+  if (final) return;
+  __syncthreads();  // every piece has been read: the first one's place is free
+#pragma unroll
+  for (int k = 0; k < kRounds; ++k) {
+    const int idx = k * kWaves * 64 + threadIdx.x;
+    const int row = idx / d4, e = (idx - row * d4) * 4;
+    if (row >= n) continue;
+    float* s = slot(0);
+    *reinterpret_cast<f32x4*>(s + row * DP + e) = o[k];
+    if (e == 0) {
+      s[16 * DP + row] = m[k];
+      s[16 * DP + 16 + row] = l[k];
+    }
+  }
+}
+
+// Counts this workgroup's partial result in; true in the workgroup that comes last of `size`, which
+// then sees the others' and leaves the counter cleared for the next run.
+__device__ inline bool arrive(uint32_t* counter, uint32_t size, uint32_t* last) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's stores are in the L2
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const uint32_t before =
+        __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    if (before + 1 == size)
+      __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *last = before + 1 == size ? 1u : 0u;
+  }
+  __syncthreads();
+  const bool mine = *last != 0;
+  if (mine) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  __syncthreads();  // *last may be written again
+  return mine;
+}
+
+// The waves' results of tokens of one head, put together: the output if that was all of the head,
+// else a partial result and its part in the joining.
+template <int DT, int ST, int DP>
+__device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w, Shared<DP>& sh,
+                               int64_t b, int head0, int n, bool whole, uint32_t begin,
+                               uint32_t pieces) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
+  const float l = across_sum(w.l);
+  if (g == 0) {
+    sh.m[wave][col] = w.m;
+    sh.l[wave][col] = l;
+  }
+  __syncthreads();
+  float m = sh.m[0][col];
+#pragma unroll
+  for (int i = 1; i < kWaves; ++i) m = fmaxf(m, sh.m[i][col]);
+  const float f = w.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(w.m - m);
+  if (col < n) {
+#pragma unroll
+    for (int c = 0; c < Raw<ST, DP>::kChunks; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int e = 128 * c + 8 * (4 * g + i);
+        if (e < DP) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            sh.acc[wave][col][e + k] = w.m == -INFINITY ? 0.0f : w.acc[8 * c + k][i] * f;
+        }
+      }
+  }
+  __syncthreads();
+  float* slot = p.partials + (int64_t)(2 * blockIdx.x + (blockIdx.x == begin ? 1 : 0)) * kPartial<DP>;
+  const int d4 = p.c.head_dim / 4;
+  for (int idx = threadIdx.x; idx < n * d4; idx += kWaves * 64) {
+    const int row = idx / d4, e = (idx - row * d4) * 4;
+    float rm = sh.m[0][row], rl = 0.0f;
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) rm = fmaxf(rm, sh.m[i][row]);
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) {
+      if (sh.m[i][row] != -INFINITY) rl += sh.l[i][row] * __builtin_amdgcn_exp2f(sh.m[i][row] - rm);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] += sh.acc[i][row][e + k];
+    }
+    if (whole) {
+      finish<DT>(p, b, head0 + row, e, o, rm, rl);
+    } else {
+      *reinterpret_cast<f32x4*>(slot + row * DP + e) = o;
+      if (e == 0) {
+        slot[16 * DP + row] = rm;
+        slot[16 * DP + 16 + row] = rl;
+      }
+    }
+  }
+  if (!whole) {
+    const uint32_t wgs = gridDim.x;
+    uint32_t* of_heads = p.counters;  // [workgroup where the head begins]
+    if (pieces <= kJoin) {
+      if (arrive(of_heads + begin, pieces, &sh.last))
+        join<DT, DP>(p, begin, 1, pieces, begin, b, head0, n, true);
+    } else {
+      // groups of 16 pieces first. A workgroup begins at most one head's group 0 and is at most one
+      // head's later group's first: two counters a workgroup
+      const uint32_t group = (blockIdx.x - begin) / kJoin, first = begin + group * kJoin;
+      const uint32_t size = min((uint32_t)kJoin, pieces - group * kJoin);
+      uint32_t* of_group = p.counters + (group == 0 ? wgs : 2 * wgs) + first;
+      if (arrive(of_group, size, &sh.last)) {
+        if (size > 1) join<DT, DP>(p, first, 1, size, begin, b, head0, n, false);
+        const uint32_t groups = (pieces + kJoin - 1) / kJoin;
+        if (arrive(of_heads + begin, groups, &sh.last))
+          join<DT, DP>(p, begin, kJoin, groups, begin, b, head0, n, true);
+      }
+    }
+  }
+  __syncthreads();  // sh is free again
+}
+
+template <int DT, int ST, int DP>
+__global__ __launch_bounds__(kWaves * 64, 2) void attn_kernel(AttnParams p) {
+  typedef Wave<DT, ST, DP> W;
+  typedef typename W::R R;
+  __shared__ Shared<DP> sh;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+
+  // this workgroup's run of tiles, [cur, end) of all
+  uint32_t sum = 0;
+  for (int b = lane; b < p.batch; b += 64) sum += tiles_of(p, b);
+  const uint32_t heads = (uint32_t)(p.c.kv_heads * p.q_groups);
+  const uint32_t total = __builtin_amdgcn_readfirstlane(wave_sum(sum)) * heads;
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
+    if (tiles_of(p, b) == 0) {
+      const int hd = p.c.head_dim;
+      for (int i = threadIdx.x; i < p.q_heads * (hd / 4); i += kWaves * 64) {
+        const int h = i / (hd / 4);
+        finish<DT>(p, b, h, (i - h * (hd / 4)) * 4, f32x4{0, 0, 0, 0}, 0.0f, 0.0f);
+      }
+    }
+  const uint32_t quota = max(1u, (total + gridDim.x - 1) / gridDim.x);
+  uint32_t cur = blockIdx.x * quota;
+  if (cur >= total) return;
+  const uint32_t end = min(cur + quota, total);
+
+  // the sequence and head where it begins
+  int b = 0;
+  uint32_t before = 0;  // tiles of one head of the sequences in front
+  for (int c = 0; c < p.batch; c += 64) {
+    const uint32_t t = c + lane < p.batch ? tiles_of(p, c + lane) : 0;
+    const uint32_t scan = wave_scan(t);
+    const uint64_t hit = __ballot((before + scan) * heads > cur);
+    if (hit) {
+      const int at = __builtin_ctzll(hit);
+      b = c + at;
+      before += (uint32_t)__builtin_amdgcn_readlane((int)(scan - t), at);
+      break;
+    }
+    before += (uint32_t)__builtin_amdgcn_readlane((int)scan, 63);
+  }
+  uint32_t tiles = __builtin_amdgcn_readfirstlane(tiles_of(p, b));
+  uint32_t head = (cur - before * heads) / tiles;
+  uint32_t start = before * heads + head * tiles;  // first tile of the head
+
+  while (cur < end) {
+    const uint32_t stop = min(end, start + tiles);
+    const Place seq = tokens_of(p, b);
+    const int64_t t0 = seq.first + (int64_t)(cur - start) * kAttnTile;
+    const int64_t t1 = min(seq.end, seq.first + (int64_t)(stop - start) * kAttnTile);
+    const int kv = (int)head / p.q_groups, part = (int)head - kv * p.q_groups;
+    const int head0 = kv * p.group + 16 * part, n = min(16, p.group - 16 * part);
+    const int64_t hoff = kv * p.c.head, shoff = kv * p.c.s_head;
+    const int32_t* table = p.table + (int64_t)b * p.table_row;
+
+    W w;
+    w.start(p, b, head0, n);
+    int64_t(*at)[2] = sh.at[wave];
+    // the page of token `base + lane` (lanes 0 .. 31), -1 if there is none
+    auto page_of = [&](int64_t base) {
+      int32_t page = -1;
+      if (lane < kWaveTokens && base + lane < t1)
+        page = table[(uint32_t)(base + lane) / p.c.page_size];
+      return page;
+    };
+    auto place = [&](int64_t base, int32_t page) {
+      if (lane < kWaveTokens) {
+        const bool there = (uint32_t)page < (uint32_t)p.num_pages;
+        const uint32_t t = (uint32_t)(base + lane);
+        const int64_t row = t - (t / p.c.page_size) * p.c.page_size.d;
+        at[lane][0] = there ? page * p.c.page + row * p.c.row : -1;
+        at[lane][1] = there ? page * p.c.s_page + row * p.c.s_row : -1;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    };
+    int64_t base = t0 + wave * kWaveTokens;
+    if (base < t1) {
+      int32_t page = page_of(base);
+      for (; base < t1; base += kAttnTile) {
+        R r;
+        place(base, page);
+        page = page_of(base + kAttnTile);
+        W::load(r, p, at, hoff, shoff);
+        w.step(r, p);
+      }
+    }
+    const bool whole = cur == start && stop == start + tiles;
+    const uint32_t begin = start / quota;
+    combine(p, w, sh, b, head0, n, whole, begin, (start + tiles - 1) / quota - begin + 1);
+
+    cur = stop;
+    if (cur < end) {  // the next head, and after the last the next sequence with a tile
+      start += tiles;
+      if (++head == heads) {
+        head = 0;
+        do {
+          tiles = __builtin_amdgcn_readfirstlane(tiles_of(p, ++b));
+        } while (tiles == 0);
+      }
+    }
+  }
+}
+
+template <int DT, int ST>
+void by_width(const AttnParams& p, int grid, hipStream_t s) {
+  const int dp = attn_padded(p.c.head_dim);
+  if (dp == 64)
+    attn_kernel<DT, ST, 64><<<grid, kWaves * 64, 0, s>>>(p);
+  else if (dp == 128)
+    attn_kernel<DT, ST, 128><<<grid, kWaves * 64, 0, s>>>(p);
+  else
+    attn_kernel<DT, ST, 256><<<grid, kWaves * 64, 0, s>>>(p);
+}
+
+template <int DT>
+void by_storage(const AttnParams& p, int storage, int grid, hipStream_t s) {
+  if (storage == AG_KV_16BIT)
+    by_width<DT, AG_KV_16BIT>(p, grid, s);
+  else if (storage == AG_KV_MXFP8)
+    by_width<DT, AG_KV_MXFP8>(p, grid, s);
+  else
+    by_width<DT, AG_KV_MXFP4>(p, grid, s);
+}
+
+}  // namespace
+
+hipError_t launch_attn(const AttnParams& p, int dtype, int storage, int grid, hipStream_t s) {
+  if (dtype == AGMM_F16)
+    by_storage<AGMM_F16>(p, storage, grid, s);
+  else
+    by_storage<AGMM_BF16>(p, storage, grid, s);
+  return hipGetLastError();
+}
+
+}  // namespace agmm

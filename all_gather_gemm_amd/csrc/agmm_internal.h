@@ -131,4 +131,7 @@ constexpr size_t kScratchBytes = (size_t)80 << 20;
 // address is looked up once per device (hipGetSymbolAddress) and then kept.
 hipError_t scratch_region(int device, void** ptr);
 
+// Sets what ag_matmul_last_hip_error returns in this thread (agmm_api.cpp).
+void set_last_hip_error(int e);
+
 }  // namespace agmm

@@ -1,0 +1,384 @@
+// gfx950 kernels of the rotary positions and of the paged key-value cache (agmm_attn.h).
+//
+// All of them move each byte once and compute little, so they are bound by memory bandwidth for
+// many tokens and by one launch for few. Work is cut into units of 16 bytes a lane, consecutive
+// lanes on consecutive units of a head, then heads, then tokens, so a wave's loads are runs of a
+// whole head or more.
+#include "agmm_attn_device.h"
+
+namespace agmm {
+namespace {
+
+// cos and sin of a position's angle for one pair, times the magnitude. The angle in turns is
+// position * theta / 2 pi; with theta / 2 pi held as a fraction of 2^64 the product modulo 2^64 is
+// its fractional part, exact but for the fraction's own rounding (2^-65 turns a position), however
+// long the context. The top 32 bits as a signed number are turns in [-1/2, 1/2), which is what
+// v_sin_f32 and v_cos_f32 take. No table of cosines is read: one would cost 8 bytes a pair
+// of cache or memory traffic beside the 8 bytes of the pair itself.
+__device__ inline void turn(uint64_t f, int64_t pos, float mag, float& c, float& s) {
+  const uint64_t phase = f * (uint64_t)pos;
+  const float t = (float)(int32_t)(phase >> 32) * 0x1p-32f;
+  c = mag * __builtin_amdgcn_cosf(t);
+  s = mag * __builtin_amdgcn_sinf(t);
+}
+
+__device__ inline void rotate(float a, float b, float c, float s, float& ya, float& yb) {
+  ya = fmaf(a, c, -(b * s));
+  yb = fmaf(b, c, a * s);
+}
+
+template <int DT>
+__device__ inline float value(const uint16_t* p) {
+  return T16<DT>::lo(*p);
+}
+template <int DT>
+__device__ inline void put(uint16_t* p, float x) {
+  *p = (uint16_t)T16<DT>::pack(x, 0.0f);
+}
+
+// One unit of one token's head in the rotated part, for up to HPT heads: 8 pairs (half) or 4
+// (interleaved); the last unit of a rotated part that is no multiple of that takes its n pairs one
+// by one. A pair is read and written by one thread only, so y may be x.
+template <int DT, bool HALF, bool GRAD, int HPT>
+__device__ inline void rotate_unit(const RopeParams& p, uint32_t u, int64_t pos,
+                                   const uint16_t* x, uint16_t* y, uint32_t h0) {
+  constexpr int NP = HALF ? 8 : 4;
+  const int r2 = p.plan.rot_dim / 2;
+  const int i0 = (int)u * NP;
+  const int n = min(NP, r2 - i0);
+  const int e1 = p.plan.rot_start + (HALF ? i0 : 2 * i0);
+  float c[NP], s[NP];
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    turn(p.plan.turns[i0 + k], pos, p.plan.magnitude, c[k], s[k]);  // (the table is padded)
+    if (GRAD) s[k] = -s[k];
+  }
+  const uint32_t step = p.groups.d;
+  if (n == NP) {
+    u32x4 a[HPT], b[HPT];
+#pragma unroll
+    for (int j = 0; j < HPT; ++j) {
+      if (h0 + j * step >= (uint32_t)p.heads) break;
+      const uint16_t* q = x + (int64_t)(h0 + j * step) * p.x_head + e1;
+      a[j] = load16(q);
+      if (HALF) b[j] = load16(q + r2);
+    }
+#pragma unroll
+    for (int j = 0; j < HPT; ++j) {
+      if (h0 + j * step >= (uint32_t)p.heads) break;
+      uint16_t* q = y + (int64_t)(h0 + j * step) * p.y_head + e1;
+      u32x4 ya, yb;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (HALF) {
+          float y0, y1, z0, z1;
+          rotate(T16<DT>::lo(a[j][k]), T16<DT>::lo(b[j][k]), c[2 * k], s[2 * k], y0, z0);
+          rotate(T16<DT>::hi(a[j][k]), T16<DT>::hi(b[j][k]), c[(2 * k + 1) % NP],
+                 s[(2 * k + 1) % NP], y1, z1);
+          ya[k] = T16<DT>::pack(y0, y1);
+          yb[k] = T16<DT>::pack(z0, z1);
+        } else {
+          float y0, y1;
+          rotate(T16<DT>::lo(a[j][k]), T16<DT>::hi(a[j][k]), c[k], s[k], y0, y1);
+          ya[k] = T16<DT>::pack(y0, y1);
+        }
+      }
+      store16(q, ya);
+      if (HALF) store16(q + r2, yb);
+    }
+  } else {
+    for (uint32_t h = h0; h < (uint32_t)p.heads; h += step) {
+      const uint16_t* q = x + (int64_t)h * p.x_head + e1;
+      uint16_t* w = y + (int64_t)h * p.y_head + e1;
+#pragma unroll
+      for (int k = 0; k < NP; ++k)
+        if (k < n) {
+          const int ia = HALF ? k : 2 * k, ib = HALF ? k + r2 : 2 * k + 1;
+          float ya, yb;
+          rotate(value<DT>(q + ia), value<DT>(q + ib), c[k], s[k], ya, yb);
+          put<DT>(w + ia, ya);
+          put<DT>(w + ib, yb);
+        }
+    }
+  }
+}
+
+// One unit of the elements that pass through: 8 of them, or the n < 8 at the end of their run.
+__device__ inline void pass_unit(const RopeParams& p, uint32_t u, const uint16_t* x, uint16_t* y,
+                                 uint32_t h0) {
+  int e, n;
+  if (u < (uint32_t)p.pass_units0) {
+    e = (int)u * 8;
+    n = min(8, p.plan.rot_start - e);
+  } else {
+    e = p.plan.rot_start + p.plan.rot_dim + (int)(u - p.pass_units0) * 8;
+    n = min(8, p.plan.head_dim - e);
+  }
+  for (uint32_t h = h0; h < (uint32_t)p.heads; h += p.groups.d) {
+    const uint16_t* q = x + (int64_t)h * p.x_head + e;
+    uint16_t* w = y + (int64_t)h * p.y_head + e;
+    if (n == 8) {
+      store16(w, load16(q));
+    } else {
+      for (int k = 0; k < n; ++k) w[k] = q[k];
+    }
+  }
+}
+
+template <int DT, bool HALF, bool GRAD, int HPT>
+__device__ inline void rope_thread(const RopeParams& p, uint32_t idx, int64_t b) {
+  if (idx >= p.total) return;
+  const uint32_t r = idx / p.units, u = idx - r * p.units.d;
+  const uint32_t t = r / p.groups, h0 = r - t * p.groups.d;
+  const uint16_t* x = p.x + b * p.x_batch + (int64_t)t * p.x_token;
+  uint16_t* y = p.y + b * p.y_batch + (int64_t)t * p.y_token;
+  if (u < (uint32_t)p.rot_units) {
+    rotate_unit<DT, HALF, GRAD, HPT>(p, u, p.positions[b * p.pos_batch + t], x, y, h0);
+  } else if (!p.in_place) {
+    pass_unit(p, u - p.rot_units, x, y, h0);
+  }
+}
+
+template <int DT, bool HALF, bool GRAD, int HPT>
+__global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
+  rope_thread<DT, HALF, GRAD, HPT>(p, blockIdx.x * kThreads + threadIdx.x, blockIdx.y);
+}
+
+// ---- the cache ----
+
+template <int DT, int ST>
+struct Mx {
+  static constexpr bool kFp8 = ST == AG_KV_MXFP8;
+  // The largest code M = 1.75 * 2^8 or 1.5 * 2^2, and the largest whose value the 16-bit type holds
+  // at the scales (exponents kEdge and above) where M's would not: 240 or 3.
+  static constexpr int kExp = kFp8 ? 8 : 2;
+  static constexpr uint32_t kMant = kFp8 ? 0x600000u : 0x400000u;
+  static constexpr float kM = kFp8 ? 448.0f : 6.0f;
+  static constexpr float kMEdge = kFp8 ? 240.0f : 3.0f;
+  static constexpr int kEdge = (DT == AGMM_F16 ? 16 : 128) - (kFp8 ? 8 : 2);
+};
+
+// Maximum over the 4 lanes of a quad.
+__device__ inline uint32_t quad_max(uint32_t a) {
+  a = max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0xB1, 0xf, 0xf, true));  // lanes ^ 1
+  return max(a, (uint32_t)__builtin_amdgcn_mov_dpp((int)a, 0x4E, 0xf, 0xf, true));  // lanes ^ 2
+}
+
+// Writes the 8 elements x of chunk `ch` of a row. 4 neighbouring lanes hold a block of 32.
+template <int DT, int ST>
+__device__ inline void write_chunk(char* row, char* srow, uint32_t ch, u32x4 x) {
+  if (ST == AG_KV_16BIT) {
+    *reinterpret_cast<u32x4*>(row + 16 * ch) = x;
+    return;
+  }
+  typedef Mx<DT, ST> M;
+  float v[8];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = T16<DT>::lo(x[k]);
+    v[2 * k + 1] = T16<DT>::hi(x[k]);
+  }
+  // magnitudes compare as their bits do, NaN above infinity above the rest
+#pragma unroll
+  for (int k = 0; k < 8; ++k) amax = max(amax, __builtin_bit_cast(uint32_t, v[k]) & 0x7fffffffu);
+  amax = quad_max(amax);
+  const bool odd = amax >= 0x7f800000u;
+  int e = (int)(amax >> 23) - 127 - M::kExp + ((amax & 0x7fffffu) > M::kMant ? 1 : 0);
+  e = odd ? 0 : max(e, -126);
+  const float inv = odd ? 0.0f : __builtin_bit_cast(float, (uint32_t)(127 - e) << 23);
+  const float top = e >= M::kEdge ? M::kMEdge : M::kM;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    v[k] = odd ? 0.0f : __builtin_amdgcn_fmed3f(v[k] * inv, -top, top);  // the product is exact
+  }
+  if (M::kFp8) {
+    u32x2 w;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      int b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * k], v[4 * k + 1], 0, false);
+      w[k] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[4 * k + 2], v[4 * k + 3], b, true);
+    }
+    *reinterpret_cast<u32x2*>(row + 8 * ch) = w;
+  } else {
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], 1.0f, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], 1.0f, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], 1.0f, 2);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], 1.0f, 3);
+    *reinterpret_cast<uint32_t*>(row + 4 * ch) = w;
+  }
+  if (ch % 4 == 0) srow[ch / 4] = (char)(odd ? 255 : e + 127);
+}
+
+// Chunk `ch` of a row, as 8 packed 16-bit values.
+template <int DT, int ST>
+__device__ inline u32x4 read_chunk(const char* row, const char* srow, uint32_t ch) {
+  if (ST == AG_KV_16BIT) return *reinterpret_cast<const u32x4*>(row + 16 * ch);
+  const float s = scale_of(*reinterpret_cast<const uint8_t*>(srow + ch / 4));
+  if (ST == AG_KV_MXFP8) {
+    const u32x2 w = *reinterpret_cast<const u32x2*>(row + 8 * ch);
+    return from_fp8x8<DT>(w[0], w[1], s);
+  }
+  return from_fp4x8<DT>(*reinterpret_cast<const uint32_t*>(row + 4 * ch), s);
+}
+
+// The 8 elements from e0 of a head, rotated as rotate_unit() would: each element's partner of its
+// pair is read beside it (from the caches, its own chunk's thread reads it too), so that a thread
+// ends with 8 consecutive elements and a quad of lanes with a block.
+template <int DT, bool HALF>
+__device__ inline u32x4 rotated_chunk(const RopePlan& r, int64_t pos, const uint16_t* head, int e0) {
+  const u32x4 own = load16(head + e0);
+  const int r2 = r.rot_dim / 2, r0 = r.rot_start;
+  if (e0 + 8 <= r0 || e0 >= r0 + r.rot_dim) return own;
+  u32x4 y;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = e0 + k - r0;  // in the rotated part
+    const uint32_t bits = (own[k / 2] >> (16 * (k % 2))) & 0xffffu;
+    uint32_t w = bits;
+    if (i >= 0 && i < r.rot_dim) {
+      const bool second = HALF ? i >= r2 : (i & 1) != 0;
+      const int pair = HALF ? (second ? i - r2 : i) : i / 2;
+      const float z = value<DT>(head + e0 + k + (HALF ? (second ? -r2 : r2) : (second ? -1 : 1)));
+      float c, s, ya, yb;
+      turn(r.turns[pair], pos, r.magnitude, c, s);
+      const float x = T16<DT>::lo(bits);
+      rotate(second ? z : x, second ? x : z, c, s, ya, yb);
+      w = T16<DT>::pack(second ? yb : ya, 0.0f) & 0xffffu;
+    }
+    y[k / 2] = (k % 2) ? (y[k / 2] | (w << 16)) : w;
+  }
+  return y;
+}
+
+template <int DT, int ST, bool ROPE, bool HALF>
+__device__ inline void append_thread(const CacheParams& p, uint32_t idx) {
+  if (idx >= p.total) return;
+  const uint32_t r = idx / p.chunks, ch = idx - r * p.chunks.d;
+  const uint32_t t = r / p.heads, h = r - t * p.heads.d;
+  const int64_t slot = p.slots[t];
+  if (slot < 0 || slot >= (int64_t)p.c.rows) return;  // the same for a block's 4 lanes
+  const uint32_t page = (uint32_t)slot / p.c.page_size;
+  const uint32_t row = (uint32_t)slot - page * p.c.page_size.d;
+  const uint16_t* kh = p.k + (int64_t)t * p.k_token + (int64_t)h * p.k_head;
+  const uint16_t* vh = p.v + (int64_t)t * p.v_token + (int64_t)h * p.v_head;
+  const u32x4 v = load16(vh + 8 * ch);
+  const u32x4 k = ROPE ? rotated_chunk<DT, HALF>(p.plan, p.positions[t], kh, 8 * (int)ch)
+                       : load16(kh + 8 * ch);
+  const int64_t at = (int64_t)page * p.c.page + (int64_t)h * p.c.head + (int64_t)row * p.c.row;
+  const int64_t sat =
+      (int64_t)page * p.c.s_page + (int64_t)h * p.c.s_head + (int64_t)row * p.c.s_row;
+  write_chunk<DT, ST>(p.c.k + at, p.c.ks + sat, ch, k);
+  write_chunk<DT, ST>(p.c.v + at, p.c.vs + sat, ch, v);
+}
+
+template <int DT, int ST>
+__global__ __launch_bounds__(kThreads) void append_kernel(CacheParams p) {
+  append_thread<DT, ST, false, false>(p, blockIdx.x * kThreads + threadIdx.x);
+}
+
+template <int DT, int ST, bool HALF>
+__global__ __launch_bounds__(kThreads) void append_rope_kernel(CacheParams p, RopeParams q) {
+  if (blockIdx.x < p.q_blocks)
+    rope_thread<DT, HALF, false, 1>(q, blockIdx.x * kThreads + threadIdx.x, 0);
+  else
+    append_thread<DT, ST, true, HALF>(p, (blockIdx.x - p.q_blocks) * kThreads + threadIdx.x);
+}
+
+template <int DT, int ST>
+__global__ __launch_bounds__(kThreads) void read_kernel(CacheParams p) {
+  const uint32_t idx = blockIdx.x * kThreads + threadIdx.x;
+  if (idx >= p.total) return;
+  const uint32_t r = idx / p.chunks, ch = idx - r * p.chunks.d;
+  const uint32_t t = r / p.heads, h = r - t * p.heads.d;
+  const int64_t slot = p.slots[t];
+  u32x4 k = {0, 0, 0, 0}, v = {0, 0, 0, 0};
+  if (slot >= 0 && slot < (int64_t)p.c.rows) {
+    const uint32_t page = (uint32_t)slot / p.c.page_size;
+    const uint32_t row = (uint32_t)slot - page * p.c.page_size.d;
+    const int64_t at = (int64_t)page * p.c.page + (int64_t)h * p.c.head + (int64_t)row * p.c.row;
+    const int64_t sat =
+        (int64_t)page * p.c.s_page + (int64_t)h * p.c.s_head + (int64_t)row * p.c.s_row;
+    k = read_chunk<DT, ST>(p.c.k + at, p.c.ks + sat, ch);
+    v = read_chunk<DT, ST>(p.c.v + at, p.c.vs + sat, ch);
+  }
+  store16(p.k_out + (int64_t)t * p.k_token + (int64_t)h * p.k_head + 8 * ch, k);
+  store16(p.v_out + (int64_t)t * p.v_token + (int64_t)h * p.v_head + 8 * ch, v);
+}
+
+template <int DT, bool HALF, bool GRAD>
+void rope_by_heads(const RopeParams& p, int per_thread, dim3 grid, hipStream_t s) {
+  if (per_thread == 1)
+    rope_kernel<DT, HALF, GRAD, 1><<<grid, kThreads, 0, s>>>(p);
+  else
+    rope_kernel<DT, HALF, GRAD, 4><<<grid, kThreads, 0, s>>>(p);
+}
+
+inline uint32_t blocks(uint32_t threads) { return (threads + kThreads - 1) / kThreads; }
+
+}  // namespace
+
+hipError_t launch_rope(const RopeParams& p, int dtype, int pairing, int gradient, int per_thread,
+                       int64_t batch, hipStream_t s) {
+  const dim3 grid(blocks(p.total), (uint32_t)batch);
+  auto by = [&](auto dt) {
+    constexpr int DT = decltype(dt)::value;
+    if (pairing == AG_ROPE_HALF)
+      gradient ? rope_by_heads<DT, true, true>(p, per_thread, grid, s)
+               : rope_by_heads<DT, true, false>(p, per_thread, grid, s);
+    else
+      gradient ? rope_by_heads<DT, false, true>(p, per_thread, grid, s)
+               : rope_by_heads<DT, false, false>(p, per_thread, grid, s);
+  };
+  if (dtype == AGMM_F16)
+    by(std::integral_constant<int, AGMM_F16>());
+  else
+    by(std::integral_constant<int, AGMM_BF16>());
+  return hipGetLastError();
+}
+
+namespace {
+
+template <class F>
+void by_type(int dtype, int storage, F f) {
+  auto st = [&](auto dt) {
+    if (storage == AG_KV_16BIT)
+      f(dt, std::integral_constant<int, AG_KV_16BIT>());
+    else if (storage == AG_KV_MXFP8)
+      f(dt, std::integral_constant<int, AG_KV_MXFP8>());
+    else
+      f(dt, std::integral_constant<int, AG_KV_MXFP4>());
+  };
+  if (dtype == AGMM_F16)
+    st(std::integral_constant<int, AGMM_F16>());
+  else
+    st(std::integral_constant<int, AGMM_BF16>());
+}
+
+}  // namespace
+
+hipError_t launch_append(const CacheParams& p, const RopeParams* rope, int dtype, int storage,
+                         int pairing, hipStream_t s) {
+  const uint32_t grid = p.q_blocks + blocks(p.total);
+  by_type(dtype, storage, [&](auto dt, auto st) {
+    constexpr int DT = decltype(dt)::value, ST = decltype(st)::value;
+    if (!rope)
+      append_kernel<DT, ST><<<grid, kThreads, 0, s>>>(p);
+    else if (pairing == AG_ROPE_HALF)
+      append_rope_kernel<DT, ST, true><<<grid, kThreads, 0, s>>>(p, *rope);
+    else
+      append_rope_kernel<DT, ST, false><<<grid, kThreads, 0, s>>>(p, *rope);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_read(const CacheParams& p, int dtype, int storage, hipStream_t s) {
+  by_type(dtype, storage, [&](auto dt, auto st) {
+    read_kernel<decltype(dt)::value, decltype(st)::value>
+        <<<blocks(p.total), kThreads, 0, s>>>(p);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace agmm
