@@ -33,10 +33,42 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kWaveTokens = 32;
 static_assert(kWaves * kWaveTokens == kAttnTile, "a workgroup's tile is one step of its waves");
-constexpr int kJoin = 16;            // pieces joined at once
+constexpr int kJoin = 16;            // pieces joined at once, and then up to
+constexpr int kPiecesMax = kAttnMaxWgs / kJoin;  // groups of them
 constexpr float kHead = 7.0f;        // weights are 2^(s - m + kHead)
 constexpr float kUnhead = 0x1p-7f;   // 2^-kHead
 constexpr float kRaise = 8.0f;       // raise the maximum when a tile's is above it by this
+
+// Partial results pass between workgroups that may sit on different XCDs, whose L2s are not coherent.
+// They are stored and loaded as relaxed atomics of agent scope, which write through and read past
+// the L2: once a store is acknowledged (vmcnt 0) every later agent-scope load sees it, so no
+// workgroup has to write its L2 back or invalidate it, which costs far more than the few kilobytes.
+__device__ inline void store_shared(float* p, f32x4 x) {
+  uint64_t* w = reinterpret_cast<uint64_t*>(p);
+  const u32x4 b = __builtin_bit_cast(u32x4, x);
+  __hip_atomic_store(w, (uint64_t)b[1] << 32 | b[0], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(w + 1, (uint64_t)b[3] << 32 | b[2], __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline void store_shared(float* p, float x) {
+  __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ inline f32x4 load_shared4(const float* p) {
+  const uint64_t* w = reinterpret_cast<const uint64_t*>(p);
+  const uint64_t a = __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const uint64_t b = __hip_atomic_load(w + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return __builtin_bit_cast(f32x4, u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b,
+                                         (uint32_t)(b >> 32)});
+}
+__device__ inline float load_shared(const float* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// The factor that brings a sum with maximum m to the maximum `top` >= m. A sum without a finite score
+// keeps its own: it is 0, or NaN.
+__device__ inline float weight(float m, float top) {
+  return m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+}
 
 // Sum or maximum over the 4 lane groups of 16 (lanes l, l ^ 16, l ^ 32, l ^ 48).
 __device__ inline float across_max(float x) {
@@ -63,10 +95,9 @@ struct Raw {
   static constexpr int kVWords = ST == AG_KV_16BIT ? 4 : ST == AG_KV_MXFP8 ? 2 : 1;
 
   uint32_t k[2][kLoads][kWords];
-  uint32_t ks[2][kScales ? kScales : 1];
   uint32_t v[8][kChunks][kVWords];
-  uint32_t vs[8][kScales ? kChunks : 1];
-  uint32_t valid;  // bit j: token j of this lane's 8 is attended to
+  uint32_t ks[kScales ? kScales : 1], vs[kScales ? kScales : 1];  // of token lane % 32
+  uint32_t there;  // bit t: token t is attended to; the same in every lane
 
   // First element of a lane's operand in matrix instruction `step`, lane group g.
   __device__ static inline int first(int step, int g) {
@@ -114,64 +145,63 @@ struct Wave {
     l = 0.0f;
   }
 
-  // Issues the loads of 32 tokens whose places (data and scale offsets, -1: not attended to) are
-  // in `at`; nothing is read for the others, and their values count as zeros.
+  // Issues the loads of 32 tokens whose places (data and scale offsets) are in `at`. Tokens that are
+  // not attended to have the place of one that is, and lanes past the head's end read its first
+  // elements: what comes back there is thrown away in step(), and the loads need no branches.
   __device__ static inline void load(R& r, const AttnParams& p, const int64_t (*at)[2],
-                                     int64_t head, int64_t s_head) {
+                                     int64_t head, int64_t s_head, uint32_t there) {
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int hd = p.c.head_dim;
+    const char* kb = p.c.k + head;
+    const char* vb = p.c.v + head;
+    r.there = there;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int64_t off = at[16 * t + col][0], soff = at[16 * t + col][1];
+      const char* row = kb + at[16 * t + col][0];
 #pragma unroll
       for (int i = 0; i < R::kLoads; ++i) {
-#pragma unroll
-        for (int w = 0; w < R::kWords; ++w) r.k[t][i][w] = 0;
-        const int e = R::first(i * R::kPer, g);
-        if (off >= 0 && e < hd) {
-          const int64_t byte = ST == AG_KV_16BIT ? 2 * e : ST == AG_KV_MXFP8 ? e : e / 2;
-          load_words<R::kWords>(r.k[t][i], p.c.k + off + head + byte);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < R::kScales; ++i) {
-        r.ks[t][i] = 0;
-        // (the bytes behind the row's last block hold anything: 255 would make its zeros NaN)
-        if (off >= 0 && 128 * i < hd)
-          r.ks[t][i] = *reinterpret_cast<const uint32_t*>(p.c.ks + soff + s_head + 4 * i) &
-                       (hd - 128 * i >= 128 ? ~0u : (1u << (hd - 128 * i) / 4) - 1u);
+        int e = R::first(i * R::kPer, g);
+        e = e < hd ? e : 0;
+        load_words<R::kWords>(r.k[t][i], row + bytes_of(e));
       }
     }
-    r.valid = 0;
+    if (R::kScales) {
+      const int64_t soff = at[lane & 31][1] + s_head;
+#pragma unroll
+      for (int i = 0; i < R::kScales; ++i) {
+        const int word = 128 * i < hd ? 4 * i : 0;
+        r.ks[i] = *reinterpret_cast<const uint32_t*>(p.c.ks + soff + word);
+        r.vs[i] = *reinterpret_cast<const uint32_t*>(p.c.vs + soff + word);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int t = (j < 4 ? 0 : 16) + 4 * g + (j & 3);
-      const int64_t off = at[t][0], soff = at[t][1];
-      r.valid |= (off >= 0 ? 1u : 0u) << j;
+      const char* row = vb + at[(j < 4 ? 0 : 16) + 4 * g + (j & 3)][0];
 #pragma unroll
       for (int c = 0; c < R::kChunks; ++c) {
-        const int e = 128 * c + 8 * col;
-#pragma unroll
-        for (int w = 0; w < R::kVWords; ++w) r.v[j][c][w] = 0;
-        if (R::kScales) r.vs[j][c] = 0;
-        if (off >= 0 && e < hd) {
-          const int64_t byte = ST == AG_KV_16BIT ? 2 * e : ST == AG_KV_MXFP8 ? e : e / 2;
-          load_words<R::kVWords>(r.v[j][c], p.c.v + off + head + byte);
-          if (R::kScales)
-            r.vs[j][c] = *reinterpret_cast<const uint8_t*>(p.c.vs + soff + s_head + e / 32);
-        }
+        int e = 128 * c + 8 * col;
+        e = e < hd ? e : 0;
+        load_words<R::kVWords>(r.v[j][c], row + bytes_of(e));
       }
     }
   }
 
-  // The K operand of matrix instruction `step` for token tile t.
-  __device__ static inline u32x4 key(const R& r, int t, int step, int g) {
+  // The scale of chunk `col` of a row (block col / 4 of these 128 elements).
+  __device__ static inline float block_scale(uint32_t word, int col) {
+    return scale_of((word >> (8 * (col >> 2))) & 255u);
+  }
+  __device__ static inline int bytes_of(int e) {
+    return ST == AG_KV_16BIT ? 2 * e : ST == AG_KV_MXFP8 ? e : e / 2;
+  }
+
+  // The K operand of matrix instruction `step` for token tile t, whose scale words are w.
+  __device__ static inline u32x4 key(const R& r, int t, int step, int g, const uint32_t* w) {
     const int i = step / R::kPer, part = step % R::kPer;
     if constexpr (ST == AG_KV_16BIT) {
       return u32x4{r.k[t][i][0], r.k[t][i][1], r.k[t][i][2], r.k[t][i][3]};
     } else {
       const int block = R::first(step, 0) / 32 + (g * R::kPer * 8) / 32;
-      const uint32_t word = R::kScales == 2 && block >= 4 ? r.ks[t][R::kScales - 1] : r.ks[t][0];
+      const uint32_t word = R::kScales == 2 && block >= 4 ? w[R::kScales - 1] : w[0];
       const float s = scale_of((word >> (8 * (block & 3))) & 255u);
       if constexpr (ST == AG_KV_MXFP8)
         return from_fp8x8<DT>(r.k[t][i][2 * part], r.k[t][i][2 * part + 1], s);
@@ -180,14 +210,70 @@ struct Wave {
     }
   }
 
-  __device__ inline void step(const R& r, const AttnParams& p) {
-    const int lane = threadIdx.x & 63, g = lane >> 4;
+  // sc: the wave's place in LDS for scale words, [32 tokens][kScales], keys' and values'.
+  __device__ inline void step(R& r, const AttnParams& p, uint32_t (*sc)[32 * 2]) {
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    const int hd = p.c.head_dim;
+    uint32_t kw[2][R::kScales ? R::kScales : 1], vw[8][R::kScales ? R::kChunks : 1];
+    if (R::kScales) {
+      if (lane < 32) {
+#pragma unroll
+        for (int i = 0; i < R::kScales; ++i) {
+          sc[0][lane * R::kScales + i] = r.ks[i];
+          sc[1][lane * R::kScales + i] = r.vs[i];
+        }
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < R::kScales; ++i) kw[t][i] = sc[0][(16 * t + col) * R::kScales + i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int c = 0; c < R::kChunks; ++c)
+          vw[j][c] = sc[1][((j < 4 ? 0 : 16) + 4 * g + (j & 3)) * R::kScales + c];
+      __builtin_amdgcn_wave_barrier();
+    }
+    const uint32_t mine = ((r.there >> (4 * g)) & 15u) | (((r.there >> (16 + 4 * g)) & 15u) << 4);
+    if (r.there != ~0u) {  // the values of tokens that are not attended to count as zeros
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (!((mine >> j) & 1u)) {
+#pragma unroll
+          for (int c = 0; c < R::kChunks; ++c) {
+#pragma unroll
+            for (int w = 0; w < R::kVWords; ++w) r.v[j][c][w] = 0;
+            if (R::kScales) vw[j][c] = 0;
+          }
+        }
+    }
+    if (hd != DP) {  // and the keys' elements past the head's end
+#pragma unroll
+      for (int i = 0; i < R::kLoads; ++i)
+        if (R::first(i * R::kPer, g) >= hd) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int w = 0; w < R::kWords; ++w) r.k[t][i][w] = 0;
+        }
+      // (the scale bytes behind the row's last block hold anything: 255 would make those zeros NaN)
+#pragma unroll
+      for (int i = 0; i < R::kScales; ++i) {
+        const int left = hd - 128 * i;
+        const uint32_t mask = left >= 128 ? ~0u : left <= 0 ? 0u : (1u << left / 4) - 1u;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) kw[t][i] &= mask;
+      }
+    }
     f32x4 st[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       st[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < R::kSteps; ++i) st[t] = T16<DT>::mfma(key(r, t, i, g), q[i], st[t]);
+      for (int i = 0; i < R::kSteps; ++i)
+        st[t] = T16<DT>::mfma(key(r, t, i, g, kw[t]), q[i], st[t]);
     }
     // scores in base 2; the capped ones by tanh x = 1 - 2 / (e^2x + 1)
     float s[8], top = -INFINITY;
@@ -200,7 +286,7 @@ struct Wave {
       } else {
         x *= p.scale;
       }
-      s[j] = (r.valid >> j) & 1u ? x : -INFINITY;
+      s[j] = (mine >> j) & 1u ? x : -INFINITY;
       top = fmaxf(top, s[j]);
     }
     top = across_max(top);
@@ -239,9 +325,9 @@ struct Wave {
         if constexpr (ST == AG_KV_16BIT)
           v[j] = u32x4{r.v[j][c][0], r.v[j][c][1], r.v[j][c][2], r.v[j][c][3]};
         else if constexpr (ST == AG_KV_MXFP8)
-          v[j] = from_fp8x8<DT>(r.v[j][c][0], r.v[j][c][1], scale_of(r.vs[j][c]));
+          v[j] = from_fp8x8<DT>(r.v[j][c][0], r.v[j][c][1], block_scale(vw[j][c], col));
         else
-          v[j] = from_fp4x8<DT>(r.v[j][c][0], scale_of(r.vs[j][c]));
+          v[j] = from_fp4x8<DT>(r.v[j][c][0], block_scale(vw[j][c], col));
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -260,6 +346,10 @@ struct Wave {
 // A partial result: 16 rows of DP sums, the rows' maxima (base 2, less kHead), the rows' sums.
 template <int DP>
 constexpr int kPartial = 16 * DP + 32;
+
+// Two tiles' registers fit beside the accumulators
+template <int ST, int DP>
+constexpr bool kTwo = DP <= 128;
 
 struct Place {  // what the workgroup works on: tokens [first, end) of sequence b
   int64_t first, end;
@@ -294,8 +384,14 @@ __device__ inline uint32_t wave_scan(uint32_t x) {
 template <int DP>
 struct Shared {
   int64_t at[kWaves][kWaveTokens][2];
+  uint32_t scales[kWaves][2][kWaveTokens * 2];
   float m[kWaves][16], l[kWaves][16];
-  float acc[kWaves][16][DP + 4];
+  union {
+    float acc[kWaves][16][DP + 4];
+    struct {
+      float join_m[kPiecesMax][16], join_l[kPiecesMax][16];
+    };
+  };
   uint32_t last;
 };
 
@@ -322,33 +418,46 @@ __device__ inline void finish(const AttnParams& p, int64_t b, int head, int e, f
 // output; else a partial result again, in the place of the first.
 template <int DT, int DP>
 __device__ void join(const AttnParams& p, uint32_t wg0, uint32_t stride, uint32_t count,
-                     uint32_t begin, int64_t b, int head0, int n, bool final) {
+                     uint32_t begin, int64_t b, int head0, int n, bool final, Shared<DP>& sh) {
   auto slot = [&](uint32_t i) {
     const uint32_t wg = wg0 + i * stride;
     return p.partials + (int64_t)(2 * wg + (wg == begin ? 1 : 0)) * kPartial<DP>;
   };
   constexpr int kRounds = 16 * DP / 4 / (kWaves * 64);
   const int d4 = p.c.head_dim / 4;
+  // the pieces' weights: thread (piece, row)
+  for (uint32_t i = threadIdx.x >> 4; i < count; i += kWaves * 4) {
+    const int row = threadIdx.x & 15;
+    if (row < n) {
+      sh.join_m[i][row] = load_shared(slot(i) + 16 * DP + row);
+      sh.join_l[i][row] = load_shared(slot(i) + 16 * DP + 16 + row);
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 16 && (int)threadIdx.x < n) {
+    const int row = threadIdx.x;
+    float top = -INFINITY, sum = 0.0f;
+    for (uint32_t i = 0; i < count; ++i) top = fmaxf(top, sh.join_m[i][row]);
+    for (uint32_t i = 0; i < count; ++i) {
+      const float f = weight(sh.join_m[i][row], top);
+      sh.join_m[i][row] = f;
+      sum += f * sh.join_l[i][row];
+    }
+    sh.m[0][row] = top;
+    sh.l[0][row] = sum;
+  }
+  __syncthreads();
   f32x4 o[kRounds];
-  float m[kRounds], l[kRounds];
 #pragma unroll
   for (int k = 0; k < kRounds; ++k) {
     const int idx = k * kWaves * 64 + threadIdx.x;
     const int row = idx / d4, e = (idx - row * d4) * 4;
-    m[k] = -INFINITY;
-    l[k] = 0.0f;
     o[k] = f32x4{0, 0, 0, 0};
     if (row >= n) continue;
-    for (uint32_t i = 0; i < count; ++i) m[k] = fmaxf(m[k], slot(i)[16 * DP + row]);
-    for (uint32_t i = 0; i < count; ++i) {
-      const float* s = slot(i);
-      const float mi = s[16 * DP + row];
-      if (mi == -INFINITY) continue;
-      const float f = __builtin_amdgcn_exp2f(mi - m[k]);
-      l[k] += f * s[16 * DP + 16 + row];
-      o[k] += *reinterpret_cast<const f32x4*>(s + row * DP + e) * f;
-    }
-    if (final) finish<DT>(p, b, head0 + row, e, o[k], m[k], l[k]);
+#pragma unroll 8
+    for (uint32_t i = 0; i < count; ++i)
+      o[k] += load_shared4(slot(i) + row * DP + e) * sh.join_m[i][row];
+    if (final) finish<DT>(p, b, head0 + row, e, o[k], sh.m[0][row], sh.l[0][row]);
   }
   if (final) return;
   __syncthreads();  // every piece has been read: the first one's place is free
@@ -358,10 +467,10 @@ __device__ void join(const AttnParams& p, uint32_t wg0, uint32_t stride, uint32_
     const int row = idx / d4, e = (idx - row * d4) * 4;
     if (row >= n) continue;
     float* s = slot(0);
-    *reinterpret_cast<f32x4*>(s + row * DP + e) = o[k];
+    store_shared(s + row * DP + e, o[k]);
     if (e == 0) {
-      s[16 * DP + row] = m[k];
-      s[16 * DP + 16 + row] = l[k];
+      store_shared(s + 16 * DP + row, sh.m[0][row]);
+      store_shared(s + 16 * DP + 16 + row, sh.l[0][row]);
     }
   }
 }
@@ -369,18 +478,17 @@ __device__ void join(const AttnParams& p, uint32_t wg0, uint32_t stride, uint32_
 // Counts this workgroup's partial result in; true in the workgroup that comes last of `size`, which
 // then sees the others' and leaves the counter cleared for the next run.
 __device__ inline bool arrive(uint32_t* counter, uint32_t size, uint32_t* last) {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's stores are in the L2
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's stores are acknowledged
   __syncthreads();
   if (threadIdx.x == 0) {
     const uint32_t before =
-        __hip_atomic_fetch_add(counter, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     if (before + 1 == size)
       __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     *last = before + 1 == size ? 1u : 0u;
   }
   __syncthreads();
   const bool mine = *last != 0;
-  if (mine) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   __syncthreads();  // *last may be written again
   return mine;
 }
@@ -401,7 +509,7 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w, S
   float m = sh.m[0][col];
 #pragma unroll
   for (int i = 1; i < kWaves; ++i) m = fmaxf(m, sh.m[i][col]);
-  const float f = w.m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(w.m - m);
+  const float f = weight(w.m, m);
   if (col < n) {
 #pragma unroll
     for (int c = 0; c < Raw<ST, DP>::kChunks; ++c)
@@ -411,7 +519,7 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w, S
         if (e < DP) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            sh.acc[wave][col][e + k] = w.m == -INFINITY ? 0.0f : w.acc[8 * c + k][i] * f;
+            sh.acc[wave][col][e + k] = w.acc[8 * c + k][i] * f;
         }
       }
   }
@@ -426,17 +534,17 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w, S
     f32x4 o = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) {
-      if (sh.m[i][row] != -INFINITY) rl += sh.l[i][row] * __builtin_amdgcn_exp2f(sh.m[i][row] - rm);
+      rl += sh.l[i][row] * weight(sh.m[i][row], rm);
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[k] += sh.acc[i][row][e + k];
     }
     if (whole) {
       finish<DT>(p, b, head0 + row, e, o, rm, rl);
     } else {
-      *reinterpret_cast<f32x4*>(slot + row * DP + e) = o;
+      store_shared(slot + row * DP + e, o);
       if (e == 0) {
-        slot[16 * DP + row] = rm;
-        slot[16 * DP + 16 + row] = rl;
+        store_shared(slot + 16 * DP + row, rm);
+        store_shared(slot + 16 * DP + 16 + row, rl);
       }
     }
   }
@@ -445,7 +553,7 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w, S
     uint32_t* of_heads = p.counters;  // [workgroup where the head begins]
     if (pieces <= kJoin) {
       if (arrive(of_heads + begin, pieces, &sh.last))
-        join<DT, DP>(p, begin, 1, pieces, begin, b, head0, n, true);
+        join<DT, DP>(p, begin, 1, pieces, begin, b, head0, n, true, sh);
     } else {
       // groups of 16 pieces first. A workgroup begins at most one head's group 0 and is at most one
       // head's later group's first: two counters a workgroup
@@ -453,10 +561,10 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w, S
       const uint32_t size = min((uint32_t)kJoin, pieces - group * kJoin);
       uint32_t* of_group = p.counters + (group == 0 ? wgs : 2 * wgs) + first;
       if (arrive(of_group, size, &sh.last)) {
-        if (size > 1) join<DT, DP>(p, first, 1, size, begin, b, head0, n, false);
+        if (size > 1) join<DT, DP>(p, first, 1, size, begin, b, head0, n, false, sh);
         const uint32_t groups = (pieces + kJoin - 1) / kJoin;
         if (arrive(of_heads + begin, groups, &sh.last))
-          join<DT, DP>(p, begin, kJoin, groups, begin, b, head0, n, true);
+          join<DT, DP>(p, begin, kJoin, groups, begin, b, head0, n, true, sh);
       }
     }
   }
@@ -528,26 +636,58 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_kernel(AttnParams p) {
         page = table[(uint32_t)(base + lane) / p.c.page_size];
       return page;
     };
+    // Puts the tokens' places into LDS; bit t of the result: token base + t is attended to. A token
+    // that is not gets the first one's place that is.
     auto place = [&](int64_t base, int32_t page) {
-      if (lane < kWaveTokens) {
-        const bool there = (uint32_t)page < (uint32_t)p.num_pages;
+      const bool ok = (uint32_t)page < (uint32_t)p.num_pages;
+      const uint32_t there = (uint32_t)__ballot(ok);
+      if (there) {
         const uint32_t t = (uint32_t)(base + lane);
-        const int64_t row = t - (t / p.c.page_size) * p.c.page_size.d;
-        at[lane][0] = there ? page * p.c.page + row * p.c.row : -1;
-        at[lane][1] = there ? page * p.c.s_page + row * p.c.s_row : -1;
+        const int row = (int)(t - (t / p.c.page_size) * p.c.page_size.d);
+        const int some = __builtin_ctz(there);
+        const int32_t pg = ok ? page : __builtin_amdgcn_readlane(page, some);
+        const int32_t rw = ok ? row : __builtin_amdgcn_readlane(row, some);
+        if (lane < kWaveTokens) {
+          at[lane][0] = pg * p.c.page + rw * p.c.row;
+          at[lane][1] = pg * p.c.s_page + rw * p.c.s_row;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
       }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      return there;
     };
     int64_t base = t0 + wave * kWaveTokens;
     if (base < t1) {
       int32_t page = page_of(base);
-      for (; base < t1; base += kAttnTile) {
-        R r;
-        place(base, page);
-        page = page_of(base + kAttnTile);
-        W::load(r, p, at, hoff, shoff);
-        w.step(r, p);
+      if constexpr (kTwo<ST, DP>) {
+        // two tiles in registers: one is loaded while the other is worked on
+        R r0, r1;
+        auto fetch = [&](R& r, int64_t base) {
+          r.there = place(base, page);
+          page = page_of(base + kAttnTile);
+          if (r.there) W::load(r, p, at, hoff, shoff, r.there);
+        };
+        fetch(r0, base);
+        while (true) {
+          fetch(r1, base + kAttnTile);
+          if (r0.there) w.step(r0, p, sh.scales[wave]);
+          base += kAttnTile;
+          if (base >= t1) break;
+          fetch(r0, base + kAttnTile);
+          if (r1.there) w.step(r1, p, sh.scales[wave]);
+          base += kAttnTile;
+          if (base >= t1) break;
+        }
+      } else {
+        for (; base < t1; base += kAttnTile) {
+          R r;
+          const uint32_t there = place(base, page);
+          page = page_of(base + kAttnTile);
+          if (there) {
+            W::load(r, p, at, hoff, shoff, there);
+            w.step(r, p, sh.scales[wave]);
+          }
+        }
       }
     }
     const bool whole = cur == start && stop == start + tiles;

@@ -206,7 +206,7 @@ int check_attn(const ag_attn_desc* d) {
   if (d->dtype != AGMM_F16 && d->dtype != AGMM_BF16) return AGMM_ERR_INVALID_ARG;
   if (d->storage < AG_KV_16BIT || d->storage > AG_KV_MXFP4) return AGMM_ERR_INVALID_ARG;
   if (d->head_dim < 1 || d->q_heads < 1 || d->kv_heads < 1 || d->q_heads % d->kv_heads ||
-      d->window < 0 || d->num_wgs < 0 || d->num_wgs > 4096)
+      d->window < 0 || d->num_wgs < 0 || d->num_wgs > agmm::kAttnMaxWgs)
     return AGMM_ERR_INVALID_ARG;
   if (!(d->scale >= 0.0f) || !isfinite(d->scale) || !(d->soft_cap >= 0.0f) ||
       !isfinite(d->soft_cap))

@@ -95,7 +95,8 @@ hipError_t launch_append(const CacheParams& p, const RopeParams* rope, int dtype
 hipError_t launch_read(const CacheParams& p, int dtype, int storage, hipStream_t s);
 // padded head_dim of the attention kernels: 64, 128 or 256
 inline int attn_padded(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
-constexpr int kAttnTile = 128;  // tokens a workgroup takes at a time
+constexpr int kAttnTile = 128;    // tokens a workgroup takes at a time
+constexpr int kAttnMaxWgs = 1024;  // workgroups of a run
 hipError_t launch_attn(const AttnParams& p, int dtype, int storage, int grid, hipStream_t s);
 
 }  // namespace agmm

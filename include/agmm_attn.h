@@ -158,7 +158,7 @@ typedef struct ag_attn_desc {
   int32_t dtype, storage;
   int32_t head_dim;          /* as in ag_kv_cache */
   int32_t q_heads, kv_heads; /* q_heads a multiple of kv_heads */
-  int32_t num_wgs;           /* workgroups, at most 4096; 0 = auto (fills the chip once) */
+  int32_t num_wgs;           /* workgroups, at most 1024; 0 = auto (fills the chip once) */
   int64_t window;            /* tokens attended to, the new one among them; 0 = all */
   float scale;               /* > 0; 0 = 1 / sqrt(head_dim) */
   float soft_cap;            /* > 0; 0 = none */

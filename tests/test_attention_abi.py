@@ -154,7 +154,7 @@ def _attn(T, **kw):
 
 @pytest.mark.parametrize("rc,bad", [
     (INVALID, dict(dtype=-1)), (INVALID, dict(storage=3)), (INVALID, dict(q_heads=3, kv_heads=2)),
-    (INVALID, dict(kv_heads=0)), (INVALID, dict(window=-1)), (INVALID, dict(num_wgs=4097)),
+    (INVALID, dict(kv_heads=0)), (INVALID, dict(window=-1)), (INVALID, dict(num_wgs=1025)),
     (INVALID, dict(scale=-1.0)), (INVALID, dict(scale=math.nan)), (INVALID, dict(soft_cap=-2.0)),
     (INVALID, dict(soft_cap=math.inf)), (UNSUPPORTED, dict(head_dim=320)),
     (UNSUPPORTED, dict(head_dim=36)), (UNSUPPORTED, dict(storage=1, head_dim=72)),
