@@ -33,8 +33,11 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kWaveTokens = 32;
 static_assert(kWaves * kWaveTokens == kAttnTile, "a workgroup's tile is one step of its waves");
-constexpr int kJoin = 16;            // pieces joined at once, and then up to
-constexpr int kPiecesMax = kAttnMaxWgs / kJoin;  // groups of them
+constexpr int kCus = 256;
+constexpr uint32_t kLeast = 4;       // tiles of a workgroup, at least, when all have work
+constexpr int kSingle = 64;          // pieces that one workgroup joins; more are joined
+constexpr int kJoin = 16;            // in groups of this many first
+constexpr int kChunk = 16;           // pieces whose loads are in flight together
 constexpr float kHead = 7.0f;        // weights are 2^(s - m + kHead)
 constexpr float kUnhead = 0x1p-7f;   // 2^-kHead
 constexpr float kRaise = 8.0f;       // raise the maximum when a tile's is above it by this
@@ -50,8 +53,10 @@ __device__ inline void store_shared(float* p, f32x4 x) {
   __hip_atomic_store(w + 1, (uint64_t)b[3] << 32 | b[2], __ATOMIC_RELAXED,
                      __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ inline void store_shared(float* p, float x) {
-  __hip_atomic_store(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ inline void store_shared2(float* p, float x, float y) {
+  __hip_atomic_store(reinterpret_cast<uint64_t*>(p),
+                     (uint64_t)__builtin_bit_cast(uint32_t, y) << 32 | __builtin_bit_cast(uint32_t, x),
+                     __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 __device__ inline f32x4 load_shared4(const float* p) {
   const uint64_t* w = reinterpret_cast<const uint64_t*>(p);
@@ -60,8 +65,11 @@ __device__ inline f32x4 load_shared4(const float* p) {
   return __builtin_bit_cast(f32x4, u32x4{(uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b,
                                          (uint32_t)(b >> 32)});
 }
-__device__ inline float load_shared(const float* p) {
-  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+__device__ inline void load_shared2(const float* p, float& x, float& y) {
+  const uint64_t a = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p), __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+  x = __builtin_bit_cast(float, (uint32_t)a);
+  y = __builtin_bit_cast(float, (uint32_t)(a >> 32));
 }
 
 // The factor that brings a sum with maximum m to the maximum `top` >= m. A sum without a finite score
@@ -343,26 +351,34 @@ struct Wave {
   }
 };
 
-// A partial result: 16 rows of DP sums, the rows' maxima (base 2, less kHead), the rows' sums.
 template <int DP>
-constexpr int kPartial = 16 * DP + 32;
+struct Shared {
+  int64_t at[kWaves][kWaveTokens][2];
+  uint32_t scales[kWaves][2][kWaveTokens * 2];
+  float m[kWaves][16], l[kWaves][16];
+  float acc[kWaves][16][DP + 4];
+  uint32_t last[2];
+};
 
 // Two tiles' registers fit beside the accumulators
 template <int ST, int DP>
 constexpr bool kTwo = DP <= 128;
 
-struct Place {  // what the workgroup works on: tokens [first, end) of sequence b
-  int64_t first, end;
+// A partial result: 16 rows of DP sums, then the rows' maxima (base 2) and sums in pairs.
+template <int DP>
+constexpr int kPartial = 16 * DP + 32;
+
+struct Range {  // tokens [first, end) of a sequence; tiles begin at `from`, a multiple of 16
+  int64_t from, first, end;
 };
-__device__ inline Place tokens_of(const AttnParams& p, int b) {
-  const int n = min(max(p.lens[b], 0), p.capacity);
-  const int64_t len = max(p.lens[b], 0);
-  const int64_t first = p.window > 0 ? max((int64_t)0, len - p.window) : 0;
-  return Place{min(first, (int64_t)n), n};
+__device__ inline Range range_of(const AttnParams& p, int32_t len) {
+  const int64_t n = max(len, 0), end = min(n, (int64_t)p.capacity);
+  const int64_t first = p.window > 0 ? min(max((int64_t)0, n - p.window), end) : 0;
+  return Range{first & ~(int64_t)15, first, end};
 }
-__device__ inline uint32_t tiles_of(const AttnParams& p, int b) {
-  const Place w = tokens_of(p, b);
-  return (uint32_t)((w.end - w.first + kAttnTile - 1) / kAttnTile);
+__device__ inline uint32_t tiles_of(const AttnParams& p, int32_t len) {
+  const Range r = range_of(p, len);
+  return r.first == r.end ? 0 : (uint32_t)((r.end - r.from + kAttnTile - 1) / kAttnTile);
 }
 
 __device__ inline uint32_t wave_sum(uint32_t x) {
@@ -381,124 +397,113 @@ __device__ inline uint32_t wave_scan(uint32_t x) {
   return x;
 }
 
-template <int DP>
-struct Shared {
-  int64_t at[kWaves][kWaveTokens][2];
-  uint32_t scales[kWaves][2][kWaveTokens * 2];
-  float m[kWaves][16], l[kWaves][16];
-  union {
-    float acc[kWaves][16][DP + 4];
-    struct {
-      float join_m[kPiecesMax][16], join_l[kPiecesMax][16];
-    };
-  };
-  uint32_t last;
-};
-
-__device__ inline void write_out(uint16_t* w, uint32_t a, uint32_t b) {
-  typedef u32x2 u32x2_any __attribute__((aligned(2)));
-  *reinterpret_cast<u32x2_any*>(w) = u32x2{a, b};
-}
-
 // Elements e .. e + 3 of a row: o over the row's sum l, and the row's lse with element 0.
 template <int DT>
 __device__ inline void finish(const AttnParams& p, int64_t b, int head, int e, f32x4 o, float m,
                               float l) {
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // 0: nothing was attended to
-  write_out(p.out + b * p.o_batch + (int64_t)head * p.o_head + e,
-            T16<DT>::pack(o[0] * inv, o[1] * inv), T16<DT>::pack(o[2] * inv, o[3] * inv));
+  typedef u32x2 u32x2_any __attribute__((aligned(2)));
+  *reinterpret_cast<u32x2_any*>(p.out + b * p.o_batch + (int64_t)head * p.o_head + e) =
+      u32x2{T16<DT>::pack(o[0] * inv, o[1] * inv), T16<DT>::pack(o[2] * inv, o[3] * inv)};
   if (e == 0 && p.lse)
     p.lse[b * p.q_heads + head] =
         l == 0.0f ? -INFINITY
                   : (m + __builtin_amdgcn_logf(l * kUnhead)) * 0.69314718055994531f;
 }
 
-// Joins `count` partial results for n q heads: of workgroups wg0, wg0 + stride, ..., the one of
-// workgroup `begin`, where the head's tiles begin, in slot 1 and the others in slot 0. final: the
-// output; else a partial result again, in the place of the first.
+// A head's part that a workgroup does not have all of.
+struct Piece {
+  int b, head0, n;          // sequence, first q head, q heads
+  uint32_t begin, pieces;   // workgroup that has the head's first tile; workgroups that have any
+};
+
+// Joins `count` partial results of a head: of workgroups wg0, wg0 + stride, ..., the one of the
+// workgroup where the head begins in slot 1 and the others in slot 0. final: the output; else a
+// partial result again, in the place of the first.
 template <int DT, int DP>
-__device__ void join(const AttnParams& p, uint32_t wg0, uint32_t stride, uint32_t count,
-                     uint32_t begin, int64_t b, int head0, int n, bool final, Shared<DP>& sh) {
+__device__ inline void join(const AttnParams& p, Shared<DP>& sh, const Piece& h, uint32_t wg0,
+                            uint32_t stride, uint32_t count, bool final) {
   auto slot = [&](uint32_t i) {
     const uint32_t wg = wg0 + i * stride;
-    return p.partials + (int64_t)(2 * wg + (wg == begin ? 1 : 0)) * kPartial<DP>;
+    return p.partials + (int64_t)(2 * wg + (wg == h.begin ? 1 : 0)) * kPartial<DP>;
   };
-  constexpr int kRounds = 16 * DP / 4 / (kWaves * 64);
   const int d4 = p.c.head_dim / 4;
-  // the pieces' weights: thread (piece, row)
-  for (uint32_t i = threadIdx.x >> 4; i < count; i += kWaves * 4) {
-    const int row = threadIdx.x & 15;
-    if (row < n) {
-      sh.join_m[i][row] = load_shared(slot(i) + 16 * DP + row);
-      sh.join_l[i][row] = load_shared(slot(i) + 16 * DP + 16 + row);
-    }
-  }
-  __syncthreads();
-  if (threadIdx.x < 16 && (int)threadIdx.x < n) {
-    const int row = threadIdx.x;
-    float top = -INFINITY, sum = 0.0f;
-    for (uint32_t i = 0; i < count; ++i) top = fmaxf(top, sh.join_m[i][row]);
-    for (uint32_t i = 0; i < count; ++i) {
-      const float f = weight(sh.join_m[i][row], top);
-      sh.join_m[i][row] = f;
-      sum += f * sh.join_l[i][row];
-    }
-    sh.m[0][row] = top;
-    sh.l[0][row] = sum;
-  }
-  __syncthreads();
-  f32x4 o[kRounds];
-#pragma unroll
-  for (int k = 0; k < kRounds; ++k) {
-    const int idx = k * kWaves * 64 + threadIdx.x;
+#pragma unroll 1
+  for (int idx = threadIdx.x; idx < h.n * d4; idx += kWaves * 64) {
     const int row = idx / d4, e = (idx - row * d4) * 4;
-    o[k] = f32x4{0, 0, 0, 0};
-    if (row >= n) continue;
-#pragma unroll 8
-    for (uint32_t i = 0; i < count; ++i)
-      o[k] += load_shared4(slot(i) + row * DP + e) * sh.join_m[i][row];
-    if (final) finish<DT>(p, b, head0 + row, e, o[k], sh.m[0][row], sh.l[0][row]);
+    f32x4 o = {0, 0, 0, 0};
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+    for (uint32_t c = 0; c < count; c += kChunk) {
+      f32x4 x[kChunk];
+      float mi[kChunk], li[kChunk];
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) {  // (past the last: the last again, not counted below)
+        const float* s = slot(min(c + i, count - 1));
+        load_shared2(s + 16 * DP + 2 * row, mi[i], li[i]);
+        x[i] = load_shared4(s + row * DP + e);
+      }
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) top = fmaxf(top, mi[i]);
+      const float f = weight(m, top);
+      l *= f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) o[w] *= f;
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) {
+        if (c + i < count) {
+          const float g = weight(mi[i], top);
+          l = fmaf(g, li[i], l);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) o[w] = fmaf(g, x[i][w], o[w]);
+        }
+      }
+      m = top;
+    }
+    if (final) {
+      finish<DT>(p, h.b, h.head0 + row, e, o, m, l);
+    } else {
+#pragma unroll
+      for (int w = 0; w < 4; ++w) sh.acc[0][row][e + w] = o[w];
+      if (e == 0) {
+        sh.m[0][row] = m;
+        sh.l[0][row] = l;
+      }
+    }
   }
   if (final) return;
   __syncthreads();  // every piece has been read: the first one's place is free
-#pragma unroll
-  for (int k = 0; k < kRounds; ++k) {
-    const int idx = k * kWaves * 64 + threadIdx.x;
+#pragma unroll 1
+  for (int idx = threadIdx.x; idx < h.n * d4; idx += kWaves * 64) {
     const int row = idx / d4, e = (idx - row * d4) * 4;
-    if (row >= n) continue;
-    float* s = slot(0);
-    store_shared(s + row * DP + e, o[k]);
-    if (e == 0) {
-      store_shared(s + 16 * DP + row, sh.m[0][row]);
-      store_shared(s + 16 * DP + 16 + row, sh.l[0][row]);
-    }
+    float* s = p.partials + (int64_t)(2 * wg0 + (wg0 == h.begin ? 1 : 0)) * kPartial<DP>;
+    const float* o = &sh.acc[0][row][e];
+    store_shared(s + row * DP + e, f32x4{o[0], o[1], o[2], o[3]});
+    if (e == 0) store_shared2(s + 16 * DP + 2 * row, sh.m[0][row], sh.l[0][row]);
   }
 }
 
-// Counts this workgroup's partial result in; true in the workgroup that comes last of `size`, which
-// then sees the others' and leaves the counter cleared for the next run.
-__device__ inline bool arrive(uint32_t* counter, uint32_t size, uint32_t* last) {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's stores are acknowledged
+// Counts a partial result in; true for the one that comes last of `size`, which leaves the counter
+// cleared for the next run. The partial result's stores have been acknowledged.
+__device__ inline bool count_in(uint32_t* counter, uint32_t size) {
+  const uint32_t before =
+      __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (before + 1 != size) return false;
+  __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return true;
+}
+// All of this workgroup's stores so far are acknowledged.
+__device__ inline void settle() {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
-  if (threadIdx.x == 0) {
-    const uint32_t before =
-        __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (before + 1 == size)
-      __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *last = before + 1 == size ? 1u : 0u;
-  }
-  __syncthreads();
-  const bool mine = *last != 0;
-  __syncthreads();  // *last may be written again
-  return mine;
 }
 
 // The waves' results of tokens of one head, put together: the output if that was all of the head,
-// else a partial result and its part in the joining.
+// else a partial result in the workgroup's slot.
 template <int DT, int ST, int DP>
-__device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w, Shared<DP>& sh,
-                               int64_t b, int head0, int n, bool whole, uint32_t begin,
-                               uint32_t pieces) {
+__device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
+                               Shared<DP>& sh, const Piece& h) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
   const float l = across_sum(w.l);
   if (g == 0) {
@@ -510,7 +515,7 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w, S
 #pragma unroll
   for (int i = 1; i < kWaves; ++i) m = fmaxf(m, sh.m[i][col]);
   const float f = weight(w.m, m);
-  if (col < n) {
+  if (col < h.n) {
 #pragma unroll
     for (int c = 0; c < Raw<ST, DP>::kChunks; ++c)
 #pragma unroll
@@ -518,15 +523,16 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w, S
         const int e = 128 * c + 8 * (4 * g + i);
         if (e < DP) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            sh.acc[wave][col][e + k] = w.acc[8 * c + k][i] * f;
+          for (int k = 0; k < 8; ++k) sh.acc[wave][col][e + k] = w.acc[8 * c + k][i] * f;
         }
       }
   }
   __syncthreads();
-  float* slot = p.partials + (int64_t)(2 * blockIdx.x + (blockIdx.x == begin ? 1 : 0)) * kPartial<DP>;
+  const bool whole = h.pieces == 1;
+  float* slot =
+      p.partials + (int64_t)(2 * blockIdx.x + (blockIdx.x == h.begin ? 1 : 0)) * kPartial<DP>;
   const int d4 = p.c.head_dim / 4;
-  for (int idx = threadIdx.x; idx < n * d4; idx += kWaves * 64) {
+  for (int idx = threadIdx.x; idx < h.n * d4; idx += kWaves * 64) {
     const int row = idx / d4, e = (idx - row * d4) * 4;
     float rm = sh.m[0][row], rl = 0.0f;
 #pragma unroll
@@ -539,33 +545,10 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w, S
       for (int k = 0; k < 4; ++k) o[k] += sh.acc[i][row][e + k];
     }
     if (whole) {
-      finish<DT>(p, b, head0 + row, e, o, rm, rl);
+      finish<DT>(p, h.b, h.head0 + row, e, o, rm, rl);
     } else {
       store_shared(slot + row * DP + e, o);
-      if (e == 0) {
-        store_shared(slot + 16 * DP + row, rm);
-        store_shared(slot + 16 * DP + 16 + row, rl);
-      }
-    }
-  }
-  if (!whole) {
-    const uint32_t wgs = gridDim.x;
-    uint32_t* of_heads = p.counters;  // [workgroup where the head begins]
-    if (pieces <= kJoin) {
-      if (arrive(of_heads + begin, pieces, &sh.last))
-        join<DT, DP>(p, begin, 1, pieces, begin, b, head0, n, true, sh);
-    } else {
-      // groups of 16 pieces first. A workgroup begins at most one head's group 0 and is at most one
-      // head's later group's first: two counters a workgroup
-      const uint32_t group = (blockIdx.x - begin) / kJoin, first = begin + group * kJoin;
-      const uint32_t size = min((uint32_t)kJoin, pieces - group * kJoin);
-      uint32_t* of_group = p.counters + (group == 0 ? wgs : 2 * wgs) + first;
-      if (arrive(of_group, size, &sh.last)) {
-        if (size > 1) join<DT, DP>(p, first, 1, size, begin, b, head0, n, false, sh);
-        const uint32_t groups = (pieces + kJoin - 1) / kJoin;
-        if (arrive(of_heads + begin, groups, &sh.last))
-          join<DT, DP>(p, begin, kJoin, groups, begin, b, head0, n, true, sh);
-      }
+      if (e == 0) store_shared2(slot + 16 * DP + 2 * row, rm, rl);
     }
   }
   __syncthreads();  // sh is free again
@@ -581,18 +564,20 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_kernel(AttnParams p) {
 
   // this workgroup's run of tiles, [cur, end) of all
   uint32_t sum = 0;
-  for (int b = lane; b < p.batch; b += 64) sum += tiles_of(p, b);
+  for (int b = lane; b < p.batch; b += 64) sum += tiles_of(p, p.lens[b]);
   const uint32_t heads = (uint32_t)(p.c.kv_heads * p.q_groups);
   const uint32_t total = __builtin_amdgcn_readfirstlane(wave_sum(sum)) * heads;
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
-    if (tiles_of(p, b) == 0) {
-      const int hd = p.c.head_dim;
-      for (int i = threadIdx.x; i < p.q_heads * (hd / 4); i += kWaves * 64) {
-        const int h = i / (hd / 4);
-        finish<DT>(p, b, h, (i - h * (hd / 4)) * 4, f32x4{0, 0, 0, 0}, 0.0f, 0.0f);
+    if (tiles_of(p, p.lens[b]) == 0) {
+      const int d4 = p.c.head_dim / 4;
+      for (int i = threadIdx.x; i < p.q_heads * d4; i += kWaves * 64) {
+        const int h = i / d4;
+        finish<DT>(p, b, h, (i - h * d4) * 4, f32x4{0, 0, 0, 0}, 0.0f, 0.0f);
       }
     }
-  const uint32_t quota = max(1u, (total + gridDim.x - 1) / gridDim.x);
+  // an equal share, but at least kLeast tiles once that gives every compute unit a workgroup
+  const uint32_t quota = max((total + gridDim.x - 1) / gridDim.x,
+                             min(kLeast, (total + kCus - 1) / kCus));
   uint32_t cur = blockIdx.x * quota;
   if (cur >= total) return;
   const uint32_t end = min(cur + quota, total);
@@ -601,7 +586,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_kernel(AttnParams p) {
   int b = 0;
   uint32_t before = 0;  // tiles of one head of the sequences in front
   for (int c = 0; c < p.batch; c += 64) {
-    const uint32_t t = c + lane < p.batch ? tiles_of(p, c + lane) : 0;
+    const uint32_t t = c + lane < p.batch ? tiles_of(p, p.lens[c + lane]) : 0;
     const uint32_t scan = wave_scan(t);
     const uint64_t hit = __ballot((before + scan) * heads > cur);
     if (hit) {
@@ -612,27 +597,34 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_kernel(AttnParams p) {
     }
     before += (uint32_t)__builtin_amdgcn_readlane((int)scan, 63);
   }
-  uint32_t tiles = __builtin_amdgcn_readfirstlane(tiles_of(p, b));
+  Range seq = range_of(p, p.lens[b]);
+  uint32_t tiles = (uint32_t)((seq.end - seq.from + kAttnTile - 1) / kAttnTile);
   uint32_t head = (cur - before * heads) / tiles;
   uint32_t start = before * heads + head * tiles;  // first tile of the head
 
-  while (cur < end) {
+  Piece part[2];  // what it has of heads shared with others: one that began before, one that goes on
+  part[0].pieces = part[1].pieces = 0;
+  while (true) {
     const uint32_t stop = min(end, start + tiles);
-    const Place seq = tokens_of(p, b);
-    const int64_t t0 = seq.first + (int64_t)(cur - start) * kAttnTile;
-    const int64_t t1 = min(seq.end, seq.first + (int64_t)(stop - start) * kAttnTile);
-    const int kv = (int)head / p.q_groups, part = (int)head - kv * p.q_groups;
-    const int head0 = kv * p.group + 16 * part, n = min(16, p.group - 16 * part);
+    const int64_t t0 = seq.from + (int64_t)(cur - start) * kAttnTile;
+    const int64_t t1 = min(seq.end, seq.from + (int64_t)(stop - start) * kAttnTile);
+    const int kv = (int)head / p.q_groups, group = (int)head - kv * p.q_groups;
     const int64_t hoff = kv * p.c.head, shoff = kv * p.c.s_head;
-    const int32_t* table = p.table + (int64_t)b * p.table_row;
+    Piece h;
+    h.b = b;
+    h.head0 = kv * p.group + 16 * group;
+    h.n = min(16, p.group - 16 * group);
+    h.begin = start / quota;
+    h.pieces = (start + tiles - 1) / quota - h.begin + 1;
 
     W w;
-    w.start(p, b, head0, n);
+    w.start(p, b, h.head0, h.n);
+    const int32_t* table = p.table + (int64_t)b * p.table_row;
     int64_t(*at)[2] = sh.at[wave];
     // the page of token `base + lane` (lanes 0 .. 31), -1 if there is none
     auto page_of = [&](int64_t base) {
       int32_t page = -1;
-      if (lane < kWaveTokens && base + lane < t1)
+      if (lane < kWaveTokens && base + lane >= seq.first && base + lane < t1)
         page = table[(uint32_t)(base + lane) / p.c.page_size];
       return page;
     };
@@ -645,8 +637,9 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_kernel(AttnParams p) {
         const uint32_t t = (uint32_t)(base + lane);
         const int row = (int)(t - (t / p.c.page_size) * p.c.page_size.d);
         const int some = __builtin_ctz(there);
-        const int32_t pg = ok ? page : __builtin_amdgcn_readlane(page, some);
-        const int32_t rw = ok ? row : __builtin_amdgcn_readlane(row, some);
+        const int32_t some_page = __builtin_amdgcn_readlane(page, some);
+        const int32_t some_row = __builtin_amdgcn_readlane(row, some);
+        const int32_t pg = ok ? page : some_page, rw = ok ? row : some_row;
         if (lane < kWaveTokens) {
           at[lane][0] = pg * p.c.page + rw * p.c.row;
           at[lane][1] = pg * p.c.s_page + rw * p.c.s_row;
@@ -690,20 +683,63 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_kernel(AttnParams p) {
         }
       }
     }
-    const bool whole = cur == start && stop == start + tiles;
-    const uint32_t begin = start / quota;
-    combine(p, w, sh, b, head0, n, whole, begin, (start + tiles - 1) / quota - begin + 1);
+    combine(p, w, sh, h);
+    if (h.pieces > 1) (h.begin == blockIdx.x ? part[1] : part[0]) = h;
 
     cur = stop;
-    if (cur < end) {  // the next head, and after the last the next sequence with a tile
-      start += tiles;
-      if (++head == heads) {
-        head = 0;
-        do {
-          tiles = __builtin_amdgcn_readfirstlane(tiles_of(p, ++b));
-        } while (tiles == 0);
-      }
+    if (cur >= end) break;
+    start += tiles;  // the next head, and after the last the next sequence with a tile
+    if (++head == heads) {
+      head = 0;
+      do {
+        seq = range_of(p, p.lens[++b]);
+        tiles = seq.first == seq.end
+                    ? 0
+                    : (uint32_t)((seq.end - seq.from + kAttnTile - 1) / kAttnTile);
+      } while (tiles == 0);
     }
+  }
+
+  if (part[0].pieces == 0 && part[1].pieces == 0) return;
+  settle();
+  const uint32_t wgs = gridDim.x;
+  // A workgroup begins at most one head that goes on, and at most one later group of 16 pieces: a
+  // counter for either, and one for the groups of a head.
+  auto group_of = [&](const Piece& h) { return (blockIdx.x - h.begin) / kJoin; };
+  if (threadIdx.x < 2) {
+    const Piece h = threadIdx.x ? part[1] : part[0];
+    bool last = false;
+    if (h.pieces > kSingle) {
+      const uint32_t g = group_of(h);
+      last = count_in(p.counters + (g == 0 ? wgs : 2 * wgs) + h.begin + g * kJoin,
+                      min((uint32_t)kJoin, h.pieces - g * kJoin));
+    } else if (h.pieces) {
+      last = count_in(p.counters + h.begin, h.pieces);
+    }
+    sh.last[threadIdx.x] = last;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if (!sh.last[i]) continue;
+    const Piece h = i ? part[1] : part[0];
+    const uint32_t g = group_of(h), groups = (h.pieces + kJoin - 1) / kJoin;
+    bool final = h.pieces <= kSingle;
+    uint32_t first = final ? h.begin : h.begin + g * kJoin, stride = 1;
+    uint32_t count = final ? h.pieces : min((uint32_t)kJoin, h.pieces - g * kJoin);
+    while (true) {
+      join<DT>(p, sh, h, first, stride, count, final);
+      if (final) break;
+      settle();
+      if (threadIdx.x == 0) sh.last[i] = count_in(p.counters + h.begin, groups);
+      __syncthreads();
+      if (!sh.last[i]) break;
+      final = true;
+      first = h.begin;
+      stride = kJoin;
+      count = groups;
+    }
+    __syncthreads();  // sh is free again
   }
 }
 

@@ -217,8 +217,10 @@ int check_attn(const ag_attn_desc* d) {
   return AGMM_OK;
 }
 
-// Workgroups of a run: two for each compute unit, which is what their registers allow at once.
-int workgroups(const ag_attn_desc& d, int num_cus) { return d.num_wgs ? d.num_wgs : 2 * num_cus; }
+// Workgroups of a run: as many as the compute units hold at once.
+int workgroups(const ag_attn_desc& d, int num_cus) {
+  return d.num_wgs ? d.num_wgs : 2 * num_cus;
+}
 
 int64_t partials_bytes(const ag_attn_desc& d, int wgs) {
   return align256((int64_t)2 * wgs * (16 * agmm::attn_padded(d.head_dim) + 32) * 4);
@@ -503,10 +505,10 @@ int ag_attn_run(ag_attn_handle* h, const ag_kv_cache* cache, const void* q, int6
   p.c = view_of(*cache);
   p.group = d.q_heads / d.kv_heads;
   p.q_groups = (p.group + 15) / 16;
-  p.capacity = (int32_t)(table_len * cache->page_size);
+  p.capacity = cache->num_pages > 0 ? (int32_t)(table_len * cache->page_size) : 0;
   // every tile has a 32-bit number
   const int64_t seen = d.window ? std::min(d.window, (int64_t)p.capacity) : p.capacity;
-  const int64_t tiles = (seen + agmm::kAttnTile - 1) / agmm::kAttnTile;
+  const int64_t tiles = (seen + 15 + agmm::kAttnTile - 1) / agmm::kAttnTile;
   const int64_t heads = (int64_t)d.kv_heads * p.q_groups;
   if ((double)tiles * heads * batch >= (double)most) return AGMM_ERR_UNSUPPORTED;
   rc = check_device(h->device);

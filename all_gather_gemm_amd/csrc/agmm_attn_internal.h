@@ -55,6 +55,15 @@ struct CacheView {
   int32_t head_dim, kv_heads;
 };
 
+// Bytes of a row's values or codes, and of its scales (whole words).
+inline int64_t row_bytes(const ag_kv_cache& c) {
+  return c.storage == AG_KV_16BIT ? 2 * c.head_dim
+                                  : c.storage == AG_KV_MXFP8 ? c.head_dim : c.head_dim / 2;
+}
+inline int64_t scale_bytes(const ag_kv_cache& c) {
+  return c.storage == AG_KV_16BIT ? 0 : (c.head_dim / 32 + 3) / 4 * 4;
+}
+
 struct CacheParams {
   CacheView c;
   const uint16_t *k, *v;     // append
@@ -95,7 +104,7 @@ hipError_t launch_append(const CacheParams& p, const RopeParams* rope, int dtype
 hipError_t launch_read(const CacheParams& p, int dtype, int storage, hipStream_t s);
 // padded head_dim of the attention kernels: 64, 128 or 256
 inline int attn_padded(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
-constexpr int kAttnTile = 128;    // tokens a workgroup takes at a time
+constexpr int kAttnTile = 128;     // tokens of a tile, the unit of the workgroups' shares
 constexpr int kAttnMaxWgs = 1024;  // workgroups of a run
 hipError_t launch_attn(const AttnParams& p, int dtype, int storage, int grid, hipStream_t s);
 
