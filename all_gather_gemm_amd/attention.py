@@ -96,8 +96,13 @@ def _checked(rc: int, where: str):
         raise AgmmError(rc, where)
 
 
-def _stream(stream, device):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+# The current stream's handle without a torch.cuda.Stream object made for it (2 us of a call's 7).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _stream(stream, index: int) -> int:
+    return stream.cuda_stream if stream is not None else _raw_stream(index)
 
 
 def _pick(table, key, what):
@@ -108,6 +113,9 @@ def _pick(table, key, what):
 
 def _tensor(t, name, dtype, shape, device=None):
     """A device tensor of this type and shape (None: any size) whose last dimension is dense."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda and \
+            (t.stride(-1) == 1 or t.shape[-1] == 1):
+        return t
     if t.dtype != dtype or not t.is_cuda or (device is not None and t.device != device):
         raise ValueError(f"{name} must be a {dtype} tensor on the GPU of the others")
     if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
@@ -173,30 +181,25 @@ class Rope:
         return self._run(dy, positions, out, stream, 1)
 
     def _run(self, x, positions, out, stream, gradient):
-        if x.dim() not in (3, 4):
+        shape, xs, device = x.shape, x.stride(), x.device
+        dims = len(shape)
+        if dims not in (3, 4):
             raise ValueError("x must be [tokens, heads, head_dim] or [batch, tokens, heads, head_dim]")
-        _tensor(x, "x", self.torch_dtype, (None,) * (x.dim() - 1) + (self.head_dim,))
+        _tensor(x, "x", self.torch_dtype, shape[:-1] + (self.head_dim,), device)
         if out is None:
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+            out = torch.empty_like(x)
         else:
-            _tensor(out, "out", self.torch_dtype, x.shape, x.device)
-        shape, xs, ys = x.shape, x.stride(), out.stride()
-        if len(shape) == 3:
-            batch, tokens, heads = 1, shape[0], shape[1]
-            xb = yb = 0
-            _tensor(positions, "positions", torch.int64, (tokens,), x.device)
-            pb = 0
-        else:
-            batch, tokens, heads = shape[:3]
-            xb, yb = xs[0], ys[0]
-            xs, ys = xs[1:], ys[1:]
-            batched = positions.dim() == 2
-            _tensor(positions, "positions", torch.int64, (batch, tokens) if batched else (tokens,),
-                    x.device)
-            pb = positions.stride(0) if batched else 0
-        rc = lib.ag_rope_run(self.handle, x.data_ptr(), xb, xs[0], xs[1], out.data_ptr(), yb, ys[0],
-                             ys[1], positions.data_ptr(), pb, batch, tokens, heads, gradient,
-                             _stream(stream, x.device))
+            _tensor(out, "out", self.torch_dtype, shape, device)
+        ys, batch, xb, yb, pb = out.stride(), 1, 0, 0, 0
+        if dims == 4:
+            batch, xb, yb = shape[0], xs[0], ys[0]
+        shared = positions.dim() == 1
+        _tensor(positions, "positions", torch.int64, shape[-3:-2] if shared else shape[:-2], device)
+        if not shared:
+            pb = positions.stride(0)
+        rc = lib.ag_rope_run(self.handle, x.data_ptr(), xb, xs[-3], xs[-2], out.data_ptr(), yb,
+                             ys[-3], ys[-2], positions.data_ptr(), pb, batch, shape[-3], shape[-2],
+                             gradient, _stream(stream, device.index))
         _checked(rc, "ag_rope_run")
         return out
 
@@ -261,40 +264,38 @@ class PagedCache:
                               device=device) for _ in "kv"]
         return cls(*t, dtype=dtype, storage=storage)
 
-    def _rows(self, t, name, tokens):
-        return _tensor(t, name, self.torch_dtype, (tokens, self.kv_heads, self.head_dim),
-                       self.device)
-
     def append(self, k, v, slots, stream=None):
         """Writes k and v [tokens, kv_heads, head_dim] to slots [tokens] (int64; page * page_size +
         row; a slot out of range leaves its token out)."""
         tokens = slots.shape[0]
-        self._rows(k, "k", tokens)
-        self._rows(v, "v", tokens)
-        _tensor(slots, "slots", torch.int64, (tokens,), self.device)
+        shape, td, device = (tokens, self.kv_heads, self.head_dim), self.torch_dtype, self.device
+        _tensor(k, "k", td, shape, device)
+        _tensor(v, "v", td, shape, device)
+        _tensor(slots, "slots", torch.int64, (tokens,), device)
         ks, vs = k.stride(), v.stride()
         rc = lib.ag_kv_append(self._ref, k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-                              slots.data_ptr(), tokens, _stream(stream, self.device))
+                              slots.data_ptr(), tokens, _stream(stream, device.index))
         _checked(rc, "ag_kv_append")
 
     def append_rope(self, rope: Rope, q, k, v, positions, slots, q_out=None, stream=None):
         """One launch for what comes before the attention: returns q [tokens, q_heads, head_dim]
         rotated, and writes k, rotated, and v to their slots."""
         tokens = slots.shape[0]
-        _tensor(q, "q", self.torch_dtype, (tokens, None, self.head_dim), self.device)
-        self._rows(k, "k", tokens)
-        self._rows(v, "v", tokens)
-        _tensor(slots, "slots", torch.int64, (tokens,), self.device)
-        _tensor(positions, "positions", torch.int64, (tokens,), self.device)
+        shape, td, device = (tokens, self.kv_heads, self.head_dim), self.torch_dtype, self.device
+        _tensor(q, "q", td, (tokens, q.shape[1] if q.dim() == 3 else None, self.head_dim), device)
+        _tensor(k, "k", td, shape, device)
+        _tensor(v, "v", td, shape, device)
+        _tensor(slots, "slots", torch.int64, (tokens,), device)
+        _tensor(positions, "positions", torch.int64, (tokens,), device)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            q_out = torch.empty_like(q)
         else:
-            _tensor(q_out, "q_out", self.torch_dtype, q.shape, self.device)
+            _tensor(q_out, "q_out", td, q.shape, device)
         qs, os, ks, vs = q.stride(), q_out.stride(), k.stride(), v.stride()
         rc = lib.ag_kv_append_rope(self._ref, rope.handle, q.data_ptr(), qs[0], qs[1], q.shape[1],
                                    q_out.data_ptr(), os[0], os[1], k.data_ptr(), ks[0], ks[1],
                                    v.data_ptr(), vs[0], vs[1], positions.data_ptr(),
-                                   slots.data_ptr(), tokens, _stream(stream, self.device))
+                                   slots.data_ptr(), tokens, _stream(stream, device.index))
         _checked(rc, "ag_kv_append_rope")
         return q_out
 
@@ -302,16 +303,15 @@ class PagedCache:
         """(k, v) [tokens, kv_heads, head_dim] of the rows at slots, as values of the 16-bit type;
         zeros for a slot out of range."""
         tokens = slots.shape[0]
-        shape = (tokens, self.kv_heads, self.head_dim)
-        _tensor(slots, "slots", torch.int64, (tokens,), self.device)
-        out = []
-        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-            out.append(torch.empty(shape, dtype=self.torch_dtype, device=self.device) if t is None
-                       else self._rows(t, name, tokens))
-        k, v = out
+        shape, td, device = (tokens, self.kv_heads, self.head_dim), self.torch_dtype, self.device
+        _tensor(slots, "slots", torch.int64, (tokens,), device)
+        k = slots.new_empty(shape, dtype=td) if k_out is None else \
+            _tensor(k_out, "k_out", td, shape, device)
+        v = slots.new_empty(shape, dtype=td) if v_out is None else \
+            _tensor(v_out, "v_out", td, shape, device)
         ks, vs = k.stride(), v.stride()
         rc = lib.ag_kv_read(self._ref, slots.data_ptr(), tokens, k.data_ptr(), ks[0], ks[1],
-                            v.data_ptr(), vs[0], vs[1], _stream(stream, self.device))
+                            v.data_ptr(), vs[0], vs[1], _stream(stream, device.index))
         _checked(rc, "ag_kv_read")
         return k, v
 
@@ -351,20 +351,21 @@ class DecodeAttention:
 
     def run(self, q, cache: PagedCache, page_table, lens, out=None, return_lse: bool = False,
             stream=None):
-        batch, device = q.shape[0], q.device
-        _tensor(q, "q", self.torch_dtype, (None, self.q_heads, self.head_dim), cache.device)
-        _tensor(page_table, "page_table", torch.int32, (batch, None), device)
+        batch, device = q.shape[0], cache.device
+        _tensor(q, "q", self.torch_dtype, (batch, self.q_heads, self.head_dim), device)
+        _tensor(page_table, "page_table", torch.int32,
+                (batch, page_table.shape[1] if page_table.dim() == 2 else None), device)
         _tensor(lens, "lens", torch.int32, (batch,), device)
         if out is None:
-            out = torch.empty((batch, self.q_heads, self.head_dim), dtype=q.dtype, device=device)
+            out = torch.empty_like(q)
         else:
             _tensor(out, "out", self.torch_dtype, q.shape, device)
-        lse = torch.empty((batch, self.q_heads), dtype=torch.float32, device=device) \
-            if return_lse else None
+        lse = q.new_empty((batch, self.q_heads), dtype=torch.float32) if return_lse else None
         qs, os = q.stride(), out.stride()
         rc = lib.ag_attn_run(self.handle, cache._ref, q.data_ptr(), qs[0], qs[1],
                              page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
                              lens.data_ptr(), batch, out.data_ptr(), os[0], os[1],
-                             lse.data_ptr() if return_lse else None, _stream(stream, device))
+                             lse.data_ptr() if return_lse else None,
+                             _stream(stream, device.index))
         _checked(rc, "ag_attn_run")
         return (out, lse) if return_lse else out
