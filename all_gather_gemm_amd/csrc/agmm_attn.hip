@@ -31,8 +31,6 @@ namespace agmm {
 namespace {
 
 constexpr int kWaves = 4;
-constexpr int kWaveTokens = 32;
-static_assert(kWaves * kWaveTokens == kAttnTile, "a workgroup's tile is one step of its waves");
 constexpr int kCus = 256;
 constexpr uint32_t kLeast = 4;       // tiles of a workgroup, at least, when all have work
 constexpr int kSingle = 64;          // pieces that one workgroup joins; more are joined
@@ -88,9 +86,21 @@ __device__ inline float across_sum(float x) {
   return x + __shfl_xor(x, 32);
 }
 
-// Loads of a tile of 32 tokens by one wave, as they come from memory.
+// Stops the compiler from moving what is computed from x out of a loop, into registers that the loop
+// needs for its loads.
+__device__ inline int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// What one wave loads of a tile of tokens, as it comes from memory.
 template <int ST, int DP>
 struct Raw {
+  // Sub-tiles of 16 tokens. 64 tokens share the cost of placing a tile and of its softmax, where two
+  // waves' registers hold them. kTwo: 32 tokens, but two tiles' registers.
+  static constexpr bool kTwo = ST == AG_KV_16BIT && DP == 128;
+  static constexpr int kSub = kTwo || (ST == AG_KV_MXFP8 && DP == 256) ? 2 : 4;
+  static constexpr int kTokens = 16 * kSub;
   static constexpr int kSteps = DP / 32;  // matrix instructions over the head for 16 tokens
   // K: loads a lane makes for one token, and words in each
   static constexpr int kWords = ST == AG_KV_MXFP4 && DP == 64 ? 2 : 4;
@@ -98,19 +108,24 @@ struct Raw {
                                 : ST == AG_KV_MXFP8 ? DP / 64 : (DP == 64 ? 1 : DP / 128);
   static constexpr int kPer = kSteps / kLoads;  // matrix instructions a load feeds
   static constexpr int kScales = ST == AG_KV_16BIT ? 0 : (DP == 256 ? 2 : 1);  // scale words a row
-  // V: chunks of 8 elements a lane takes of each token, and words in a chunk
+  static constexpr int kScaleRegs = kScales ? kScales : 1;
+  // V: chunks of kElems elements a lane takes of each token, and bytes of a chunk
+  static constexpr int kElems = DP == 64 ? 4 : 8;
   static constexpr int kChunks = DP == 256 ? 2 : 1;
-  static constexpr int kVWords = ST == AG_KV_16BIT ? 4 : ST == AG_KV_MXFP8 ? 2 : 1;
+  static constexpr int kBytes = ST == AG_KV_16BIT ? 2 * kElems : ST == AG_KV_MXFP8 ? kElems : kElems / 2;
+  static constexpr int kVWords = (kBytes + 3) / 4;
 
-  uint32_t k[2][kLoads][kWords];
-  uint32_t v[8][kChunks][kVWords];
-  uint32_t ks[kScales ? kScales : 1], vs[kScales ? kScales : 1];  // of token lane % 32
-  uint32_t there;  // bit t: token t is attended to; the same in every lane
+  uint32_t k[kSub][kLoads][kWords];
+  uint32_t v[kSub][4][kChunks][kVWords];    // of tokens 4 g .. 4 g + 3 of each sub-tile
+  uint32_t ks[kScaleRegs], vs[kScaleRegs];  // of token `lane`
 
   // First element of a lane's operand in matrix instruction `step`, lane group g.
   __device__ static inline int first(int step, int g) {
     const int load = step / kPer, part = step % kPer;
     return load * 32 * kPer + g * 8 * kPer + part * 8;
+  }
+  __device__ static inline int bytes_of(int e) {
+    return ST == AG_KV_16BIT ? 2 * e : ST == AG_KV_MXFP8 ? e : e / 2;
   }
 };
 
@@ -129,17 +144,29 @@ __device__ inline void load_words(uint32_t (&w)[N], const char* p) {
   }
 }
 
+template <int DP>
+constexpr int kScalesOf = 64 * (DP == 256 ? 2 : 1);
+template <int DP>
+struct Shared {
+  int64_t at[kWaves][64][2];                  // the tokens' places: data and scale offsets
+  uint32_t scales[kWaves][2][kScalesOf<DP>];  // the tokens' scale words, keys' and values'
+  float m[kWaves][16], l[kWaves][16];
+  float acc[kWaves][16][DP + 4];
+  uint32_t last[2];
+};
+
 template <int DT, int ST, int DP>
 struct Wave {
   typedef Raw<ST, DP> R;
-  static constexpr int kAcc = 8 * R::kChunks;
+  static constexpr int kAcc = R::kElems * R::kChunks;
+  static constexpr uint64_t kAll = R::kTokens == 64 ? ~0ull : (1ull << (R::kTokens & 63)) - 1;
 
   u32x4 q[R::kSteps];
   f32x4 acc[kAcc];
   float m, l;  // of this lane's q head; l of this lane's tokens alone
 
   __device__ inline void start(const AttnParams& p, int64_t b, int head0, int n) {
-    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    const int lane = here(threadIdx.x) & 63, col = lane & 15, g = lane >> 4;
     const uint16_t* row = p.q + b * p.q_batch + (int64_t)(head0 + (col < n ? col : 0)) * p.q_head;
 #pragma unroll
     for (int i = 0; i < R::kSteps; ++i) {
@@ -153,56 +180,65 @@ struct Wave {
     l = 0.0f;
   }
 
-  // Issues the loads of 32 tokens whose places (data and scale offsets) are in `at`. Tokens that are
-  // not attended to have the place of one that is, and lanes past the head's end read its first
-  // elements: what comes back there is thrown away in step(), and the loads need no branches.
-  __device__ static inline void load(R& r, const AttnParams& p, const int64_t (*at)[2],
-                                     int64_t head, int64_t s_head, uint32_t there) {
+  // The loads of the tile whose tokens' places are in `at`. A token that is not attended to has the
+  // place of the pools' first row, and lanes past the head's end read its first elements: what comes
+  // back there is thrown away below, and the loads need no branches.
+  __device__ static inline void load_k(R& r, const AttnParams& p, const int64_t (*at)[2],
+                                       int64_t head, int64_t s_head) {
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int hd = p.c.head_dim;
-    const char* kb = p.c.k + head;
-    const char* vb = p.c.v + head;
-    r.there = there;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const char* row = kb + at[16 * t + col][0];
+    for (int t = 0; t < R::kSub; ++t) {
+      const char* row = p.c.k + head + at[16 * t + col][0];
 #pragma unroll
       for (int i = 0; i < R::kLoads; ++i) {
-        int e = R::first(i * R::kPer, g);
-        e = e < hd ? e : 0;
-        load_words<R::kWords>(r.k[t][i], row + bytes_of(e));
+        const int e = R::first(i * R::kPer, g);
+        load_words<R::kWords>(r.k[t][i], row + R::bytes_of(e < hd ? e : 0));
       }
     }
-    if (R::kScales) {
-      const int64_t soff = at[lane & 31][1] + s_head;
-#pragma unroll
-      for (int i = 0; i < R::kScales; ++i) {
-        const int word = 128 * i < hd ? 4 * i : 0;
-        r.ks[i] = *reinterpret_cast<const uint32_t*>(p.c.ks + soff + word);
-        r.vs[i] = *reinterpret_cast<const uint32_t*>(p.c.vs + soff + word);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const char* row = vb + at[(j < 4 ? 0 : 16) + 4 * g + (j & 3)][0];
-#pragma unroll
-      for (int c = 0; c < R::kChunks; ++c) {
-        int e = 128 * c + 8 * col;
-        e = e < hd ? e : 0;
-        load_words<R::kVWords>(r.v[j][c], row + bytes_of(e));
-      }
-    }
+    if (R::kScales) load_scales(r.ks, p.c.ks + s_head, hd, at);
   }
 
-  // The scale of chunk `col` of a row (block col / 4 of these 128 elements).
-  __device__ static inline float block_scale(uint32_t word, int col) {
-    return scale_of((word >> (8 * (col >> 2))) & 255u);
-  }
-  __device__ static inline int bytes_of(int e) {
-    return ST == AG_KV_16BIT ? 2 * e : ST == AG_KV_MXFP8 ? e : e / 2;
+  __device__ static inline void load_v(R& r, const AttnParams& p, const int64_t (*at)[2],
+                                       int64_t head, int64_t s_head) {
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    const int hd = p.c.head_dim;
+#pragma unroll
+    for (int t = 0; t < R::kSub; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const char* row = p.c.v + head + at[16 * t + 4 * g + j][0];
+#pragma unroll
+        for (int c = 0; c < R::kChunks; ++c) {
+          const int e = 128 * c + R::kElems * col;
+          const char* from = row + R::bytes_of(e < hd ? e : 0);
+          if constexpr (R::kBytes == 2)
+            r.v[t][j][c][0] = *reinterpret_cast<const uint16_t*>(from);
+          else
+            load_words<R::kVWords>(r.v[t][j][c], from);
+        }
+      }
+    if (R::kScales) load_scales(r.vs, p.c.vs + s_head, hd, at);
   }
 
-  // The K operand of matrix instruction `step` for token tile t, whose scale words are w.
+  __device__ static inline void load_scales(uint32_t (&w)[R::kScaleRegs], const char* pool, int hd,
+                                            const int64_t (*at)[2]) {
+    const char* row = pool + at[threadIdx.x & 63][1];
+#pragma unroll
+    for (int i = 0; i < R::kScales; ++i)
+      w[i] = *reinterpret_cast<const uint32_t*>(row + (128 * i < hd ? 4 * i : 0));
+  }
+
+  // Scale words from the lane that loaded them to where the other lanes find them.
+  __device__ static inline void share(uint32_t* to, const uint32_t (&w)[R::kScaleRegs]) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int i = 0; i < R::kScales; ++i) to[lane * R::kScales + i] = w[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+
+  // The K operand of matrix instruction `step` for sub-tile t, whose scale words are w.
   __device__ static inline u32x4 key(const R& r, int t, int step, int g, const uint32_t* w) {
     const int i = step / R::kPer, part = step % R::kPer;
     if constexpr (ST == AG_KV_16BIT) {
@@ -218,51 +254,25 @@ struct Wave {
     }
   }
 
-  // sc: the wave's place in LDS for scale words, [32 tokens][kScales], keys' and values'.
-  __device__ inline void step(R& r, const AttnParams& p, uint32_t (*sc)[32 * 2]) {
+  // S^T of the tile; `sc`: the wave's place for the keys' scale words.
+  __device__ inline void scores(R& r, const AttnParams& p, uint32_t* sc, f32x4 (&st)[R::kSub]) const {
     const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
     const int hd = p.c.head_dim;
-    uint32_t kw[2][R::kScales ? R::kScales : 1], vw[8][R::kScales ? R::kChunks : 1];
+    uint32_t kw[R::kSub][R::kScaleRegs];
     if (R::kScales) {
-      if (lane < 32) {
+      share(sc, r.ks);
 #pragma unroll
-        for (int i = 0; i < R::kScales; ++i) {
-          sc[0][lane * R::kScales + i] = r.ks[i];
-          sc[1][lane * R::kScales + i] = r.vs[i];
-        }
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
+      for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < R::kScales; ++i) kw[t][i] = sc[0][(16 * t + col) * R::kScales + i];
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int c = 0; c < R::kChunks; ++c)
-          vw[j][c] = sc[1][((j < 4 ? 0 : 16) + 4 * g + (j & 3)) * R::kScales + c];
-      __builtin_amdgcn_wave_barrier();
+        for (int i = 0; i < R::kScales; ++i) kw[t][i] = sc[(16 * t + col) * R::kScales + i];
     }
-    const uint32_t mine = ((r.there >> (4 * g)) & 15u) | (((r.there >> (16 + 4 * g)) & 15u) << 4);
-    if (r.there != ~0u) {  // the values of tokens that are not attended to count as zeros
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (!((mine >> j) & 1u)) {
-#pragma unroll
-          for (int c = 0; c < R::kChunks; ++c) {
-#pragma unroll
-            for (int w = 0; w < R::kVWords; ++w) r.v[j][c][w] = 0;
-            if (R::kScales) vw[j][c] = 0;
-          }
-        }
-    }
-    if (hd != DP) {  // and the keys' elements past the head's end
+    if (hd != DP) {  // the keys' elements past the head's end are zeros
+      const int me = here(g);
 #pragma unroll
       for (int i = 0; i < R::kLoads; ++i)
-        if (R::first(i * R::kPer, g) >= hd) {
+        if (R::first(i * R::kPer, me) >= hd) {
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
             for (int w = 0; w < R::kWords; ++w) r.k[t][i][w] = 0;
         }
@@ -272,35 +282,50 @@ struct Wave {
         const int left = hd - 128 * i;
         const uint32_t mask = left >= 128 ? ~0u : left <= 0 ? 0u : (1u << left / 4) - 1u;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) kw[t][i] &= mask;
+        for (int t = 0; t < R::kSub; ++t) kw[t][i] &= mask;
       }
     }
-    f32x4 st[2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      st[t] = f32x4{0, 0, 0, 0};
+    for (int t = 0; t < R::kSub; ++t) st[t] = f32x4{0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < R::kSteps; ++i)
+    for (int i = 0; i < R::kSteps; ++i)
+#pragma unroll
+      for (int t = 0; t < R::kSub; ++t)
         st[t] = T16<DT>::mfma(key(r, t, i, g, kw[t]), q[i], st[t]);
-    }
-    // scores in base 2; the capped ones by tanh x = 1 - 2 / (e^2x + 1)
-    float s[8], top = -INFINITY;
+  }
+
+  // Scores to weights: st becomes 2^(s - m + kHead), s the scores in base 2, with m raised and what
+  // is summed rescaled first where needed.
+  __device__ inline void weights(const AttnParams& p, uint64_t there, f32x4 (&st)[R::kSub]) {
+    float scale = p.scale;
+    if (p.cap != 0.0f) {  // cap * tanh x by tanh x = 1 - 2 / (e^2x + 1)
+      scale = 1.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float x = st[j >> 2][j & 3];
-      if (p.cap != 0.0f) {
-        const float e = __builtin_amdgcn_exp2f(x * p.inv_cap);
-        x = p.cap - 2.0f * p.cap / (e + 1.0f);
-      } else {
-        x *= p.scale;
-      }
-      s[j] = (mine >> j) & 1u ? x : -INFINITY;
-      top = fmaxf(top, s[j]);
+      for (int t = 0; t < R::kSub; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          st[t][j] = p.cap - 2.0f * p.cap *
+                                 __builtin_amdgcn_rcpf(
+                                     __builtin_amdgcn_exp2f(st[t][j] * p.inv_cap) + 1.0f);
     }
-    top = across_max(top);
+    if (there != kAll) {
+      const int g = here(threadIdx.x & 63) >> 4;
+#pragma unroll
+      for (int t = 0; t < R::kSub; ++t) {
+        const uint32_t mine = (uint32_t)(there >> (16 * t)) >> (4 * g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st[t][j] = (mine >> j) & 1u ? st[t][j] : -INFINITY;
+      }
+    }
+    float top = -INFINITY;
+#pragma unroll
+    for (int t = 0; t < R::kSub; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) top = fmaxf(top, st[t][j]);
+    top = across_max(top) * scale;
     if (__any(top > m + kRaise)) {
       const float raised = fmaxf(m, top);
-      const float f = raised == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - raised);
+      const float f = weight(m, raised);
 #pragma unroll
       for (int i = 0; i < kAcc; ++i)
 #pragma unroll
@@ -308,61 +333,90 @@ struct Wave {
       l *= f;
       m = raised;
     }
-    const float ref = m == -INFINITY ? 0.0f : m - kHead;
-    u32x4 hi, lo;
+    const float ref = m == -INFINITY ? 0.0f : kHead - m;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = __builtin_amdgcn_exp2f(s[2 * j] - ref);
-      const float b = __builtin_amdgcn_exp2f(s[2 * j + 1] - ref);
-      l += a + b;
-      if (DT == AGMM_F16) {
-        hi[j] = T16<DT>::pack(a, b);  // 11 bits of a weight
-      } else {
-        // bf16 weights keep 8 bits: what cutting them there leaves goes into a second operand, 16 in
-        // all. That part is kept above 0 (by 2^-126), since 0 times an infinite value is NaN.
-        const uint32_t ab = __builtin_bit_cast(uint32_t, a), bb = __builtin_bit_cast(uint32_t, b);
-        hi[j] = __builtin_amdgcn_perm(bb, ab, 0x07060302u);
-        lo[j] = T16<DT>::pack(fmaxf(a - T16<DT>::hi(ab), 0x1p-126f), fmaxf(b - T16<DT>::hi(bb), 0x1p-126f));
+    for (int t = 0; t < R::kSub; ++t)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        st[t][j] = __builtin_amdgcn_exp2f(fmaf(st[t][j], scale, ref));
+        l += st[t][j];
       }
-    }
+  }
+
+  // O^T += V^T P^T; `sc`: the wave's place for the values' scale words.
+  __device__ inline void values(R& r, uint64_t there, uint32_t* sc, const f32x4 (&st)[R::kSub]) {
+    const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+    if (R::kScales) share(sc, r.vs);
 #pragma unroll
-    for (int c = 0; c < R::kChunks; ++c) {
-      u32x4 v[8];  // 8 tokens x 8 elements
+    for (int h = 0; h < R::kSub; h += 2) {  // 32 tokens
+      u32x4 hi, lo;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if constexpr (ST == AG_KV_16BIT)
-          v[j] = u32x4{r.v[j][c][0], r.v[j][c][1], r.v[j][c][2], r.v[j][c][3]};
-        else if constexpr (ST == AG_KV_MXFP8)
-          v[j] = from_fp8x8<DT>(r.v[j][c][0], r.v[j][c][1], block_scale(vw[j][c], col));
-        else
-          v[j] = from_fp4x8<DT>(r.v[j][c][0], block_scale(vw[j][c], col));
+      for (int j = 0; j < 4; ++j) {
+        const float a = st[h + j / 2][2 * j % 4], b = st[h + j / 2][2 * j % 4 + 1];
+        if (DT == AGMM_F16) {
+          hi[j] = T16<DT>::pack(a, b);  // 11 bits of a weight
+        } else {
+          // bf16 weights keep 8 bits: what cutting them there leaves goes into a second operand, 16
+          // in all. That part is kept above 0 (by 2^-126): 0 times an infinite value is NaN.
+          const uint32_t ab = __builtin_bit_cast(uint32_t, a), bb = __builtin_bit_cast(uint32_t, b);
+          hi[j] = __builtin_amdgcn_perm(bb, ab, 0x07060302u);
+          lo[j] = T16<DT>::pack(fmaxf(a - T16<DT>::hi(ab), 0x1p-126f),
+                                fmaxf(b - T16<DT>::hi(bb), 0x1p-126f));
+        }
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        u32x4 a;  // 8 tokens of element e
+      for (int c = 0; c < R::kChunks; ++c) {
+        uint32_t v[8][R::kElems / 2];  // 8 tokens x kElems elements
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          a[j] = __builtin_amdgcn_perm(v[2 * j + 1][e / 2], v[2 * j][e / 2],
-                                       e % 2 ? 0x07060302u : 0x05040100u);
-        acc[8 * c + e] = T16<DT>::mfma(a, hi, acc[8 * c + e]);
-        if (DT == AGMM_BF16) acc[8 * c + e] = T16<DT>::mfma(a, lo, acc[8 * c + e]);
+        for (int j = 0; j < 8; ++j) {
+          const auto& w = r.v[h + j / 4][j % 4][c];
+          if constexpr (ST == AG_KV_16BIT) {
+#pragma unroll
+            for (int i = 0; i < R::kElems / 2; ++i) v[j][i] = w[i];
+          } else {
+            // the scale of this lane's elements: block kElems * col / 32 of these 128
+            const uint32_t word = sc[(16 * (h + j / 4) + 4 * g + j % 4) * R::kScales + c];
+            const float s = scale_of((word >> (8 * (R::kElems * col >> 5))) & 255u);
+            if constexpr (ST == AG_KV_MXFP8) {
+#pragma unroll
+              for (int i = 0; i < R::kVWords; ++i) {
+                v[j][2 * i] = T16<DT>::template from_fp8<0>(w[i], s);
+                v[j][2 * i + 1] = T16<DT>::template from_fp8<1>(w[i], s);
+              }
+            } else {
+              v[j][0] = T16<DT>::template from_fp4<0>(w[0], s);
+              v[j][1] = T16<DT>::template from_fp4<1>(w[0], s);
+              if constexpr (R::kElems == 8) {
+                v[j][2] = T16<DT>::template from_fp4<2>(w[0], s);
+                v[j][3] = T16<DT>::template from_fp4<3>(w[0], s);
+              }
+            }
+          }
+        }
+        if (there != kAll) {  // the values of tokens that are not attended to count as zeros
+          const int me = here(g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (!((uint32_t)(there >> (16 * (h + j / 4))) >> (4 * me + j % 4) & 1u)) {
+#pragma unroll
+              for (int i = 0; i < R::kElems / 2; ++i) v[j][i] = 0;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < R::kElems; ++e) {
+          u32x4 a;  // 8 tokens of element e
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            a[j] = __builtin_amdgcn_perm(v[2 * j + 1][e / 2], v[2 * j][e / 2],
+                                         e % 2 ? 0x07060302u : 0x05040100u);
+          f32x4& o = acc[R::kElems * c + e];
+          o = T16<DT>::mfma(a, hi, o);
+          if (DT == AGMM_BF16) o = T16<DT>::mfma(a, lo, o);
+        }
       }
     }
   }
 };
-
-template <int DP>
-struct Shared {
-  int64_t at[kWaves][kWaveTokens][2];
-  uint32_t scales[kWaves][2][kWaveTokens * 2];
-  float m[kWaves][16], l[kWaves][16];
-  float acc[kWaves][16][DP + 4];
-  uint32_t last[2];
-};
-
-// Two tiles' registers fit beside the accumulators
-template <int ST, int DP>
-constexpr bool kTwo = DP <= 128;
 
 // A partial result: 16 rows of DP sums, then the rows' maxima (base 2) and sums in pairs.
 template <int DP>
@@ -504,7 +558,8 @@ __device__ inline void settle() {
 template <int DT, int ST, int DP>
 __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
                                Shared<DP>& sh, const Piece& h) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
+  const int tid = here(threadIdx.x);
+  const int lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
   const float l = across_sum(w.l);
   if (g == 0) {
     sh.m[wave][col] = w.m;
@@ -516,23 +571,21 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
   for (int i = 1; i < kWaves; ++i) m = fmaxf(m, sh.m[i][col]);
   const float f = weight(w.m, m);
   if (col < h.n) {
+    constexpr int kElems = Raw<ST, DP>::kElems;
 #pragma unroll
     for (int c = 0; c < Raw<ST, DP>::kChunks; ++c)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = 128 * c + 8 * (4 * g + i);
-        if (e < DP) {
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int k = 0; k < 8; ++k) sh.acc[wave][col][e + k] = w.acc[8 * c + k][i] * f;
-        }
-      }
+        for (int k = 0; k < kElems; ++k)
+          sh.acc[wave][col][128 * c + kElems * (4 * g + i) + k] = w.acc[kElems * c + k][i] * f;
   }
   __syncthreads();
   const bool whole = h.pieces == 1;
   float* slot =
       p.partials + (int64_t)(2 * blockIdx.x + (blockIdx.x == h.begin ? 1 : 0)) * kPartial<DP>;
   const int d4 = p.c.head_dim / 4;
-  for (int idx = threadIdx.x; idx < h.n * d4; idx += kWaves * 64) {
+  for (int idx = tid; idx < h.n * d4; idx += kWaves * 64) {
     const int row = idx / d4, e = (idx - row * d4) * 4;
     float rm = sh.m[0][row], rl = 0.0f;
 #pragma unroll
@@ -555,7 +608,7 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
 }
 
 template <int DT, int ST, int DP>
-__global__ __launch_bounds__(kWaves * 64, 2) void attn_kernel(AttnParams p) {
+__global__ __launch_bounds__(kWaves * 64, attn_per_cu(ST, DP)) void attn_kernel(AttnParams p) {
   typedef Wave<DT, ST, DP> W;
   typedef typename W::R R;
   __shared__ Shared<DP> sh;
@@ -621,65 +674,75 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attn_kernel(AttnParams p) {
     w.start(p, b, h.head0, h.n);
     const int32_t* table = p.table + (int64_t)b * p.table_row;
     int64_t(*at)[2] = sh.at[wave];
-    // the page of token `base + lane` (lanes 0 .. 31), -1 if there is none
+    // The page of token base + lane; past the end, the last token's.
     auto page_of = [&](int64_t base) {
-      int32_t page = -1;
-      if (lane < kWaveTokens && base + lane >= seq.first && base + lane < t1)
-        page = table[(uint32_t)(base + lane) / p.c.page_size];
-      return page;
+      const uint32_t t = (uint32_t)min(base + lane, t1 - 1);
+      return table[t / p.c.page_size];
     };
-    // Puts the tokens' places into LDS; bit t of the result: token base + t is attended to. A token
-    // that is not gets the first one's place that is.
+    // Puts the tokens' places into LDS; bit t of the result: token base + t is attended to.
     auto place = [&](int64_t base, int32_t page) {
-      const bool ok = (uint32_t)page < (uint32_t)p.num_pages;
-      const uint32_t there = (uint32_t)__ballot(ok);
-      if (there) {
-        const uint32_t t = (uint32_t)(base + lane);
-        const int row = (int)(t - (t / p.c.page_size) * p.c.page_size.d);
-        const int some = __builtin_ctz(there);
-        const int32_t some_page = __builtin_amdgcn_readlane(page, some);
-        const int32_t some_row = __builtin_amdgcn_readlane(row, some);
-        const int32_t pg = ok ? page : some_page, rw = ok ? row : some_row;
-        if (lane < kWaveTokens) {
-          at[lane][0] = pg * p.c.page + rw * p.c.row;
-          at[lane][1] = pg * p.c.s_page + rw * p.c.s_row;
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-      }
+      const int64_t tok = base + lane;
+      const bool ok = (uint32_t)page < (uint32_t)p.num_pages && tok >= seq.first && tok < t1;
+      const uint64_t there = __ballot(ok) & W::kAll;
+      const uint32_t t = (uint32_t)tok;
+      const uint32_t row = t - (t / p.c.page_size) * p.c.page_size.d;
+      at[lane][0] = ok ? page * p.c.page + row * p.c.row : 0;
+      if (R::kScales) at[lane][1] = ok ? page * p.c.s_page + row * p.c.s_row : 0;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
       return there;
     };
-    int64_t base = t0 + wave * kWaveTokens;
+    // Tiles of the wave, t0 + (wave + kWaves * i) * kTokens. (Past the last tile the loads read the
+    // pools' first row.)
+    constexpr int kStep = kWaves * R::kTokens;
+    int64_t base = t0 + wave * R::kTokens;
     if (base < t1) {
-      int32_t page = page_of(base);
-      if constexpr (kTwo<ST, DP>) {
-        // two tiles in registers: one is loaded while the other is worked on
+      uint64_t there = place(base, page_of(base));
+      int32_t page = page_of(base + kStep);
+      uint32_t(*sc)[kScalesOf<DP>] = sh.scales[wave];
+      if constexpr (R::kTwo) {
+        // a tile is loaded while the one in front of it is worked on
         R r0, r1;
-        auto fetch = [&](R& r, int64_t base) {
-          r.there = place(base, page);
-          page = page_of(base + kAttnTile);
-          if (r.there) W::load(r, p, at, hoff, shoff, r.there);
+        auto load = [&](R& r) {
+          W::load_k(r, p, at, hoff, shoff);
+          W::load_v(r, p, at, hoff, shoff);
         };
-        fetch(r0, base);
+        auto step = [&](R& now, R& after) {
+          base += kStep;
+          const uint64_t next = place(base, page);
+          page = page_of(base + kStep);
+          load(after);
+          f32x4 st[R::kSub];
+          w.scores(now, p, sc[0], st);
+          w.weights(p, there, st);
+          w.values(now, there, sc[1], st);
+          there = next;
+        };
+        load(r0);
         while (true) {
-          fetch(r1, base + kAttnTile);
-          if (r0.there) w.step(r0, p, sh.scales[wave]);
-          base += kAttnTile;
+          step(r0, r1);
           if (base >= t1) break;
-          fetch(r0, base + kAttnTile);
-          if (r1.there) w.step(r1, p, sh.scales[wave]);
-          base += kAttnTile;
+          step(r1, r0);
           if (base >= t1) break;
         }
       } else {
-        for (; base < t1; base += kAttnTile) {
-          R r;
-          const uint32_t there = place(base, page);
-          page = page_of(base + kAttnTile);
-          if (there) {
-            W::load(r, p, at, hoff, shoff, there);
-            w.step(r, p, sh.scales[wave]);
-          }
+        // The next tile's keys are loaded into their registers as soon as the scores are made, the
+        // next values once theirs are used, so that loads are under way all the time.
+        R r;
+        W::load_k(r, p, at, hoff, shoff);
+        W::load_v(r, p, at, hoff, shoff);
+        while (true) {
+          f32x4 st[R::kSub];
+          w.scores(r, p, sc[0], st);
+          base += kStep;
+          const uint64_t next = place(base, page);
+          page = page_of(base + kStep);
+          W::load_k(r, p, at, hoff, shoff);
+          w.weights(p, there, st);
+          w.values(r, there, sc[1], st);
+          if (base >= t1) break;
+          W::load_v(r, p, at, hoff, shoff);
+          there = next;
         }
       }
     }

@@ -219,7 +219,8 @@ int check_attn(const ag_attn_desc* d) {
 
 // Workgroups of a run: as many as the compute units hold at once.
 int workgroups(const ag_attn_desc& d, int num_cus) {
-  return d.num_wgs ? d.num_wgs : 2 * num_cus;
+  return d.num_wgs ? d.num_wgs
+                   : agmm::attn_per_cu(d.storage, agmm::attn_padded(d.head_dim)) * num_cus;
 }
 
 int64_t partials_bytes(const ag_attn_desc& d, int wgs) {

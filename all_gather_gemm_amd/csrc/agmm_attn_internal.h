@@ -106,6 +106,10 @@ hipError_t launch_read(const CacheParams& p, int dtype, int storage, hipStream_t
 inline int attn_padded(int head_dim) { return head_dim <= 64 ? 64 : head_dim <= 128 ? 128 : 256; }
 constexpr int kAttnTile = 128;     // tokens of a tile, the unit of the workgroups' shares
 constexpr int kAttnMaxWgs = 1024;  // workgroups of a run
+// Workgroups of the attention kernel that share a compute unit, by the registers of a tile.
+constexpr int attn_per_cu(int storage, int padded) {
+  return storage == AG_KV_16BIT && padded == 256 ? 1 : 2;
+}
 hipError_t launch_attn(const AttnParams& p, int dtype, int storage, int grid, hipStream_t s);
 
 }  // namespace agmm

@@ -166,13 +166,13 @@ def test_attention_refusals(T, rc, bad):
 
 
 def test_attention_workspace(T):
-    # two partial results of 16 padded rows, 16 maxima and 16 sums for each of 512 workgroups, and
-    # three counters
+    # two partial results of 16 padded rows, 16 maxima and 16 sums for each workgroup (two a compute
+    # unit, one for rows of 256 16-bit elements), and three counters
     al = lambda x: (x + 255) & ~255  # noqa: E731
-    for hd, padded in ((64, 64), (80, 128), (128, 128), (136, 256)):
+    for hd, padded, wgs in ((64, 64, 512), (80, 128, 512), (128, 128, 512), (136, 256, 256)):
         d = _attn(T, head_dim=hd, q_heads=8, kv_heads=2)
         assert T.lib.ag_attn_workspace_bytes(ctypes.byref(d)) == \
-            al(2 * 512 * (16 * padded + 32) * 4) + al(3 * 512 * 4)
+            al(2 * wgs * (16 * padded + 32) * 4) + al(3 * wgs * 4)
 
 
 def test_binding_refuses_cpu_tensors(T):
