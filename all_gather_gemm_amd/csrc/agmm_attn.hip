@@ -30,7 +30,6 @@
 namespace agmm {
 namespace {
 
-constexpr int kWaves = 4;
 constexpr int kCus = 256;
 constexpr uint32_t kLeast = 4;       // tiles of a workgroup, at least, when all have work
 constexpr int kSingle = 64;          // pieces that one workgroup joins; more are joined
@@ -68,6 +67,22 @@ __device__ inline void load_shared2(const float* p, float& x, float& y) {
                                        __HIP_MEMORY_SCOPE_AGENT);
   x = __builtin_bit_cast(float, (uint32_t)a);
   y = __builtin_bit_cast(float, (uint32_t)(a >> 32));
+}
+
+// What works on a run of tiles: a workgroup's 4 waves together, or (NW = 1) each wave by itself, for
+// which the barriers below are none and threads are counted in the wave.
+template <int NW>
+__device__ inline void sync() {
+  if constexpr (NW == 1) {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  } else {
+    __syncthreads();
+  }
+}
+template <int NW>
+__device__ inline int thread() {
+  return NW == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
 }
 
 // The factor that brings a sum with maximum m to the maximum `top` >= m. A sum without a finite score
@@ -146,12 +161,12 @@ __device__ inline void load_words(uint32_t (&w)[N], const char* p) {
 
 template <int DP>
 constexpr int kScalesOf = 64 * (DP == 256 ? 2 : 1);
-template <int DP>
+template <int DP, int NW>
 struct Shared {
-  int64_t at[kWaves][64][2];                  // the tokens' places: data and scale offsets
-  uint32_t scales[kWaves][2][kScalesOf<DP>];  // the tokens' scale words, keys' and values'
-  float m[kWaves][16], l[kWaves][16];
-  float acc[kWaves][16][DP + 4];
+  int64_t at[NW][64][2];                  // the tokens' places: data and scale offsets
+  uint32_t scales[NW][2][kScalesOf<DP>];  // the tokens' scale words, keys' and values'
+  float m[NW][16], l[NW][16];
+  float acc[NW][16][DP + 4];
   uint32_t last[2];
 };
 
@@ -418,9 +433,11 @@ struct Wave {
   }
 };
 
-// A partial result: 16 rows of DP sums, then the rows' maxima (base 2) and sums in pairs.
+// A partial result: p.rows rows of DP sums, then the rows' maxima (base 2) and sums in pairs.
 template <int DP>
-constexpr int kPartial = 16 * DP + 32;
+__device__ inline float* partial(const AttnParams& p, uint32_t slot) {
+  return p.partials + (int64_t)slot * (p.rows * (DP + 2));
+}
 
 struct Range {  // tokens [first, end) of a sequence; tiles begin at `from`, a multiple of 16
   int64_t from, first, end;
@@ -474,16 +491,16 @@ struct Piece {
 // Joins `count` partial results of a head: of workgroups wg0, wg0 + stride, ..., the one of the
 // workgroup where the head begins in slot 1 and the others in slot 0. final: the output; else a
 // partial result again, in the place of the first.
-template <int DT, int DP>
-__device__ inline void join(const AttnParams& p, Shared<DP>& sh, const Piece& h, uint32_t wg0,
+template <int DT, int DP, int NW>
+__device__ inline void join(const AttnParams& p, Shared<DP, NW>& sh, const Piece& h, uint32_t wg0,
                             uint32_t stride, uint32_t count, bool final) {
   auto slot = [&](uint32_t i) {
     const uint32_t wg = wg0 + i * stride;
-    return p.partials + (int64_t)(2 * wg + (wg == h.begin ? 1 : 0)) * kPartial<DP>;
+    return partial<DP>(p, 2 * wg + (wg == h.begin ? 1 : 0));
   };
-  const int d4 = p.c.head_dim / 4;
+  const int d4 = p.c.head_dim / 4, tid = here(thread<NW>());
 #pragma unroll 1
-  for (int idx = threadIdx.x; idx < h.n * d4; idx += kWaves * 64) {
+  for (int idx = tid; idx < h.n * d4; idx += NW * 64) {
     const int row = idx / d4, e = (idx - row * d4) * 4;
     f32x4 o = {0, 0, 0, 0};
     float m = -INFINITY, l = 0.0f;
@@ -494,7 +511,7 @@ __device__ inline void join(const AttnParams& p, Shared<DP>& sh, const Piece& h,
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) {  // (past the last: the last again, not counted below)
         const float* s = slot(min(c + i, count - 1));
-        load_shared2(s + 16 * DP + 2 * row, mi[i], li[i]);
+        load_shared2(s + p.rows * DP + 2 * row, mi[i], li[i]);
         x[i] = load_shared4(s + row * DP + e);
       }
       float top = m;
@@ -527,14 +544,14 @@ __device__ inline void join(const AttnParams& p, Shared<DP>& sh, const Piece& h,
     }
   }
   if (final) return;
-  __syncthreads();  // every piece has been read: the first one's place is free
+  sync<NW>();  // every piece has been read: the first one's place is free
 #pragma unroll 1
-  for (int idx = threadIdx.x; idx < h.n * d4; idx += kWaves * 64) {
+  for (int idx = tid; idx < h.n * d4; idx += NW * 64) {
     const int row = idx / d4, e = (idx - row * d4) * 4;
-    float* s = p.partials + (int64_t)(2 * wg0 + (wg0 == h.begin ? 1 : 0)) * kPartial<DP>;
+    float* s = slot(0);
     const float* o = &sh.acc[0][row][e];
     store_shared(s + row * DP + e, f32x4{o[0], o[1], o[2], o[3]});
-    if (e == 0) store_shared2(s + 16 * DP + 2 * row, sh.m[0][row], sh.l[0][row]);
+    if (e == 0) store_shared2(s + p.rows * DP + 2 * row, sh.m[0][row], sh.l[0][row]);
   }
 }
 
@@ -547,28 +564,30 @@ __device__ inline bool count_in(uint32_t* counter, uint32_t size) {
   __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   return true;
 }
-// All of this workgroup's stores so far are acknowledged.
+// All stores so far are acknowledged.
+template <int NW>
 __device__ inline void settle() {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  __syncthreads();
+  sync<NW>();
 }
 
 // The waves' results of tokens of one head, put together: the output if that was all of the head,
 // else a partial result in the workgroup's slot.
-template <int DT, int ST, int DP>
+template <int DT, int ST, int DP, int NW>
 __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
-                               Shared<DP>& sh, const Piece& h) {
-  const int tid = here(threadIdx.x);
+                               Shared<DP, NW>& sh, const Piece& h,
+                               uint32_t me) {
+  const int tid = here(thread<NW>());
   const int lane = tid & 63, wave = tid >> 6, col = lane & 15, g = lane >> 4;
   const float l = across_sum(w.l);
   if (g == 0) {
     sh.m[wave][col] = w.m;
     sh.l[wave][col] = l;
   }
-  __syncthreads();
+  sync<NW>();
   float m = sh.m[0][col];
 #pragma unroll
-  for (int i = 1; i < kWaves; ++i) m = fmaxf(m, sh.m[i][col]);
+  for (int i = 1; i < NW; ++i) m = fmaxf(m, sh.m[i][col]);
   const float f = weight(w.m, m);
   if (col < h.n) {
     constexpr int kElems = Raw<ST, DP>::kElems;
@@ -580,19 +599,18 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
         for (int k = 0; k < kElems; ++k)
           sh.acc[wave][col][128 * c + kElems * (4 * g + i) + k] = w.acc[kElems * c + k][i] * f;
   }
-  __syncthreads();
+  sync<NW>();
   const bool whole = h.pieces == 1;
-  float* slot =
-      p.partials + (int64_t)(2 * blockIdx.x + (blockIdx.x == h.begin ? 1 : 0)) * kPartial<DP>;
+  float* slot = partial<DP>(p, 2 * me + (me == h.begin ? 1 : 0));
   const int d4 = p.c.head_dim / 4;
-  for (int idx = tid; idx < h.n * d4; idx += kWaves * 64) {
+  for (int idx = tid; idx < h.n * d4; idx += NW * 64) {
     const int row = idx / d4, e = (idx - row * d4) * 4;
     float rm = sh.m[0][row], rl = 0.0f;
 #pragma unroll
-    for (int i = 1; i < kWaves; ++i) rm = fmaxf(rm, sh.m[i][row]);
+    for (int i = 1; i < NW; ++i) rm = fmaxf(rm, sh.m[i][row]);
     f32x4 o = {0, 0, 0, 0};
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
+    for (int i = 0; i < NW; ++i) {
       rl += sh.l[i][row] * weight(sh.m[i][row], rm);
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[k] += sh.acc[i][row][e + k];
@@ -601,37 +619,26 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
       finish<DT>(p, h.b, h.head0 + row, e, o, rm, rl);
     } else {
       store_shared(slot + row * DP + e, o);
-      if (e == 0) store_shared2(slot + 16 * DP + 2 * row, rm, rl);
+      if (e == 0) store_shared2(slot + p.rows * DP + 2 * row, rm, rl);
     }
   }
-  __syncthreads();  // sh is free again
+  sync<NW>();  // sh is free again
 }
 
-template <int DT, int ST, int DP>
-__global__ __launch_bounds__(kWaves * 64, attn_per_cu(ST, DP)) void attn_kernel(AttnParams p) {
+// The run of tiles of worker `me` of `wgs`, out of the `total` tiles of all sequences and heads.
+template <int DT, int ST, int DP, int NW>
+__device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me, uint32_t wgs,
+                            uint32_t total) {
   typedef Wave<DT, ST, DP> W;
   typedef typename W::R R;
-  __shared__ Shared<DP> sh;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-
-  // this workgroup's run of tiles, [cur, end) of all
-  uint32_t sum = 0;
-  for (int b = lane; b < p.batch; b += 64) sum += tiles_of(p, p.lens[b]);
+  const int tid = thread<NW>(), lane = threadIdx.x & 63;
+  const int wave = NW == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const uint32_t heads = (uint32_t)(p.c.kv_heads * p.q_groups);
-  const uint32_t total = __builtin_amdgcn_readfirstlane(wave_sum(sum)) * heads;
-  for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
-    if (tiles_of(p, p.lens[b]) == 0) {
-      const int d4 = p.c.head_dim / 4;
-      for (int i = threadIdx.x; i < p.q_heads * d4; i += kWaves * 64) {
-        const int h = i / d4;
-        finish<DT>(p, b, h, (i - h * d4) * 4, f32x4{0, 0, 0, 0}, 0.0f, 0.0f);
-      }
-    }
+  constexpr uint32_t kFill = 4 * kCus / NW;
   // an equal share, but at least kLeast tiles once that gives every compute unit a workgroup
-  const uint32_t quota = max((total + gridDim.x - 1) / gridDim.x,
-                             min(kLeast, (total + kCus - 1) / kCus));
-  uint32_t cur = blockIdx.x * quota;
+  const uint32_t quota = max((total + wgs - 1) / wgs,
+                             min(kLeast, (total + kFill - 1) / kFill));
+  uint32_t cur = me * quota;
   if (cur >= total) return;
   const uint32_t end = min(cur + quota, total);
 
@@ -692,9 +699,9 @@ __global__ __launch_bounds__(kWaves * 64, attn_per_cu(ST, DP)) void attn_kernel(
       __builtin_amdgcn_wave_barrier();
       return there;
     };
-    // Tiles of the wave, t0 + (wave + kWaves * i) * kTokens. (Past the last tile the loads read the
+    // Tiles of the wave, t0 + (wave + NW * i) * kTokens. (Past the last tile the loads read the
     // pools' first row.)
-    constexpr int kStep = kWaves * R::kTokens;
+    constexpr int kStep = NW * R::kTokens;
     int64_t base = t0 + wave * R::kTokens;
     if (base < t1) {
       uint64_t there = place(base, page_of(base));
@@ -746,8 +753,8 @@ __global__ __launch_bounds__(kWaves * 64, attn_per_cu(ST, DP)) void attn_kernel(
         }
       }
     }
-    combine(p, w, sh, h);
-    if (h.pieces > 1) (h.begin == blockIdx.x ? part[1] : part[0]) = h;
+    combine(p, w, sh, h, me);
+    if (h.pieces > 1) (h.begin == me ? part[1] : part[0]) = h;
 
     cur = stop;
     if (cur >= end) break;
@@ -764,13 +771,12 @@ __global__ __launch_bounds__(kWaves * 64, attn_per_cu(ST, DP)) void attn_kernel(
   }
 
   if (part[0].pieces == 0 && part[1].pieces == 0) return;
-  settle();
-  const uint32_t wgs = gridDim.x;
+  settle<NW>();
   // A workgroup begins at most one head that goes on, and at most one later group of 16 pieces: a
   // counter for either, and one for the groups of a head.
-  auto group_of = [&](const Piece& h) { return (blockIdx.x - h.begin) / kJoin; };
-  if (threadIdx.x < 2) {
-    const Piece h = threadIdx.x ? part[1] : part[0];
+  auto group_of = [&](const Piece& h) { return (me - h.begin) / kJoin; };
+  if (tid < 2) {
+    const Piece h = tid ? part[1] : part[0];
     bool last = false;
     if (h.pieces > kSingle) {
       const uint32_t g = group_of(h);
@@ -779,9 +785,9 @@ __global__ __launch_bounds__(kWaves * 64, attn_per_cu(ST, DP)) void attn_kernel(
     } else if (h.pieces) {
       last = count_in(p.counters + h.begin, h.pieces);
     }
-    sh.last[threadIdx.x] = last;
+    sh.last[tid] = last;
   }
-  __syncthreads();
+  sync<NW>();
 #pragma unroll 1
   for (int i = 0; i < 2; ++i) {
     if (!sh.last[i]) continue;
@@ -793,16 +799,50 @@ __global__ __launch_bounds__(kWaves * 64, attn_per_cu(ST, DP)) void attn_kernel(
     while (true) {
       join<DT>(p, sh, h, first, stride, count, final);
       if (final) break;
-      settle();
-      if (threadIdx.x == 0) sh.last[i] = count_in(p.counters + h.begin, groups);
-      __syncthreads();
+      settle<NW>();
+      if (tid == 0) sh.last[i] = count_in(p.counters + h.begin, groups);
+      sync<NW>();
       if (!sh.last[i]) break;
       final = true;
       first = h.begin;
       stride = kJoin;
       count = groups;
     }
-    __syncthreads();  // sh is free again
+    sync<NW>();  // sh is free again
+  }
+}
+
+template <int DT, int ST, int DP>
+__global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(AttnParams p) {
+  __shared__ union {
+    Shared<DP, 4> together;
+    Shared<DP, 1> alone[4];
+  } sh;
+  const int lane = threadIdx.x & 63;
+  uint32_t sum = 0, few = 0;
+  for (int b = lane; b < p.batch; b += 64) {
+    const uint32_t t = tiles_of(p, p.lens[b]);
+    sum += t;
+    few += t == 1 || t == 2 ? 1 : 0;
+  }
+  const uint32_t heads = (uint32_t)(p.c.kv_heads * p.q_groups);
+  const uint32_t total = __builtin_amdgcn_readfirstlane(wave_sum(sum)) * heads;
+  const uint32_t small = __builtin_amdgcn_readfirstlane(wave_sum(few)) * heads;
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
+    if (tiles_of(p, p.lens[b]) == 0) {
+      const int d4 = p.c.head_dim / 4;
+      for (int i = threadIdx.x; i < p.q_heads * d4; i += kThreads) {
+        const int h = i / d4;
+        finish<DT>(p, b, h, (i - h * d4) * 4, f32x4{0, 0, 0, 0}, 0.0f, 0.0f);
+      }
+    }
+  // Where many heads have but a tile or two, a workgroup's waves would wait for each other at every
+  // one of them: each wave works by itself then.
+  if (3 * small >= gridDim.x) {
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    work<DT, ST, DP, 1>(p, sh.alone[wave], 4 * blockIdx.x + wave, 4 * gridDim.x, total);
+  } else {
+    work<DT, ST, DP, 4>(p, sh.together, blockIdx.x, gridDim.x, total);
   }
 }
 
@@ -810,11 +850,11 @@ template <int DT, int ST>
 void by_width(const AttnParams& p, int grid, hipStream_t s) {
   const int dp = attn_padded(p.c.head_dim);
   if (dp == 64)
-    attn_kernel<DT, ST, 64><<<grid, kWaves * 64, 0, s>>>(p);
+    attn_kernel<DT, ST, 64><<<grid, kThreads, 0, s>>>(p);
   else if (dp == 128)
-    attn_kernel<DT, ST, 128><<<grid, kWaves * 64, 0, s>>>(p);
+    attn_kernel<DT, ST, 128><<<grid, kThreads, 0, s>>>(p);
   else
-    attn_kernel<DT, ST, 256><<<grid, kWaves * 64, 0, s>>>(p);
+    attn_kernel<DT, ST, 256><<<grid, kThreads, 0, s>>>(p);
 }
 
 template <int DT>

@@ -223,11 +223,13 @@ int workgroups(const ag_attn_desc& d, int num_cus) {
                    : agmm::attn_per_cu(d.storage, agmm::attn_padded(d.head_dim)) * num_cus;
 }
 
+// Two partial results for each wave of a run, and three counters.
+int attn_rows(const ag_attn_desc& d) { return std::min(16, d.q_heads / d.kv_heads); }
 int64_t partials_bytes(const ag_attn_desc& d, int wgs) {
-  return align256((int64_t)2 * wgs * (16 * agmm::attn_padded(d.head_dim) + 32) * 4);
+  return align256((int64_t)2 * 4 * wgs * attn_rows(d) * (agmm::attn_padded(d.head_dim) + 2) * 4);
 }
 int64_t attn_bytes(const ag_attn_desc& d, int wgs) {
-  return partials_bytes(d, wgs) + align256((int64_t)3 * wgs * 4);
+  return partials_bytes(d, wgs) + align256((int64_t)3 * 4 * wgs * 4);
 }
 
 }  // namespace
@@ -506,6 +508,7 @@ int ag_attn_run(ag_attn_handle* h, const ag_kv_cache* cache, const void* q, int6
   p.c = view_of(*cache);
   p.group = d.q_heads / d.kv_heads;
   p.q_groups = (p.group + 15) / 16;
+  p.rows = attn_rows(d);
   p.capacity = cache->num_pages > 0 ? (int32_t)(table_len * cache->page_size) : 0;
   // every tile has a 32-bit number
   const int64_t seen = d.window ? std::min(d.window, (int64_t)p.capacity) : p.capacity;

@@ -85,13 +85,14 @@ struct AttnParams {
   const int32_t* table;
   const int32_t* lens;
   int64_t q_batch, q_head, o_batch, o_head, table_row;
-  float* partials;         // [2 * workgroups]: 16 rows of padded head_dim, then 16 m, 16 l
-  uint32_t* counters;      // [3 * workgroups]
+  float* partials;         // [2 * 4 * workgroups]: rows x (padded head_dim + 2)
+  uint32_t* counters;      // [3 * 4 * workgroups]
   int64_t window;          // 0 = all
   int32_t capacity;        // tokens that the table reaches
   int32_t num_pages;
   int32_t batch, q_heads;
   int32_t group, q_groups; // q heads of a kv head; 16-wide groups of them
+  int32_t rows;            // of a partial result: q heads in the largest of these groups
   float scale;             // times log2 e
   float cap, inv_cap;      // cap * log2 e, and 2 log2 e * scale / cap; cap 0 = none
 };
