@@ -91,14 +91,22 @@ __device__ inline float weight(float m, float top) {
   return m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top);
 }
 
-// Sum or maximum over the 4 lane groups of 16 (lanes l, l ^ 16, l ^ 32, l ^ 48).
+// Sum or maximum over the 4 lane groups of 16 (lanes l, l ^ 16, l ^ 32, l ^ 48), by exchanges of rows
+// between registers; a shuffle through LDS takes some 100 clocks, and every tile waits for one.
+template <class F>
+__device__ inline float across(float x, F f) {
+  const auto h = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x),
+                                                  __builtin_bit_cast(uint32_t, x), false, false);
+  x = f(__builtin_bit_cast(float, (uint32_t)h[0]), __builtin_bit_cast(float, (uint32_t)h[1]));
+  const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x),
+                                                  __builtin_bit_cast(uint32_t, x), false, false);
+  return f(__builtin_bit_cast(float, (uint32_t)r[0]), __builtin_bit_cast(float, (uint32_t)r[1]));
+}
 __device__ inline float across_max(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
+  return across(x, [](float a, float b) { return fmaxf(a, b); });
 }
 __device__ inline float across_sum(float x) {
-  x += __shfl_xor(x, 16);
-  return x + __shfl_xor(x, 32);
+  return across(x, [](float a, float b) { return a + b; });
 }
 
 // Stops the compiler from moving what is computed from x out of a loop, into registers that the loop
@@ -452,20 +460,21 @@ __device__ inline uint32_t tiles_of(const AttnParams& p, int32_t len) {
   return r.first == r.end ? 0 : (uint32_t)((r.end - r.from + kAttnTile - 1) / kAttnTile);
 }
 
-__device__ inline uint32_t wave_sum(uint32_t x) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) x += (uint32_t)__shfl_xor((int)x, d);
-  return x;
+template <int CTRL, int ROWS>
+__device__ inline uint32_t add_from(uint32_t x) {
+  return x + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false);
 }
-// Sum over the lanes up to and with this one.
+// Sum over the lanes up to and with this one: within rows of 16 lanes, then the rows' sums.
 __device__ inline uint32_t wave_scan(uint32_t x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint32_t y = (uint32_t)__shfl_up((int)x, d);
-    if (lane >= d) x += y;
-  }
-  return x;
+  x = add_from<0x111, 0xf>(x);
+  x = add_from<0x112, 0xf>(x);
+  x = add_from<0x114, 0xf>(x);
+  x = add_from<0x118, 0xf>(x);
+  x = add_from<0x142, 0xa>(x);
+  return add_from<0x143, 0xc>(x);
+}
+__device__ inline uint32_t wave_sum(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_readlane((int)wave_scan(x), 63);
 }
 
 // Elements e .. e + 3 of a row: o over the row's sum l, and the row's lse with element 0.
@@ -826,8 +835,8 @@ __global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(Att
     few += t == 1 || t == 2 ? 1 : 0;
   }
   const uint32_t heads = (uint32_t)(p.c.kv_heads * p.q_groups);
-  const uint32_t total = __builtin_amdgcn_readfirstlane(wave_sum(sum)) * heads;
-  const uint32_t small = __builtin_amdgcn_readfirstlane(wave_sum(few)) * heads;
+  const uint32_t total = wave_sum(sum) * heads;
+  const uint32_t small = wave_sum(few) * heads;
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
     if (tiles_of(p, p.lens[b]) == 0) {
       const int d4 = p.c.head_dim / 4;
