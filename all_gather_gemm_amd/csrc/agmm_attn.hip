@@ -31,7 +31,7 @@ namespace agmm {
 namespace {
 
 constexpr int kCus = 256;
-constexpr uint32_t kLeast = 4;       // tiles of a workgroup, at least, when all have work
+constexpr uint32_t kLeast = 4;       // tiles of a workgroup's share, at least
 constexpr int kSingle = 64;          // pieces that one workgroup joins; more are joined
 constexpr int kJoin = 16;            // in groups of this many first
 constexpr int kChunk = 16;           // pieces whose loads are in flight together
@@ -637,16 +637,15 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
 // The run of tiles of worker `me` of `wgs`, out of the `total` tiles of all sequences and heads.
 template <int DT, int ST, int DP, int NW>
 __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me, uint32_t wgs,
-                            uint32_t total) {
+                            uint32_t total, uint32_t least) {
   typedef Wave<DT, ST, DP> W;
   typedef typename W::R R;
   const int tid = thread<NW>(), lane = threadIdx.x & 63;
   const int wave = NW == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const uint32_t heads = (uint32_t)(p.c.kv_heads * p.q_groups);
+  // an equal share, but at least `least` tiles once that gives every compute unit 4 waves
   constexpr uint32_t kFill = 4 * kCus / NW;
-  // an equal share, but at least kLeast tiles once that gives every compute unit a workgroup
-  const uint32_t quota = max((total + wgs - 1) / wgs,
-                             min(kLeast, (total + kFill - 1) / kFill));
+  const uint32_t quota = max((total + wgs - 1) / wgs, min(least, (total + kFill - 1) / kFill));
   uint32_t cur = me * quota;
   if (cur >= total) return;
   const uint32_t end = min(cur + quota, total);
@@ -828,15 +827,15 @@ __global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(Att
     Shared<DP, 1> alone[4];
   } sh;
   const int lane = threadIdx.x & 63;
-  uint32_t sum = 0, few = 0;
+  uint32_t sum = 0, few = 0, some = 0;  // tiles; sequences with one or two; sequences with any
   for (int b = lane; b < p.batch; b += 64) {
     const uint32_t t = tiles_of(p, p.lens[b]);
     sum += t;
     few += t == 1 || t == 2 ? 1 : 0;
+    some += t ? 1 : 0;
   }
   const uint32_t heads = (uint32_t)(p.c.kv_heads * p.q_groups);
-  const uint32_t total = wave_sum(sum) * heads;
-  const uint32_t small = wave_sum(few) * heads;
+  const uint32_t tiles = wave_sum(sum), short_ones = wave_sum(few), sequences = wave_sum(some);
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
     if (tiles_of(p, p.lens[b]) == 0) {
       const int d4 = p.c.head_dim / 4;
@@ -846,12 +845,13 @@ __global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(Att
       }
     }
   // Where many heads have but a tile or two, a workgroup's waves would wait for each other at every
-  // one of them: each wave works by itself then.
-  if (3 * small >= gridDim.x) {
+  // one of them: each wave works by itself then, on two tiles or more unless no head has more than one.
+  if (3 * short_ones * heads >= gridDim.x) {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    work<DT, ST, DP, 1>(p, sh.alone[wave], 4 * blockIdx.x + wave, 4 * gridDim.x, total);
+    work<DT, ST, DP, 1>(p, sh.alone[wave], 4 * blockIdx.x + wave, 4 * gridDim.x, tiles * heads,
+                        tiles == sequences ? 1 : 2);
   } else {
-    work<DT, ST, DP, 4>(p, sh.together, blockIdx.x, gridDim.x, total);
+    work<DT, ST, DP, 4>(p, sh.together, blockIdx.x, gridDim.x, tiles * heads, kLeast);
   }
 }
 
