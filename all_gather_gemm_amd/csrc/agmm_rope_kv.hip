@@ -22,9 +22,13 @@ __device__ inline void turn(uint64_t f, int64_t pos, float mag, float& c, float&
   s = mag * __builtin_amdgcn_sinf(t);
 }
 
+// The empty asm keeps the results 32-bit values that are rounded to 16 bits afterwards: folded into a
+// mixed-precision multiply-add in some places and not in others, the same pair would differ in its
+// last bit between them.
 __device__ inline void rotate(float a, float b, float c, float s, float& ya, float& yb) {
   ya = fmaf(a, c, -(b * s));
   yb = fmaf(b, c, a * s);
+  asm("" : "+v"(ya), "+v"(yb));
 }
 
 template <int DT>
@@ -37,14 +41,17 @@ __device__ inline void put(uint16_t* p, float x) {
 }
 
 // One unit of one token's head in the rotated part, for up to HPT heads: 8 pairs (half) or 4
-// (interleaved); the last unit of a rotated part that is no multiple of that takes its n pairs one
-// by one. A pair is read and written by one thread only, so y may be x.
+// (interleaved). The last unit of a rotated part that is no multiple of that begins earlier, and what
+// two units share is written twice, the same; in place, where a pair has to be read and written by
+// one thread only, it takes its n pairs one by one (4096 tokens x 72 heads of 128 with 24 rotated: 47
+// us pair by pair).
 template <int DT, bool HALF, bool GRAD, int HPT>
 __device__ inline void rotate_unit(const RopeParams& p, uint32_t u, int64_t pos,
                                    const uint16_t* x, uint16_t* y, uint32_t h0) {
   constexpr int NP = HALF ? 8 : 4;
   const int r2 = p.plan.rot_dim / 2;
-  const int i0 = (int)u * NP;
+  int i0 = (int)u * NP;
+  if (!p.in_place && r2 >= NP) i0 = min(i0, r2 - NP);
   const int n = min(NP, r2 - i0);
   const int e1 = p.plan.rot_start + (HALF ? i0 : 2 * i0);
   float c[NP], s[NP];
@@ -103,25 +110,33 @@ __device__ inline void rotate_unit(const RopeParams& p, uint32_t u, int64_t pos,
   }
 }
 
-// One unit of the elements that pass through: 8 of them, or the n < 8 at the end of their run.
+// One unit of the elements that pass through (never in place): 8 of them, the last unit of a run
+// beginning earlier where needed, or all n of a run shorter than that.
+template <int HPT>
 __device__ inline void pass_unit(const RopeParams& p, uint32_t u, const uint16_t* x, uint16_t* y,
                                  uint32_t h0) {
-  int e, n;
-  if (u < (uint32_t)p.pass_units0) {
-    e = (int)u * 8;
-    n = min(8, p.plan.rot_start - e);
-  } else {
-    e = p.plan.rot_start + p.plan.rot_dim + (int)(u - p.pass_units0) * 8;
-    n = min(8, p.plan.head_dim - e);
-  }
-  for (uint32_t h = h0; h < (uint32_t)p.heads; h += p.groups.d) {
-    const uint16_t* q = x + (int64_t)h * p.x_head + e;
-    uint16_t* w = y + (int64_t)h * p.y_head + e;
-    if (n == 8) {
-      store16(w, load16(q));
-    } else {
-      for (int k = 0; k < n; ++k) w[k] = q[k];
+  const bool front = u < (uint32_t)p.pass_units0;
+  const int begin = front ? 0 : p.plan.rot_start + p.plan.rot_dim;
+  const int end = front ? p.plan.rot_start : p.plan.head_dim;
+  const int n = min(8, end - begin);
+  const int e = min(begin + 8 * (int)(front ? u : u - p.pass_units0), end - n);
+  const uint32_t step = p.groups.d;
+  if (n == 8) {
+    u32x4 a[HPT];
+#pragma unroll
+    for (int j = 0; j < HPT; ++j) {
+      if (h0 + j * step >= (uint32_t)p.heads) break;
+      a[j] = load16(x + (int64_t)(h0 + j * step) * p.x_head + e);
     }
+#pragma unroll
+    for (int j = 0; j < HPT; ++j) {
+      if (h0 + j * step >= (uint32_t)p.heads) break;
+      store16(y + (int64_t)(h0 + j * step) * p.y_head + e, a[j]);
+    }
+  } else {
+    for (uint32_t h = h0; h < (uint32_t)p.heads; h += step)
+      for (int k = 0; k < n; ++k)
+        y[(int64_t)h * p.y_head + e + k] = x[(int64_t)h * p.x_head + e + k];
   }
 }
 
@@ -135,7 +150,7 @@ __device__ inline void rope_thread(const RopeParams& p, uint32_t idx, int64_t b)
   if (u < (uint32_t)p.rot_units) {
     rotate_unit<DT, HALF, GRAD, HPT>(p, u, p.positions[b * p.pos_batch + t], x, y, h0);
   } else if (!p.in_place) {
-    pass_unit(p, u - p.rot_units, x, y, h0);
+    pass_unit<HPT>(p, u - p.rot_units, x, y, h0);
   }
 }
 
