@@ -337,7 +337,9 @@ struct Wave {
       for (int t = 0; t < R::kSub; ++t) {
         const uint32_t mine = (uint32_t)(there >> (16 * t)) >> (4 * g);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) st[t][j] = (mine >> j) & 1u ? st[t][j] : -INFINITY;
+        for (int j = 0; j < 4; ++j)
+          st[t][j] = __builtin_bit_cast(
+              float, here(__builtin_bit_cast(int, (mine >> j) & 1u ? st[t][j] : -INFINITY)));
       }
     }
     float top = -INFINITY;
@@ -416,14 +418,15 @@ struct Wave {
             }
           }
         }
-        if (there != kAll) {  // the values of tokens that are not attended to count as zeros
-          const int me = here(g);
+        // the values of tokens that are not attended to count as zeros (the results go through here()
+        // so that this stays a branch, which all but the last tiles skip)
+        if (there != kAll) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (!((uint32_t)(there >> (16 * (h + j / 4))) >> (4 * me + j % 4) & 1u)) {
+          for (int j = 0; j < 8; ++j) {
+            const bool keep = (uint32_t)(there >> (16 * (h + j / 4))) >> (4 * here(g) + j % 4) & 1u;
 #pragma unroll
-              for (int i = 0; i < R::kElems / 2; ++i) v[j][i] = 0;
-            }
+            for (int i = 0; i < R::kElems / 2; ++i) v[j][i] = here(keep ? v[j][i] : 0);
+          }
         }
 #pragma unroll
         for (int e = 0; e < R::kElems; ++e) {
@@ -701,8 +704,8 @@ __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me
       const uint64_t there = __ballot(ok) & W::kAll;
       const uint32_t t = (uint32_t)tok;
       const uint32_t row = t - (t / p.c.page_size) * p.c.page_size.d;
-      at[lane][0] = ok ? page * p.c.page + row * p.c.row : 0;
-      if (R::kScales) at[lane][1] = ok ? page * p.c.s_page + row * p.c.s_row : 0;
+      at[lane][0] = ok ? row_at(p.c, page, row) : 0;
+      if (R::kScales) at[lane][1] = ok ? scales_at(p.c, page, row) : 0;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       return there;

@@ -136,11 +136,14 @@ int check_cache(const ag_kv_cache* c) {
   if (c->page_stride < 0 || c->head_stride < 0 || c->row_stride < 0 ||
       (c->page_stride | c->head_stride | c->row_stride) & 15)
     return AGMM_ERR_INVALID_ARG;
+  const int64_t wide = (int64_t)1 << 32;
+  if (c->page_stride >= wide || c->row_stride >= wide) return AGMM_ERR_UNSUPPORTED;
   if (c->num_pages > 0 && (!aligned(c->k, 16) || !aligned(c->v, 16))) return AGMM_ERR_INVALID_ARG;
   if (c->storage != AG_KV_16BIT) {
     if (c->scale_page < 0 || c->scale_head < 0 || c->scale_row < 0 ||
         (c->scale_page | c->scale_head | c->scale_row) & 3)
       return AGMM_ERR_INVALID_ARG;
+    if (c->scale_page >= wide || c->scale_row >= wide) return AGMM_ERR_UNSUPPORTED;
     if (c->num_pages > 0 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
       return AGMM_ERR_INVALID_ARG;
   } else if (c->k_scale || c->v_scale) {
@@ -155,12 +158,12 @@ CacheView view_of(const ag_kv_cache& c) {
   v.v = (char*)c.v;
   v.ks = (char*)c.k_scale;
   v.vs = (char*)c.v_scale;
-  v.page = c.page_stride;
+  v.page = (uint32_t)c.page_stride;
   v.head = c.head_stride;
-  v.row = c.row_stride;
-  v.s_page = c.scale_page;
+  v.row = (uint32_t)c.row_stride;
+  v.s_page = (uint32_t)c.scale_page;
   v.s_head = c.scale_head;
-  v.s_row = c.scale_row;
+  v.s_row = (uint32_t)c.scale_row;
   v.page_size = agmm::fast_div((uint32_t)c.page_size);
   v.rows = (uint32_t)(c.num_pages * c.page_size);
   v.head_dim = c.head_dim;

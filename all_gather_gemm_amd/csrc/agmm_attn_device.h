@@ -23,6 +23,14 @@ __device__ inline uint32_t operator/(uint32_t n, const FastDiv& f) {
   return (__umulhi(f.mul, n) + n) >> f.shift;
 }
 
+// Bytes from the pools' starts (of one head) to a row, and to its scales.
+__device__ inline int64_t row_at(const CacheView& c, uint32_t page, uint32_t row) {
+  return (int64_t)((uint64_t)page * c.page + (uint64_t)row * c.row);
+}
+__device__ inline int64_t scales_at(const CacheView& c, uint32_t page, uint32_t row) {
+  return (int64_t)((uint64_t)page * c.s_page + (uint64_t)row * c.s_row);
+}
+
 __device__ inline u32x4 load16(const uint16_t* p) {
   return *reinterpret_cast<const u32x4_any*>(p);
 }

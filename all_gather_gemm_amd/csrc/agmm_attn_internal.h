@@ -49,7 +49,8 @@ struct RopeParams {
 
 struct CacheView {
   char *k, *v, *ks, *vs;
-  int64_t page, head, row, s_page, s_head, s_row;  // bytes
+  int64_t head, s_head;              // bytes
+  uint32_t page, row, s_page, s_row;
   FastDiv page_size;
   uint32_t rows;                                   // num_pages * page_size
   int32_t head_dim, kv_heads;

@@ -281,9 +281,8 @@ __device__ inline void append_thread(const CacheParams& p, uint32_t idx) {
   const u32x4 v = load16(vh + 8 * ch);
   const u32x4 k = ROPE ? rotated_chunk<DT, HALF>(p.plan, p.positions[t], kh, 8 * (int)ch)
                        : load16(kh + 8 * ch);
-  const int64_t at = (int64_t)page * p.c.page + (int64_t)h * p.c.head + (int64_t)row * p.c.row;
-  const int64_t sat =
-      (int64_t)page * p.c.s_page + (int64_t)h * p.c.s_head + (int64_t)row * p.c.s_row;
+  const int64_t at = row_at(p.c, page, row) + (int64_t)h * p.c.head;
+  const int64_t sat = scales_at(p.c, page, row) + (int64_t)h * p.c.s_head;
   write_chunk<DT, ST>(p.c.k + at, p.c.ks + sat, ch, k);
   write_chunk<DT, ST>(p.c.v + at, p.c.vs + sat, ch, v);
 }
@@ -312,9 +311,8 @@ __global__ __launch_bounds__(kThreads) void read_kernel(CacheParams p) {
   if (slot >= 0 && slot < (int64_t)p.c.rows) {
     const uint32_t page = (uint32_t)slot / p.c.page_size;
     const uint32_t row = (uint32_t)slot - page * p.c.page_size.d;
-    const int64_t at = (int64_t)page * p.c.page + (int64_t)h * p.c.head + (int64_t)row * p.c.row;
-    const int64_t sat =
-        (int64_t)page * p.c.s_page + (int64_t)h * p.c.s_head + (int64_t)row * p.c.s_row;
+    const int64_t at = row_at(p.c, page, row) + (int64_t)h * p.c.head;
+    const int64_t sat = scales_at(p.c, page, row) + (int64_t)h * p.c.s_head;
     k = read_chunk<DT, ST>(p.c.k + at, p.c.ks + sat, ch);
     v = read_chunk<DT, ST>(p.c.v + at, p.c.vs + sat, ch);
   }

@@ -112,9 +112,10 @@ typedef struct ag_kv_cache {
   int32_t reserved;  /* 0 */
   int64_t num_pages; /* num_pages * page_size < 2^31 */
   void *k, *v;       /* device, 16-byte aligned */
-  int64_t page_stride, head_stride, row_stride; /* bytes, of k and of v: multiples of 16, >= 0 */
+  int64_t page_stride, head_stride, row_stride; /* bytes, of k and of v: multiples of 16, >= 0;
+                                                   pages and rows below 2^32 apart */
   void *k_scale, *v_scale; /* device, 4-byte aligned; NULL for 16BIT */
-  int64_t scale_page, scale_head, scale_row;    /* bytes, >= 0, multiples of 4 */
+  int64_t scale_page, scale_head, scale_row;    /* the same of the scales: multiples of 4 */
 } ag_kv_cache;
 
 /* Writes the keys and values of `tokens` tokens to their slots.

@@ -115,6 +115,8 @@ def _cache(T, **kw):
     (UNSUPPORTED, dict(storage=1, head_dim=80)), (UNSUPPORTED, dict(storage=2, head_dim=16)),
     (UNSUPPORTED, dict(num_pages=1 << 27)), (UNSUPPORTED, dict(num_pages=1 << 31)),
     (UNSUPPORTED, dict(num_pages=(1 << 62) + 1)),
+    (UNSUPPORTED, dict(page_stride=1 << 32)), (UNSUPPORTED, dict(row_stride=1 << 40)),
+    (UNSUPPORTED, dict(storage=1, scale_page=1 << 32)),
     (INVALID, dict(page_stride=8200)), (INVALID, dict(row_stride=-256)), (INVALID, dict(k=4104)),
     (INVALID, dict(v=None)), (INVALID, dict(k_scale=4096)),
     (INVALID, dict(storage=1, k_scale=None)), (INVALID, dict(storage=1, scale_row=2)),
@@ -166,13 +168,15 @@ def test_attention_refusals(T, rc, bad):
 
 
 def test_attention_workspace(T):
-    # two partial results of 16 padded rows, 16 maxima and 16 sums for each workgroup (two a compute
-    # unit, one for rows of 256 16-bit elements), and three counters
+    # two partial results (the group's rows, each padded and with its maximum and sum) and three
+    # counters for each wave: 4 a workgroup, two workgroups a compute unit, one for rows of 256 16-bit
+    # elements
     al = lambda x: (x + 255) & ~255  # noqa: E731
     for hd, padded, wgs in ((64, 64, 512), (80, 128, 512), (128, 128, 512), (136, 256, 256)):
-        d = _attn(T, head_dim=hd, q_heads=8, kv_heads=2)
-        assert T.lib.ag_attn_workspace_bytes(ctypes.byref(d)) == \
-            al(2 * wgs * (16 * padded + 32) * 4) + al(3 * wgs * 4)
+        for q_heads, rows in ((8, 4), (64, 16)):
+            d = _attn(T, head_dim=hd, q_heads=q_heads, kv_heads=2)
+            assert T.lib.ag_attn_workspace_bytes(ctypes.byref(d)) == \
+                al(8 * wgs * rows * (padded + 2) * 4) + al(12 * wgs * 4)
 
 
 def test_binding_refuses_cpu_tensors(T):
