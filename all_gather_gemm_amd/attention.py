@@ -307,8 +307,7 @@ class PagedCache:
         _tensor(slots, "slots", torch.int64, (tokens,), device)
         k = slots.new_empty(shape, dtype=td) if k_out is None else \
             _tensor(k_out, "k_out", td, shape, device)
-        v = slots.new_empty(shape, dtype=td) if v_out is None else \
-            _tensor(v_out, "v_out", td, shape, device)
+        v = torch.empty_like(k) if v_out is None else _tensor(v_out, "v_out", td, shape, device)
         ks, vs = k.stride(), v.stride()
         rc = lib.ag_kv_read(self._ref, slots.data_ptr(), tokens, k.data_ptr(), ks[0], ks[1],
                             v.data_ptr(), vs[0], vs[1], _stream(stream, device.index))

@@ -32,7 +32,7 @@ namespace {
 
 constexpr int kCus = 256;
 constexpr uint32_t kLeast = 4;       // tiles of a workgroup's share, at least
-constexpr int kSingle = 64;          // pieces that one workgroup joins; more are joined
+constexpr int kSingle = 32;          // pieces that are joined at once; more are joined
 constexpr int kJoin = 16;            // in groups of this many first
 constexpr int kChunk = 16;           // pieces whose loads are in flight together
 constexpr float kHead = 7.0f;        // weights are 2^(s - m + kHead)

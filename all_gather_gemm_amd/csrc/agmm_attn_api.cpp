@@ -113,14 +113,14 @@ agmm::RopePlan plan_of(const ag_rope_handle& h) {
   return r;
 }
 
-// Units of a head and how threads share them; per_thread heads go to one thread.
-void rope_units(const ag_rope_desc& d, int64_t heads, int per_thread, RopeParams* p) {
+// The units that threads take of a head.
+void rope_units(const ag_rope_desc& d, int64_t heads, RopeParams* p) {
   p->rot_units = d.pairing == AG_ROPE_HALF ? (d.rot_dim / 2 + 7) / 8 : (d.rot_dim / 2 + 3) / 4;
   p->pass_units0 = (d.rot_start + 7) / 8;
-  p->pass_units1 = (d.head_dim - d.rot_start - d.rot_dim + 7) / 8;
-  const int pass = p->in_place ? 0 : p->pass_units0 + p->pass_units1;
+  const int behind = (d.head_dim - d.rot_start - d.rot_dim + 7) / 8;
+  const int pass = p->in_place ? 0 : p->pass_units0 + behind;
   p->units = agmm::fast_div((uint32_t)(p->rot_units + pass));
-  p->groups = agmm::fast_div((uint32_t)((heads + per_thread - 1) / per_thread));
+  p->heads = agmm::fast_div((uint32_t)heads);
 }
 
 int check_cache(const ag_kv_cache* c) {
@@ -319,15 +319,9 @@ int ag_rope_run(ag_rope_handle* h, const void* x, int64_t x_batch, int64_t x_tok
   p.y_token = y_token;
   p.y_head = y_head;
   p.pos_batch = pos_batch;
-  p.heads = (int32_t)heads;
   p.in_place = x == y && x_batch == y_batch && x_token == y_token && x_head == y_head;
-  // Four heads to a thread share the angles of a unit once that still leaves enough threads to fill
-  // the chip's 2048 places a compute unit twice over; one head to a thread below.
-  rope_units(h->desc, heads, 1, &p);
-  const int per =
-      (double)batch * tokens * heads * p.units.d >= 4.0 * 2 * 2048 * kDefaultCus ? 4 : 1;
-  rope_units(h->desc, heads, per, &p);
-  const uint64_t per_token = (uint64_t)p.units.d * p.groups.d;
+  rope_units(h->desc, heads, &p);
+  const uint64_t per_token = (uint64_t)p.units.d * p.heads.d;
   const int64_t step = tokens_per_launch(per_token), bstep = 65535;
   for (int64_t b0 = 0; b0 < batch; b0 += bstep)
     for (int64_t t0 = 0; t0 < tokens; t0 += step) {
@@ -335,9 +329,8 @@ int ag_rope_run(ag_rope_handle* h, const void* x, int64_t x_batch, int64_t x_tok
       p.x = (const uint16_t*)x + b0 * x_batch + t0 * x_token;
       p.y = (uint16_t*)y + b0 * y_batch + t0 * y_token;
       p.positions = positions + b0 * pos_batch + t0;
-      p.tokens = (int32_t)n;
       p.total = (uint32_t)(n * (int64_t)per_token);
-      ATTN_HIP(agmm::launch_rope(p, h->desc.dtype, h->desc.pairing, gradient, per,
+      ATTN_HIP(agmm::launch_rope(p, h->desc.dtype, h->desc.pairing, gradient,
                                  std::min(bstep, batch - b0), (hipStream_t)hip_stream));
     }
   return AGMM_OK;
@@ -390,10 +383,9 @@ int ag_kv_append_rope(const ag_kv_cache* cache, ag_rope_handle* rope, const void
   r.x_head = q_head;
   r.y_token = qo_token;
   r.y_head = qo_head;
-  r.heads = (int32_t)q_heads;
   r.in_place = q == q_out && q_token == qo_token && q_head == qo_head;
-  rope_units(rope->desc, std::max<int64_t>(1, q_heads), 1, &r);
-  const uint64_t q_threads = q_heads ? (uint64_t)r.units.d * r.groups.d : 0;
+  rope_units(rope->desc, std::max<int64_t>(1, q_heads), &r);
+  const uint64_t q_threads = q_heads ? (uint64_t)r.units.d * r.heads.d : 0;
   const int64_t step = tokens_per_launch(
       std::max(q_threads, (uint64_t)cache->kv_heads * (cache->head_dim / 8)));
   for (int64_t t0 = 0; t0 < tokens; t0 += step) {
@@ -403,7 +395,6 @@ int ag_kv_append_rope(const ag_kv_cache* cache, ag_rope_handle* rope, const void
     r.x = (const uint16_t*)q + t0 * q_token;
     r.y = (uint16_t*)q_out + t0 * qo_token;
     r.positions = positions + t0;
-    r.tokens = (int32_t)n;
     r.total = (uint32_t)(n * (int64_t)q_threads);
     p.q_blocks = (r.total + 255) / 256;
     ATTN_HIP(agmm::launch_append(p, &r, cache->dtype, cache->storage, rope->desc.pairing,

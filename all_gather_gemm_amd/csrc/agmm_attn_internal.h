@@ -30,21 +30,19 @@ struct RopePlan {
   int32_t head_dim, rot_dim, rot_start;
 };
 
-// Heads to rotate: `tokens` x `heads` of one batch entry (blockIdx.y), element strides.
+// Heads to rotate, of one batch entry (blockIdx.y): element strides.
 struct RopeParams {
   RopePlan plan;
   const uint16_t* x;
   uint16_t* y;
   const int64_t* positions;
   int64_t x_batch, x_token, x_head, y_batch, y_token, y_head, pos_batch;
-  int32_t tokens, heads;
   int32_t in_place;         // the elements that pass through need no copy
   int32_t rot_units;        // units of a head that rotate (8 half pairs or 4 interleaved ones),
-  int32_t pass_units0;      // units of 8 elements in front of the rotated part,
-  int32_t pass_units1;      // and behind it
+  int32_t pass_units0;      // and units of 8 elements in front of the rotated part
   FastDiv units;            // all units of a head
-  FastDiv groups;           // threads share a head's units; each takes heads g, g + groups, ...
-  uint32_t total;           // threads: tokens * groups * units
+  FastDiv heads;
+  uint32_t total;           // threads: tokens * heads * units
 };
 
 struct CacheView {
@@ -98,8 +96,8 @@ struct AttnParams {
   float cap, inv_cap;      // cap * log2 e, and 2 log2 e * scale / cap; cap 0 = none
 };
 
-hipError_t launch_rope(const RopeParams& p, int dtype, int pairing, int gradient, int per_thread,
-                       int64_t batch, hipStream_t s);
+hipError_t launch_rope(const RopeParams& p, int dtype, int pairing, int gradient, int64_t batch,
+                       hipStream_t s);
 // rope: nullptr, or the rotation of q (its threads come in the leading q_blocks workgroups)
 hipError_t launch_append(const CacheParams& p, const RopeParams* rope, int dtype, int storage,
                          int pairing, hipStream_t s);

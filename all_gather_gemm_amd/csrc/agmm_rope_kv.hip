@@ -40,123 +40,92 @@ __device__ inline void put(uint16_t* p, float x) {
   *p = (uint16_t)T16<DT>::pack(x, 0.0f);
 }
 
-// One unit of one token's head in the rotated part, for up to HPT heads: 8 pairs (half) or 4
-// (interleaved). The last unit of a rotated part that is no multiple of that begins earlier, and what
-// two units share is written twice, the same; in place, where a pair has to be read and written by
-// one thread only, it takes its n pairs one by one (4096 tokens x 72 heads of 128 with 24 rotated: 47
-// us pair by pair).
-template <int DT, bool HALF, bool GRAD, int HPT>
+// One unit of a head's rotated part: 8 pairs (half) or 4 (interleaved). The last unit of a rotated
+// part that is no multiple of that begins earlier, and what two units share is written twice, the
+// same; in place, where a pair has to be read and written by one thread only, it takes its n pairs
+// one by one (4096 tokens x 72 heads of 128, 24 rotated: 33 us so, 47 us pair by pair).
+//
+// A thread takes one unit of one head and makes its own angles. Four heads to a thread, which share
+// them, measured slower: 16384 x 72 heads of 128 108 us against 100, 4097 x 28 of 80 9.5 against 8.7.
+template <int DT, bool HALF, bool GRAD>
 __device__ inline void rotate_unit(const RopeParams& p, uint32_t u, int64_t pos,
-                                   const uint16_t* x, uint16_t* y, uint32_t h0) {
+                                   const uint16_t* x, uint16_t* y) {
   constexpr int NP = HALF ? 8 : 4;
   const int r2 = p.plan.rot_dim / 2;
   int i0 = (int)u * NP;
   if (!p.in_place && r2 >= NP) i0 = min(i0, r2 - NP);
   const int n = min(NP, r2 - i0);
   const int e1 = p.plan.rot_start + (HALF ? i0 : 2 * i0);
+  x += e1;
+  y += e1;
   float c[NP], s[NP];
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
     turn(p.plan.turns[i0 + k], pos, p.plan.magnitude, c[k], s[k]);  // (the table is padded)
     if (GRAD) s[k] = -s[k];
   }
-  const uint32_t step = p.groups.d;
   if (n == NP) {
-    u32x4 a[HPT], b[HPT];
+    const u32x4 a = load16(x), b = HALF ? load16(x + r2) : a;
+    u32x4 ya, yb;
 #pragma unroll
-    for (int j = 0; j < HPT; ++j) {
-      if (h0 + j * step >= (uint32_t)p.heads) break;
-      const uint16_t* q = x + (int64_t)(h0 + j * step) * p.x_head + e1;
-      a[j] = load16(q);
-      if (HALF) b[j] = load16(q + r2);
-    }
-#pragma unroll
-    for (int j = 0; j < HPT; ++j) {
-      if (h0 + j * step >= (uint32_t)p.heads) break;
-      uint16_t* q = y + (int64_t)(h0 + j * step) * p.y_head + e1;
-      u32x4 ya, yb;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (HALF) {
-          float y0, y1, z0, z1;
-          rotate(T16<DT>::lo(a[j][k]), T16<DT>::lo(b[j][k]), c[2 * k], s[2 * k], y0, z0);
-          rotate(T16<DT>::hi(a[j][k]), T16<DT>::hi(b[j][k]), c[(2 * k + 1) % NP],
-                 s[(2 * k + 1) % NP], y1, z1);
-          ya[k] = T16<DT>::pack(y0, y1);
-          yb[k] = T16<DT>::pack(z0, z1);
-        } else {
-          float y0, y1;
-          rotate(T16<DT>::lo(a[j][k]), T16<DT>::hi(a[j][k]), c[k], s[k], y0, y1);
-          ya[k] = T16<DT>::pack(y0, y1);
-        }
+    for (int k = 0; k < 4; ++k) {
+      float y0, y1, z0, z1;
+      if (HALF) {
+        rotate(T16<DT>::lo(a[k]), T16<DT>::lo(b[k]), c[2 * k % NP], s[2 * k % NP], y0, z0);
+        rotate(T16<DT>::hi(a[k]), T16<DT>::hi(b[k]), c[(2 * k + 1) % NP], s[(2 * k + 1) % NP], y1,
+               z1);
+        yb[k] = T16<DT>::pack(z0, z1);
+      } else {
+        rotate(T16<DT>::lo(a[k]), T16<DT>::hi(a[k]), c[k], s[k], y0, y1);
       }
-      store16(q, ya);
-      if (HALF) store16(q + r2, yb);
+      ya[k] = T16<DT>::pack(y0, y1);
     }
+    store16(y, ya);
+    if (HALF) store16(y + r2, yb);
   } else {
-    for (uint32_t h = h0; h < (uint32_t)p.heads; h += step) {
-      const uint16_t* q = x + (int64_t)h * p.x_head + e1;
-      uint16_t* w = y + (int64_t)h * p.y_head + e1;
 #pragma unroll
-      for (int k = 0; k < NP; ++k)
-        if (k < n) {
-          const int ia = HALF ? k : 2 * k, ib = HALF ? k + r2 : 2 * k + 1;
-          float ya, yb;
-          rotate(value<DT>(q + ia), value<DT>(q + ib), c[k], s[k], ya, yb);
-          put<DT>(w + ia, ya);
-          put<DT>(w + ib, yb);
-        }
-    }
+    for (int k = 0; k < NP; ++k)
+      if (k < n) {
+        const int ia = HALF ? k : 2 * k, ib = HALF ? k + r2 : 2 * k + 1;
+        float ya, yb;
+        rotate(value<DT>(x + ia), value<DT>(x + ib), c[k], s[k], ya, yb);
+        put<DT>(y + ia, ya);
+        put<DT>(y + ib, yb);
+      }
   }
 }
 
 // One unit of the elements that pass through (never in place): 8 of them, the last unit of a run
 // beginning earlier where needed, or all n of a run shorter than that.
-template <int HPT>
-__device__ inline void pass_unit(const RopeParams& p, uint32_t u, const uint16_t* x, uint16_t* y,
-                                 uint32_t h0) {
+__device__ inline void pass_unit(const RopeParams& p, uint32_t u, const uint16_t* x, uint16_t* y) {
   const bool front = u < (uint32_t)p.pass_units0;
   const int begin = front ? 0 : p.plan.rot_start + p.plan.rot_dim;
   const int end = front ? p.plan.rot_start : p.plan.head_dim;
   const int n = min(8, end - begin);
   const int e = min(begin + 8 * (int)(front ? u : u - p.pass_units0), end - n);
-  const uint32_t step = p.groups.d;
   if (n == 8) {
-    u32x4 a[HPT];
-#pragma unroll
-    for (int j = 0; j < HPT; ++j) {
-      if (h0 + j * step >= (uint32_t)p.heads) break;
-      a[j] = load16(x + (int64_t)(h0 + j * step) * p.x_head + e);
-    }
-#pragma unroll
-    for (int j = 0; j < HPT; ++j) {
-      if (h0 + j * step >= (uint32_t)p.heads) break;
-      store16(y + (int64_t)(h0 + j * step) * p.y_head + e, a[j]);
-    }
+    store16(y + e, load16(x + e));
   } else {
-    for (uint32_t h = h0; h < (uint32_t)p.heads; h += step)
-      for (int k = 0; k < n; ++k)
-        y[(int64_t)h * p.y_head + e + k] = x[(int64_t)h * p.x_head + e + k];
+    for (int k = 0; k < n; ++k) y[e + k] = x[e + k];
   }
 }
 
-template <int DT, bool HALF, bool GRAD, int HPT>
+template <int DT, bool HALF, bool GRAD>
 __device__ inline void rope_thread(const RopeParams& p, uint32_t idx, int64_t b) {
   if (idx >= p.total) return;
   const uint32_t r = idx / p.units, u = idx - r * p.units.d;
-  const uint32_t t = r / p.groups, h0 = r - t * p.groups.d;
-  const uint16_t* x = p.x + b * p.x_batch + (int64_t)t * p.x_token;
-  uint16_t* y = p.y + b * p.y_batch + (int64_t)t * p.y_token;
-  if (u < (uint32_t)p.rot_units) {
-    rotate_unit<DT, HALF, GRAD, HPT>(p, u, p.positions[b * p.pos_batch + t], x, y, h0);
-  } else if (!p.in_place) {
-    pass_unit<HPT>(p, u - p.rot_units, x, y, h0);
-  }
+  const uint32_t t = r / p.heads, h = r - t * p.heads.d;
+  const uint16_t* x = p.x + b * p.x_batch + (int64_t)t * p.x_token + (int64_t)h * p.x_head;
+  uint16_t* y = p.y + b * p.y_batch + (int64_t)t * p.y_token + (int64_t)h * p.y_head;
+  if (u < (uint32_t)p.rot_units)
+    rotate_unit<DT, HALF, GRAD>(p, u, p.positions[b * p.pos_batch + t], x, y);
+  else
+    pass_unit(p, u - p.rot_units, x, y);
 }
 
-template <int DT, bool HALF, bool GRAD, int HPT>
+template <int DT, bool HALF, bool GRAD>
 __global__ __launch_bounds__(kThreads) void rope_kernel(RopeParams p) {
-  rope_thread<DT, HALF, GRAD, HPT>(p, blockIdx.x * kThreads + threadIdx.x, blockIdx.y);
+  rope_thread<DT, HALF, GRAD>(p, blockIdx.x * kThreads + threadIdx.x, blockIdx.y);
 }
 
 // ---- the cache ----
@@ -295,7 +264,7 @@ __global__ __launch_bounds__(kThreads) void append_kernel(CacheParams p) {
 template <int DT, int ST, bool HALF>
 __global__ __launch_bounds__(kThreads) void append_rope_kernel(CacheParams p, RopeParams q) {
   if (blockIdx.x < p.q_blocks)
-    rope_thread<DT, HALF, false, 1>(q, blockIdx.x * kThreads + threadIdx.x, 0);
+    rope_thread<DT, HALF, false>(q, blockIdx.x * kThreads + threadIdx.x, 0);
   else
     append_thread<DT, ST, true, HALF>(p, (blockIdx.x - p.q_blocks) * kThreads + threadIdx.x);
 }
@@ -320,34 +289,31 @@ __global__ __launch_bounds__(kThreads) void read_kernel(CacheParams p) {
   store16(p.v_out + (int64_t)t * p.v_token + (int64_t)h * p.v_head + 8 * ch, v);
 }
 
-template <int DT, bool HALF, bool GRAD>
-void rope_by_heads(const RopeParams& p, int per_thread, dim3 grid, hipStream_t s) {
-  if (per_thread == 1)
-    rope_kernel<DT, HALF, GRAD, 1><<<grid, kThreads, 0, s>>>(p);
-  else
-    rope_kernel<DT, HALF, GRAD, 4><<<grid, kThreads, 0, s>>>(p);
-}
-
 inline uint32_t blocks(uint32_t threads) { return (threads + kThreads - 1) / kThreads; }
 
 }  // namespace
 
-hipError_t launch_rope(const RopeParams& p, int dtype, int pairing, int gradient, int per_thread,
-                       int64_t batch, hipStream_t s) {
+hipError_t launch_rope(const RopeParams& p, int dtype, int pairing, int gradient, int64_t batch,
+                       hipStream_t s) {
   const dim3 grid(blocks(p.total), (uint32_t)batch);
-  auto by = [&](auto dt) {
+  auto by = [&](auto dt, auto half) {
     constexpr int DT = decltype(dt)::value;
-    if (pairing == AG_ROPE_HALF)
-      gradient ? rope_by_heads<DT, true, true>(p, per_thread, grid, s)
-               : rope_by_heads<DT, true, false>(p, per_thread, grid, s);
+    constexpr bool HALF = decltype(half)::value;
+    if (gradient)
+      rope_kernel<DT, HALF, true><<<grid, kThreads, 0, s>>>(p);
     else
-      gradient ? rope_by_heads<DT, false, true>(p, per_thread, grid, s)
-               : rope_by_heads<DT, false, false>(p, per_thread, grid, s);
+      rope_kernel<DT, HALF, false><<<grid, kThreads, 0, s>>>(p);
+  };
+  auto pairs = [&](auto dt) {
+    if (pairing == AG_ROPE_HALF)
+      by(dt, std::true_type());
+    else
+      by(dt, std::false_type());
   };
   if (dtype == AGMM_F16)
-    by(std::integral_constant<int, AGMM_F16>());
+    pairs(std::integral_constant<int, AGMM_F16>());
   else
-    by(std::integral_constant<int, AGMM_BF16>());
+    pairs(std::integral_constant<int, AGMM_BF16>());
   return hipGetLastError();
 }
 
