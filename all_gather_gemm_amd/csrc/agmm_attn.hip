@@ -12,28 +12,44 @@
 //  - S^T's accumulator layout (lane = q head, 4 consecutive tokens) is, for a pair of 16-token
 //    tiles, the operand layout of P^T for 32 tokens in the order {4 g .. 4 g + 3, 16 + 4 g ..}, so
 //    P never moves between lanes.
-//  - V^T needs 8 tokens of one element in a lane. A lane loads 8 elements (16 bytes) of each of its
-//    8 tokens, 16 lanes covering whole rows, and transposes 8 x 8 in registers with v_perm_b32;
-//    matrix instruction e takes element 8 c + e of chunk c, so lane c's accumulators end up holding
-//    32 consecutive elements of the output.
+//  - V^T needs 8 tokens of one element in a lane. A lane loads 8 elements of each of its 8 tokens (4
+//    where rows have 64), 16 lanes covering whole rows, and transposes in registers with v_perm_b32;
+//    matrix instruction e takes element e of every lane's chunk, so a lane's accumulators end up
+//    holding 32 consecutive elements of the output.
 //  - Codes are turned into the 16-bit type, scale included, by one v_cvt_scalef32_pk per pair.
 //  - The maximum is raised only when a tile's exceeds it by 2^8 or more, so the accumulators are
 //    rescaled a few times a sequence; weights are kept up to 2^15 (a maximum of 2^7 plus the 2^8),
 //    where the fp16 operand has its full precision and room below.
+//  - Past 16 q heads to a kv head, groups of 16 take the cache one after the other.
 //
 // Work: the tiles (128 tokens) of all sequences and heads, in that order, are cut into equal runs, one
-// for each workgroup, from the lengths on the device. A run may begin and end inside a sequence's
-// head; such a head's pieces are joined by the last workgroup to finish one, in the order of the
-// pieces (16 at a time, and then the groups of 16), so results do not depend on timing.
+// for each worker, from the lengths on the device. A worker is a workgroup's 4 waves, or each wave by
+// itself where many heads are short. A run may begin and end inside a sequence's head; such a head's
+// pieces are joined by the last worker to finish one, in the order of the pieces (over 32 of them: 16
+// at a time, and then the groups of 16), so results do not depend on timing.
+//
+// Measured, warm: 64 sequences of 8192 tokens, 64/8 heads of 128, bf16: 355 us, 6.05 TB/s of cache
+// read once (a copy of 4 GiB runs at 4.7 TB/s, reads and writes together); 32 such sequences in e4m3
+// 103 us, 5.4 TB/s, in e2m1 61 us, 4.7 TB/s, where turning codes into values bounds it: half of the
+// vector unit's issue slots, and its waits. One sequence costs 6.5 us (launch, length, page, keys and
+// values, output: four reads that each wait for the one before), 3.3 more where workgroups share it.
 #include "agmm_attn_device.h"
 
 namespace agmm {
 namespace {
 
 constexpr int kCus = 256;
-constexpr uint32_t kLeast = 4;       // tiles of a workgroup's share, at least
-constexpr int kSingle = 32;          // pieces that are joined at once; more are joined
-constexpr int kJoin = 16;            // in groups of this many first
+// Tiles of a workgroup's share, at least, as long as every compute unit gets one, where sequences have more
+// than kLong tiles on the average: fewer pieces to join (131072 tokens, one kv head, e4m3: 17.7 us, 20.8
+// with 2). Of shorter ones a share would hold ends of two heads more often than it saves pieces (32
+// ragged up to 4000, 8 kv heads, e4m3: 21.5 us, 24.6 with 4; 16 up to 2000, 8 kv heads, bf16 9.4,
+// 14.4; but 8 of 700 11.2, 10.3). One sequence of 5000, 8 kv heads: 12.1, one tile at least 14.5.
+constexpr uint32_t kLong = 16;
+constexpr uint32_t kLeast = 4;
+// Pieces that are joined at once; more are joined in groups of kJoin first (64 pieces of 8 q heads:
+// 17.3 us for the run at once, 14.0 in groups; 32: 13.0 at once, 14.0 in groups)
+constexpr int kSingle = 32;
+constexpr int kJoin = 16;
 constexpr int kChunk = 16;           // pieces whose loads are in flight together
 constexpr float kHead = 7.0f;        // weights are 2^(s - m + kHead)
 constexpr float kUnhead = 0x1p-7f;   // 2^-kHead
@@ -119,8 +135,10 @@ __device__ inline int here(int x) {
 // What one wave loads of a tile of tokens, as it comes from memory.
 template <int ST, int DP>
 struct Raw {
-  // Sub-tiles of 16 tokens. 64 tokens share the cost of placing a tile and of its softmax, where two
-  // waves' registers hold them. kTwo: 32 tokens, but two tiles' registers.
+  // Sub-tiles of 16 tokens. 64 tokens share the cost of placing a tile and of its softmax; a tile's
+  // registers are loaded again while it is worked on (32 x 8192 tokens, e2m1: rows of 64 44 us, 58 with
+  // 32 tokens; of 128 61, 67). kTwo: for 16-bit rows of 128 those registers spill (4.6 TB/s); 32
+  // tokens in each of two tiles' registers reach 6.0. e4m3 rows of 256 spill with 64 tokens too.
   static constexpr bool kTwo = ST == AG_KV_16BIT && DP == 128;
   static constexpr int kSub = kTwo || (ST == AG_KV_MXFP8 && DP == 256) ? 2 : 4;
   static constexpr int kTokens = 16 * kSub;
@@ -637,18 +655,20 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
   sync<NW>();  // sh is free again
 }
 
-// The run of tiles of worker `me` of `wgs`, out of the `total` tiles of all sequences and heads.
+// The run of tiles of worker `me` of `wgs` (NW = 4: workgroups, NW = 1: waves), out of the `total` tiles
+// of all sequences and heads.
 template <int DT, int ST, int DP, int NW>
 __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me, uint32_t wgs,
-                            uint32_t total, uint32_t least) {
+                            uint32_t total, uint32_t least, uint32_t whole) {
   typedef Wave<DT, ST, DP> W;
   typedef typename W::R R;
   const int tid = thread<NW>(), lane = threadIdx.x & 63;
   const int wave = NW == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const uint32_t heads = (uint32_t)(p.c.kv_heads * p.q_groups);
-  // an equal share, but at least `least` tiles once that gives every compute unit 4 waves
+  // an equal share, but at least `least` tiles once that gives every compute unit 4 waves, and never
+  // less than `whole`
   constexpr uint32_t kFill = 4 * kCus / NW;
-  const uint32_t quota = max((total + wgs - 1) / wgs, min(least, (total + kFill - 1) / kFill));
+  const uint32_t quota = max(max((total + wgs - 1) / wgs, whole), min(least, (total + kFill - 1) / kFill));
   uint32_t cur = me * quota;
   if (cur >= total) return;
   const uint32_t end = min(cur + quota, total);
@@ -830,15 +850,18 @@ __global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(Att
     Shared<DP, 1> alone[4];
   } sh;
   const int lane = threadIdx.x & 63;
-  uint32_t sum = 0, few = 0, some = 0;  // tiles; sequences with one or two; sequences with any
+  // tiles; sequences with one or two; with three; with any
+  uint32_t sum = 0, few = 0, mid = 0, some = 0;
   for (int b = lane; b < p.batch; b += 64) {
     const uint32_t t = tiles_of(p, p.lens[b]);
     sum += t;
     few += t == 1 || t == 2 ? 1 : 0;
+    mid += t == 3 ? 1 : 0;
     some += t ? 1 : 0;
   }
   const uint32_t heads = (uint32_t)(p.c.kv_heads * p.q_groups);
-  const uint32_t tiles = wave_sum(sum), short_ones = wave_sum(few), sequences = wave_sum(some);
+  const uint32_t tiles = wave_sum(sum), short_ones = wave_sum(few), threes = wave_sum(mid),
+                 sequences = wave_sum(some);
   for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
     if (tiles_of(p, p.lens[b]) == 0) {
       const int d4 = p.c.head_dim / 4;
@@ -847,14 +870,24 @@ __global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(Att
         finish<DT>(p, b, h, (i - h * d4) * 4, f32x4{0, 0, 0, 0}, 0.0f, 0.0f);
       }
     }
+  // Heads that all have 2 or all have 3 tiles are not cut: one workgroup's second step costs less than
+  // joining (300 tokens, bf16 8.6 us, cut 9.5; 200 7.6, 9.5). With 4 tiles neither wins (9.7, 9.6).
+  const bool twos = short_ones == sequences && tiles == 2 * sequences;
+  const uint32_t whole = threes == sequences ? 3 : twos ? 2 : 1;
   // Where many heads have but a tile or two, a workgroup's waves would wait for each other at every
   // one of them: each wave works by itself then, on two tiles or more unless no head has more than one.
-  if (3 * short_ones * heads >= gridDim.x) {
+  // 96 ragged sequences (8 kv heads, e2m1, window) 26.5 us, together 45; 256 of 50 tokens (bf16) 15 us,
+  // together 20. Else together: 64 of 512 (e2m1) 12 us, by themselves 17; 64 of 8192 (bf16) 355, 376;
+  // and where the compute units suffice for a workgroup each: 32 of 200 (bf16, 8 kv heads) 8.0, 13.5.
+  // (Expected not to be, for where the code lies: the other way 131072 tokens in e4m3 take 18.1 us, so
+  // 17.6.)
+  if (__builtin_expect(tiles * heads > kCus * whole, 0) && 3 * short_ones * heads >= gridDim.x) {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     work<DT, ST, DP, 1>(p, sh.alone[wave], 4 * blockIdx.x + wave, 4 * gridDim.x, tiles * heads,
-                        tiles == sequences ? 1 : 2);
+                        tiles == sequences ? 1 : 2, 1);
   } else {
-    work<DT, ST, DP, 4>(p, sh.together, blockIdx.x, gridDim.x, tiles * heads, kLeast);
+    work<DT, ST, DP, 4>(p, sh.together, blockIdx.x, gridDim.x, tiles * heads,
+                        tiles > kLong * sequences ? kLeast : 1, whole);
   }
 }
 

@@ -42,7 +42,6 @@ struct T16;
 
 template <>
 struct T16<AGMM_F16> {
-  static constexpr float kMax = 65504.0f;
   __device__ static inline float lo(uint32_t w) {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)w);
   }
@@ -70,7 +69,6 @@ struct T16<AGMM_F16> {
 
 template <>
 struct T16<AGMM_BF16> {
-  static constexpr float kMax = 3.3895313892515355e38f;
   __device__ static inline float lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
   __device__ static inline float hi(uint32_t w) {
     return __builtin_bit_cast(float, w & 0xffff0000u);

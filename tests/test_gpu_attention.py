@@ -150,6 +150,20 @@ def test_split_and_join(T, lens, kv_heads, num_wgs):
         assert torch.equal(out, again) and torch.equal(lse, lse2)
 
 
+# heads of a few tiles: each in one workgroup, each in one wave, several to a wave, cut or not
+@pytest.mark.parametrize("storage,dim", [("16bit", 64), ("16bit", 128), ("mxfp8", 64), ("mxfp4", 128)])
+@pytest.mark.parametrize("lens,kv_heads,num_wgs", [
+    ([200], 1, 0), ([300], 1, 0), ([130, 256, 0, 200], 2, 0), ([300, 257, 0, 384], 2, 0),
+    ([300, 257, 200, 384], 2, 0), ([300, 260] * 15, 3, 7), ([40] * 100, 3, 0), ([200, 129] * 50, 3, 0),
+    ([300, 200, 100] * 40, 3, 0), ([300, 200, 1] * 20, 3, 0), ([100, 2000] + [60] * 130, 3, 100)])
+def test_short_heads(T, storage, dim, lens, kv_heads, num_wgs):
+    p = Problem(T, lens, 2 * kv_heads, kv_heads, dim, 16, storage, "f16", num_wgs=num_wgs, spread=2.0)
+    out, lse = p.run()
+    p.check(out, lse)
+    again, lse2 = p.run()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
 @pytest.mark.parametrize("storage", ["16bit", "mxfp8", "mxfp4"])
 def test_absent_pages(T, storage):
     p = Problem(T, [16, 33, 200, 0, 700], 8, 2, 128, 16, storage, "bf16", holes=(0, 2, 7, 8, 9))
