@@ -151,10 +151,10 @@ int ag_kv_read(const ag_kv_cache* cache, const int64_t* slots, int64_t tokens, v
  *     s_t = scale * q . k_t, or soft_cap * tanh(scale * q . k_t / soft_cap)
  *     out = sum_t exp(s_t) v_t / sum_t exp(s_t),   lse = ln sum_t exp(s_t)
  * No token to attend to (a length of 0, every page absent): out = 0, lse = -infinity.
- * The sequences' tokens are shared out evenly over the workgroups on the device (lengths are read
- * there), so one long sequence fills the chip as many short ones do; where workgroups share a
- * sequence's head, the last of them to finish joins their partial results in a fixed order.
- * Results do not depend on timing. */
+ * The sequences' tokens are shared out evenly over the workgroups, or their waves, on the device
+ * (lengths are read there), so one long sequence fills the chip as many short ones do; where several
+ * share a sequence's head, the last of them to finish joins their partial results in a fixed
+ * order. Results do not depend on timing. */
 typedef struct ag_attn_desc {
   int32_t dtype, storage;
   int32_t head_dim;          /* as in ag_kv_cache */
