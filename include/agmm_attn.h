@@ -14,9 +14,9 @@
  * Types: q, k, v and the outputs share one 16-bit type (AGMM_F16 or AGMM_BF16); every sum, angle
  * and softmax statistic is held in 32 bits or more. Strides are counted in elements of the tensor
  * unless they say bytes; a head's values are always contiguous. Codes and threading are those of
- * agmm.h (ag_matmul_strerror and ag_matmul_last_hip_error serve these functions too). Nothing
- * here synchronizes the host, except ag_attn_destroy and ag_rope_destroy; every run may be
- * captured into a HIP graph and replayed.
+ * agmm.h (ag_matmul_strerror and ag_matmul_last_hip_error serve these functions too). The
+ * creates and destroys wait for the device; the runs, appends and reads do not, and may be captured
+ * into a HIP graph and replayed.
  */
 #ifndef AGMM_ATTN_H
 #define AGMM_ATTN_H
