@@ -126,6 +126,20 @@ __device__ inline float across_sum(float x) {
   return across(x, [](float a, float b) { return a + b; });
 }
 
+// cap * tanh(s / cap) of a product x = q . k, in base 2, to a few roundings of the score itself however
+// far the cap is from it. With u = s / cap: from |u| = 1/2 on as (e^2u - 1) / (e^2u + 1), where the
+// subtraction loses a bit at most; below, where it would lose them all, as s times the fifth convergent of
+// Lambert's continued fraction of tanh(u) / u, 1 / (1 + u^2 / (3 + u^2 / (5 + ...))), 1e-10 off there.
+// A NaN takes the latter.
+__device__ inline float capped(const AttnParams& p, float x) {
+  const float u = x * p.inv_cap, y = u * u;
+  const bool far = fabsf(u) >= 0.5f;
+  const float e = __builtin_amdgcn_exp2f(fminf(fabsf(u) * 2.88539008177792681f, 64.0f));
+  const float num = far ? e - 1.0f : fmaf(y, y + 105.0f, 945.0f);
+  const float den = far ? e + 1.0f : fmaf(y, fmaf(y, 15.0f, 420.0f), 945.0f);
+  return num * __builtin_amdgcn_rcpf(den) * (far ? copysignf(p.cap, u) : x * p.scale);
+}
+
 // Stops the compiler from moving what is computed from x out of a loop, into registers that the loop
 // needs for its loads.
 __device__ inline int here(int x) {
@@ -340,15 +354,12 @@ struct Wave {
   // is summed rescaled first where needed.
   __device__ inline void weights(const AttnParams& p, uint64_t there, f32x4 (&st)[R::kSub]) {
     float scale = p.scale;
-    if (p.cap != 0.0f) {  // cap * tanh x by tanh x = 1 - 2 / (e^2x + 1)
+    if (p.cap != 0.0f) {
       scale = 1.0f;
 #pragma unroll
       for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          st[t][j] = p.cap - 2.0f * p.cap *
-                                 __builtin_amdgcn_rcpf(
-                                     __builtin_amdgcn_exp2f(st[t][j] * p.inv_cap) + 1.0f);
+        for (int j = 0; j < 4; ++j) st[t][j] = capped(p, st[t][j]);
     }
     if (there != kAll) {
       const int g = here(threadIdx.x & 63) >> 4;

@@ -1,4 +1,5 @@
 // Host side of the C ABI declared in include/agmm_attn.h: validation, plans, launches.
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 #include <string.h>
@@ -530,8 +531,11 @@ int ag_attn_run(ag_attn_handle* h, const ag_kv_cache* cache, const void* q, int6
   const double log2e = 1.4426950408889634073599;
   const double scale = d.scale != 0.0f ? d.scale : 1.0 / sqrt((double)d.head_dim);
   p.scale = (float)(scale * log2e);
-  p.cap = (float)(d.soft_cap * log2e);
-  p.inv_cap = d.soft_cap != 0.0f ? (float)(2.0 * log2e * scale / d.soft_cap) : 0.0f;
+  // (finite and above 0 at the ends of the cap's range)
+  p.cap = (float)std::min(d.soft_cap * log2e, (double)FLT_MAX);
+  p.inv_cap = d.soft_cap != 0.0f ? (float)std::min(std::max(scale / d.soft_cap, (double)FLT_MIN),
+                                                   (double)FLT_MAX)
+                                 : 0.0f;
   const int64_t grid = std::min<int64_t>(h->num_wgs, std::max<int64_t>(1, tiles * heads * batch));
   ATTN_HIP(agmm::launch_attn(p, d.dtype, d.storage, (int)grid, (hipStream_t)hip_stream));
   return AGMM_OK;
