@@ -55,6 +55,7 @@ constexpr int kChunk = 16;           // pieces whose loads are in flight togethe
 constexpr float kHead = 7.0f;        // weights are 2^(s - m + kHead)
 constexpr float kUnhead = 0x1p-7f;   // 2^-kHead
 constexpr float kRaise = 8.0f;       // raise the maximum when a tile's is above it by this
+constexpr float kRounded = 0x1p16f;  // maxima from here on are taken from rounded scores
 
 // Partial results pass between workgroups that may sit on different XCDs, whose L2s are not coherent.
 // They are stored and loaded as relaxed atomics of agent scope, which write through and read past
@@ -106,6 +107,13 @@ __device__ inline int thread() {
 // keeps its own: it is 0, or NaN.
 __device__ inline float weight(float m, float top) {
   return m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+}
+
+// A product that is rounded by itself, in no multiply-add.
+__device__ inline float scaled(float x, float scale) {
+  float y = x * scale;
+  asm("" : "+v"(y));
+  return y;
 }
 
 // Sum or maximum over the 4 lane groups of 16 (lanes l, l ^ 16, l ^ 32, l ^ 48), by exchanges of rows
@@ -378,7 +386,7 @@ struct Wave {
 #pragma unroll
       for (int j = 0; j < 4; ++j) top = fmaxf(top, st[t][j]);
     top = across_max(top) * scale;
-    if (__any(top > m + kRaise)) {
+    if (__any(top - m > kRaise)) {
       const float raised = fmaxf(m, top);
       const float f = weight(m, raised);
 #pragma unroll
@@ -387,6 +395,16 @@ struct Wave {
         for (int w = 0; w < 4; ++w) acc[i][w] *= f;
       l *= f;
       m = raised;
+    }
+    // One multiply-add below takes the score from the exact product, m from a rounded one. Where an ulp
+    // of m is not small beside 1 the scores are rounded first as m was, or weights would be a power of 2
+    // too large or too small, and infinite or 0 from scores of 2^30 on.
+    if (__any(fabsf(m) >= kRounded)) {
+#pragma unroll
+      for (int t = 0; t < R::kSub; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) st[t][j] = scaled(st[t][j], scale);
+      scale = 1.0f;
     }
     const float ref = m == -INFINITY ? 0.0f : kHead - m;
 #pragma unroll

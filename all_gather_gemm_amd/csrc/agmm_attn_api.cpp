@@ -530,8 +530,8 @@ int ag_attn_run(ag_attn_handle* h, const ag_kv_cache* cache, const void* q, int6
   p.q_heads = d.q_heads;
   const double log2e = 1.4426950408889634073599;
   const double scale = d.scale != 0.0f ? d.scale : 1.0 / sqrt((double)d.head_dim);
-  p.scale = (float)(scale * log2e);
-  // (finite and above 0 at the ends of the cap's range)
+  // (finite, and the cap's above 0, at the ends of their ranges)
+  p.scale = (float)std::min(scale * log2e, (double)FLT_MAX);
   p.cap = (float)std::min(d.soft_cap * log2e, (double)FLT_MAX);
   p.inv_cap = d.soft_cap != 0.0f ? (float)std::min(std::max(scale / d.soft_cap, (double)FLT_MIN),
                                                    (double)FLT_MAX)

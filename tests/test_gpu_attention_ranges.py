@@ -61,3 +61,44 @@ def test_caps_of_infinite_and_nan_scores(T):
     refill(p, k=k)
     out, lse = p.run()
     assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
+@pytest.mark.parametrize("scale", [1e-44, 1e-30, 1e38, 3.4e38])
+def test_scales(T, scale):
+    """Scales at the ends of 32 bits: the softmax of zeros, and of zeros and one key that is far above
+    the others at the large scales and like them at the small ones."""
+    p = Problem(T, [1, 40, 300], 2, 1, 64, 16, "16bit", "bf16", scale=scale)
+    k = np.zeros_like(p.k)
+    p.q = torch.zeros_like(p.q)
+    p.q[..., 0] = 1.0
+    refill(p, k=k)
+    p.check(*p.run())
+    ends = np.cumsum(p.lens)
+    k[ends - 1, 0, 0] = 0.5
+    refill(p, k=k)
+    out = ref.f64(p.run()[0])
+    for b, (n, end) in enumerate(zip(p.lens, ends)):
+        want = p.v[end - 1, 0] if scale > 1 else p.v[end - n:end, 0].mean(0)
+        # half an ulp, and of an average of normal values the 16 bits of a weight
+        assert (np.abs(out[b] - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -14).all()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_large_scores(T, dtype):
+    """Scores of 2^20 to 2^32, where 32 bits hold them to no more than a whole number: the tokens with the
+    largest key share the weight, whatever the order, and the others get none."""
+    n, heads = 700, 24
+    p = Problem(T, [n], heads, 1, 64, 16, "16bit", dtype, scale=1.0)
+    p.q = torch.zeros_like(p.q)
+    p.q[0, :, 0] = torch.exp2(torch.arange(heads) / 2 + 4).to(p.q.dtype)     # 2^4 to 2^15.5
+    # (a step between keys is 256: 2^12 in a score)
+    k = np.zeros_like(p.k)
+    k[:, 0, 0] = 256.0 * np.random.default_rng(1).integers(-200, 200, n)
+    for top in ([5], [650], [3, 70, 699]):
+        k[top, 0, 0] = 256.0 * 220
+        refill(p, k=k)
+        out, lse = p.run()
+        want, s = p.v[top, 0].mean(0), ref.f64(p.q)[0, :, 0] * 256 * 220 + math.log(len(top))
+        assert (np.abs(ref.f64(out)[0] - want) <= ref.HALF_ULP[dtype] * np.abs(want) + 2.0 ** -10).all()
+        assert (np.abs(ref.f64(lse)[0] - s) <= 2.0 ** -21 * (1 + np.abs(s))).all()
+        k[top, 0, 0] = 0.0
