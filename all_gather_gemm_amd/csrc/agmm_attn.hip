@@ -18,8 +18,10 @@
 //    holding 32 consecutive elements of the output.
 //  - Codes are turned into the 16-bit type, scale included, by one v_cvt_scalef32_pk per pair.
 //  - The maximum is raised only when a tile's exceeds it by 2^8 or more, so the accumulators are
-//    rescaled a few times a sequence; weights are kept up to 2^15 (a maximum of 2^7 plus the 2^8),
-//    where the fp16 operand has its full precision and room below.
+//    rescaled a few times a sequence. Weights are 2^(s - m + head). fp16: head 7, so up to 2^15, where the
+//    operand has its full precision and room below. bf16, whose values reach to the end of 32 bits:
+//    low enough that all of a sequence's weights add up to 1 at most, and with them no sum exceeds the
+//    largest value, which 32 bits hold.
 //  - Past 16 q heads to a kv head, groups of 16 take the cache one after the other.
 //
 // Work: the tiles (128 tokens) of all sequences and heads, in that order, are cut into equal runs, one
@@ -52,9 +54,7 @@ constexpr uint32_t kLeast = 4;
 constexpr int kSingle = 32;
 constexpr int kJoin = 16;
 constexpr int kChunk = 16;           // pieces whose loads are in flight together
-constexpr float kHead = 7.0f;        // weights are 2^(s - m + kHead)
-constexpr float kUnhead = 0x1p-7f;   // 2^-kHead
-constexpr float kRaise = 8.0f;       // raise the maximum when a tile's is above it by this
+constexpr int kRaise = 8;            // raise the maximum when a tile's is above it by this
 constexpr float kRounded = 0x1p16f;  // maxima from here on are taken from rounded scores
 
 // Partial results pass between workgroups that may sit on different XCDs, whose L2s are not coherent.
@@ -146,6 +146,14 @@ __device__ inline float capped(const AttnParams& p, float x) {
   const float num = far ? e - 1.0f : fmaf(y, y + 105.0f, 945.0f);
   const float den = far ? e + 1.0f : fmaf(y, fmaf(y, 15.0f, 420.0f), 945.0f);
   return num * __builtin_amdgcn_rcpf(den) * (far ? copysignf(p.cap, u) : x * p.scale);
+}
+
+// The head of a sequence's weights by the tokens that are attended to. (The other end, bf16: the
+// products of values below 2^-118, and 2^-101 of 131072 tokens, are subnormal and may lose bits.)
+template <int DT>
+__device__ inline int head_of(int64_t tokens) {
+  if (DT == AGMM_F16) return 7;
+  return -kRaise - (tokens > 1 ? 32 - __builtin_clz((uint32_t)(tokens - 1)) : 0);
 }
 
 // Stops the compiler from moving what is computed from x out of a loop, into registers that the loop
@@ -358,9 +366,9 @@ struct Wave {
         st[t] = T16<DT>::mfma(key(r, t, i, g, kw[t]), q[i], st[t]);
   }
 
-  // Scores to weights: st becomes 2^(s - m + kHead), s the scores in base 2, with m raised and what
-  // is summed rescaled first where needed.
-  __device__ inline void weights(const AttnParams& p, uint64_t there, f32x4 (&st)[R::kSub]) {
+  // Scores to weights: st becomes 2^(s - m + up), s the scores in base 2, with m raised and what is
+  // summed rescaled first where needed.
+  __device__ inline void weights(const AttnParams& p, uint64_t there, int up, f32x4 (&st)[R::kSub]) {
     float scale = p.scale;
     if (p.cap != 0.0f) {
       scale = 1.0f;
@@ -386,7 +394,7 @@ struct Wave {
 #pragma unroll
       for (int j = 0; j < 4; ++j) top = fmaxf(top, st[t][j]);
     top = across_max(top) * scale;
-    if (__any(top - m > kRaise)) {
+    if (__any(top - m > (float)kRaise)) {
       const float raised = fmaxf(m, top);
       const float f = weight(m, raised);
 #pragma unroll
@@ -406,7 +414,7 @@ struct Wave {
         for (int j = 0; j < 4; ++j) st[t][j] = scaled(st[t][j], scale);
       scale = 1.0f;
     }
-    const float ref = m == -INFINITY ? 0.0f : kHead - m;
+    const float ref = m == -INFINITY ? 0.0f : (float)up - m;
 #pragma unroll
     for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
@@ -430,11 +438,12 @@ struct Wave {
           hi[j] = T16<DT>::pack(a, b);  // 11 bits of a weight
         } else {
           // bf16 weights keep 8 bits: what cutting them there leaves goes into a second operand, 16
-          // in all. That part is kept above 0 (by 2^-126): 0 times an infinite value is NaN.
+          // in all. That part is kept above 0 (by 2^-126, or the weight): 0 times an infinite value is
+          // NaN.
           const uint32_t ab = __builtin_bit_cast(uint32_t, a), bb = __builtin_bit_cast(uint32_t, b);
           hi[j] = __builtin_amdgcn_perm(bb, ab, 0x07060302u);
-          lo[j] = T16<DT>::pack(fmaxf(a - T16<DT>::hi(ab), 0x1p-126f),
-                                fmaxf(b - T16<DT>::hi(bb), 0x1p-126f));
+          lo[j] = T16<DT>::pack(__builtin_amdgcn_fmed3f(a - T16<DT>::hi(ab), 0x1p-126f, a),
+                                __builtin_amdgcn_fmed3f(b - T16<DT>::hi(bb), 0x1p-126f, b));
         }
       }
 #pragma unroll
@@ -531,7 +540,7 @@ __device__ inline uint32_t wave_sum(uint32_t x) {
 // Elements e .. e + 3 of a row: o over the row's sum l, and the row's lse with element 0.
 template <int DT>
 __device__ inline void finish(const AttnParams& p, int64_t b, int head, int e, f32x4 o, float m,
-                              float l) {
+                              float l, int up) {
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // 0: nothing was attended to
   typedef u32x2 u32x2_any __attribute__((aligned(2)));
   *reinterpret_cast<u32x2_any*>(p.out + b * p.o_batch + (int64_t)head * p.o_head + e) =
@@ -539,12 +548,13 @@ __device__ inline void finish(const AttnParams& p, int64_t b, int head, int e, f
   if (e == 0 && p.lse)
     p.lse[b * p.q_heads + head] =
         l == 0.0f ? -INFINITY
-                  : (m + __builtin_amdgcn_logf(l * kUnhead)) * 0.69314718055994531f;
+                  : (m + __builtin_amdgcn_logf(ldexpf(l, -up))) * 0.69314718055994531f;
 }
 
 // A head's part that a workgroup does not have all of.
 struct Piece {
   int b, head0, n;          // sequence, first q head, q heads
+  int up;                   // head of the sequence's weights
   uint32_t begin, pieces;   // workgroup that has the head's first tile; workgroups that have any
 };
 
@@ -593,7 +603,7 @@ __device__ inline void join(const AttnParams& p, Shared<DP, NW>& sh, const Piece
       m = top;
     }
     if (final) {
-      finish<DT>(p, h.b, h.head0 + row, e, o, m, l);
+      finish<DT>(p, h.b, h.head0 + row, e, o, m, l, h.up);
     } else {
 #pragma unroll
       for (int w = 0; w < 4; ++w) sh.acc[0][row][e + w] = o[w];
@@ -676,7 +686,7 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
       for (int k = 0; k < 4; ++k) o[k] += sh.acc[i][row][e + k];
     }
     if (whole) {
-      finish<DT>(p, h.b, h.head0 + row, e, o, rm, rl);
+      finish<DT>(p, h.b, h.head0 + row, e, o, rm, rl, h.up);
     } else {
       store_shared(slot + row * DP + e, o);
       if (e == 0) store_shared2(slot + p.rows * DP + 2 * row, rm, rl);
@@ -735,6 +745,7 @@ __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me
     h.b = b;
     h.head0 = kv * p.group + 16 * group;
     h.n = min(16, p.group - 16 * group);
+    h.up = head_of<DT>(seq.end - seq.first);
     h.begin = start / quota;
     h.pieces = (start + tiles - 1) / quota - h.begin + 1;
 
@@ -782,7 +793,7 @@ __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me
           load(after);
           f32x4 st[R::kSub];
           w.scores(now, p, sc[0], st);
-          w.weights(p, there, st);
+          w.weights(p, there, h.up, st);
           w.values(now, there, sc[1], st);
           there = next;
         };
@@ -806,7 +817,7 @@ __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me
           const uint64_t next = place(base, page);
           page = page_of(base + kStep);
           W::load_k(r, p, at, hoff, shoff);
-          w.weights(p, there, st);
+          w.weights(p, there, h.up, st);
           w.values(r, there, sc[1], st);
           if (base >= t1) break;
           W::load_v(r, p, at, hoff, shoff);
@@ -897,7 +908,7 @@ __global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(Att
       const int d4 = p.c.head_dim / 4;
       for (int i = threadIdx.x; i < p.q_heads * d4; i += kThreads) {
         const int h = i / d4;
-        finish<DT>(p, b, h, (i - h * d4) * 4, f32x4{0, 0, 0, 0}, 0.0f, 0.0f);
+        finish<DT>(p, b, h, (i - h * d4) * 4, f32x4{0, 0, 0, 0}, 0.0f, 0.0f, 0);
       }
     }
   // Heads that all have 2 or all have 3 tiles are not cut: one workgroup's second step costs less than

@@ -102,3 +102,46 @@ def test_large_scores(T, dtype):
         assert (np.abs(ref.f64(out)[0] - want) <= ref.HALF_ULP[dtype] * np.abs(want) + 2.0 ** -10).all()
         assert (np.abs(ref.f64(lse)[0] - s) <= 2.0 ** -21 * (1 + np.abs(s))).all()
         k[top, 0, 0] = 0.0
+
+
+LENS = [1, 2, 0, 300, 9000]
+
+
+@pytest.mark.parametrize("storage", ["16bit", "mxfp8"])
+@pytest.mark.parametrize("spread", [1.0, 6.0])
+@pytest.mark.parametrize("size", [2.0 ** -100, 1e30, 2.0 ** 126.9])
+def test_bf16_values_of_every_size(T, storage, spread, size):
+    """Averages of finite values are finite: no sum on the way exceeds 32 bits. (Of values of one sign,
+    so that the average is as large as they are.)"""
+    p = Problem(T, LENS, 4, 2, 64, 16, storage, "bf16", spread=spread)
+    v = size * (1.0 + np.random.default_rng(2).random(p.v.shape))
+    refill(p, v=v)
+    out, lse = p.run()
+    assert torch.isfinite(out).all()
+    p.check(out, lse)
+
+
+def test_bf16_largest_values(T):
+    """The largest value in every token comes out as it went in."""
+    p = Problem(T, LENS, 4, 2, 64, 16, "16bit", "bf16")
+    most = float(torch.finfo(torch.bfloat16).max)
+    refill(p, v=np.full_like(p.v, -most))
+    out, _ = p.run()
+    assert all((out[b] == (-most if n else 0.0)).all() for b, n in enumerate(p.lens))
+
+
+def test_no_weight_is_none(T):
+    """Tokens whose score is minus infinity get no weight at all, however large their values are."""
+    for dtype in ("bf16", "f16"):
+        n = 200
+        p = Problem(T, [n], 2, 1, 64, 16, "16bit", dtype)
+        p.q = torch.zeros_like(p.q)
+        p.q[..., 0] = 1.0
+        most = float(torch.finfo(ref.TORCH[dtype]).max)
+        k, v = p.k.copy(), p.v * 1e-3
+        k[50:, 0, 0] = -math.inf
+        v[50:] = most
+        refill(p, k=k, v=v)
+        out, lse = p.run()
+        p.lens, p.k, p.v = [50], p.k[:50], p.v[:50]
+        p.check(out, lse)
