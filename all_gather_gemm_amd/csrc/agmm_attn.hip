@@ -17,9 +17,10 @@
 //    matrix instruction e takes element e of every lane's chunk, so a lane's accumulators end up
 //    holding 32 consecutive elements of the output.
 //  - Codes are turned into the 16-bit type, scale included, by one v_cvt_scalef32_pk per pair.
-//  - The maximum is raised only when a tile's exceeds it by 2^8 or more, so the accumulators are
-//    rescaled a few times a sequence. Weights are 2^(s - m + head). fp16: head 7, so up to 2^15, where the
-//    operand has its full precision and room below. bf16, whose values reach to the end of 32 bits:
+//  - Weights enter the product in two parts of the 16-bit type, 22 bits (fp16) or 16 (bf16) in all.
+//  - The maximum is raised only when a tile's exceeds it by 2^4 or more, so the accumulators are
+//    rescaled a few times a sequence. Weights are 2^(s - m + head). fp16: head 11, so up to 2^15, where
+//    both parts have their full precision and room below. bf16, whose values reach to the end of 32 bits:
 //    low enough that all of a sequence's weights add up to 1 at most, and with them no sum exceeds the
 //    largest value, which 32 bits hold.
 //  - Past 16 q heads to a kv head, groups of 16 take the cache one after the other.
@@ -54,7 +55,7 @@ constexpr uint32_t kLeast = 4;
 constexpr int kSingle = 32;
 constexpr int kJoin = 16;
 constexpr int kChunk = 16;           // pieces whose loads are in flight together
-constexpr int kRaise = 8;            // raise the maximum when a tile's is above it by this
+constexpr int kRaise = 4;            // raise the maximum when a tile's is above it by this
 constexpr float kRounded = 0x1p16f;  // maxima from here on are taken from rounded scores
 
 // Partial results pass between workgroups that may sit on different XCDs, whose L2s are not coherent.
@@ -152,7 +153,7 @@ __device__ inline float capped(const AttnParams& p, float x) {
 // products of values below 2^-118, and 2^-101 of 131072 tokens, are subnormal and may lose bits.)
 template <int DT>
 __device__ inline int head_of(int64_t tokens) {
-  if (DT == AGMM_F16) return 7;
+  if (DT == AGMM_F16) return 11;
   return -kRaise - (tokens > 1 ? 32 - __builtin_clz((uint32_t)(tokens - 1)) : 0);
 }
 
@@ -433,18 +434,9 @@ struct Wave {
       u32x4 hi, lo;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float a = st[h + j / 2][2 * j % 4], b = st[h + j / 2][2 * j % 4 + 1];
-        if (DT == AGMM_F16) {
-          hi[j] = T16<DT>::pack(a, b);  // 11 bits of a weight
-        } else {
-          // bf16 weights keep 8 bits: what cutting them there leaves goes into a second operand, 16
-          // in all. That part is kept above 0 (by 2^-126, or the weight): 0 times an infinite value is
-          // NaN.
-          const uint32_t ab = __builtin_bit_cast(uint32_t, a), bb = __builtin_bit_cast(uint32_t, b);
-          hi[j] = __builtin_amdgcn_perm(bb, ab, 0x07060302u);
-          lo[j] = T16<DT>::pack(__builtin_amdgcn_fmed3f(a - T16<DT>::hi(ab), 0x1p-126f, a),
-                                __builtin_amdgcn_fmed3f(b - T16<DT>::hi(bb), 0x1p-126f, b));
-        }
+        const u32x2 w = T16<DT>::split(st[h + j / 2][2 * j % 4], st[h + j / 2][2 * j % 4 + 1]);
+        hi[j] = w[0];
+        lo[j] = w[1];
       }
 #pragma unroll
       for (int c = 0; c < R::kChunks; ++c) {
@@ -494,7 +486,7 @@ struct Wave {
                                          e % 2 ? 0x07060302u : 0x05040100u);
           f32x4& o = acc[R::kElems * c + e];
           o = T16<DT>::mfma(a, hi, o);
-          if (DT == AGMM_BF16) o = T16<DT>::mfma(a, lo, o);
+          o = T16<DT>::mfma(a, lo, o);
         }
       }
     }

@@ -37,6 +37,11 @@ __device__ inline u32x4 load16(const uint16_t* p) {
 __device__ inline void store16(uint16_t* p, u32x4 v) { *reinterpret_cast<u32x4_any*>(p) = v; }
 
 // The 16-bit types: the values of a packed pair, and two floats rounded (RNE) to a packed pair.
+//
+// split: two floats >= 0 as a pair cut to the type and a pair of what that leaves, 22 bits (fp16) or 16
+// (bf16) of each together. What is left is kept above 0 (at the type's least power of 2 that matrix
+// instructions take, or the number itself if that is less): as a factor of an infinite value 0 would
+// make the sum of the two products NaN.
 template <int DT>
 struct T16;
 
@@ -51,6 +56,11 @@ struct T16<AGMM_F16> {
     v.x = (_Float16)a;
     v.y = (_Float16)b;
     return __builtin_bit_cast(uint32_t, v);
+  }
+  __device__ static inline u32x2 split(float a, float b) {
+    const uint32_t cut = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(a, b));
+    return u32x2{cut, pack(__builtin_amdgcn_fmed3f(a - lo(cut), 0x1p-24f, a),
+                           __builtin_amdgcn_fmed3f(b - hi(cut), 0x1p-24f, b))};
   }
   __device__ static inline f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, a),
@@ -78,6 +88,12 @@ struct T16<AGMM_BF16> {
     v.x = (__bf16)a;
     v.y = (__bf16)b;
     return __builtin_bit_cast(uint32_t, v);
+  }
+  __device__ static inline u32x2 split(float a, float b) {
+    const uint32_t cut = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, b),
+                                               __builtin_bit_cast(uint32_t, a), 0x07060302u);
+    return u32x2{cut, pack(__builtin_amdgcn_fmed3f(a - lo(cut), 0x1p-126f, a),
+                           __builtin_amdgcn_fmed3f(b - hi(cut), 0x1p-126f, b))};
   }
   __device__ static inline f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8_t, a),

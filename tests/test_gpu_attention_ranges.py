@@ -145,3 +145,39 @@ def test_no_weight_is_none(T):
         out, lse = p.run()
         p.lens, p.k, p.v = [50], p.k[:50], p.v[:50]
         p.check(out, lse)
+
+
+@pytest.mark.parametrize("storage,dim", [("16bit", 8), ("16bit", 256), ("mxfp8", 32), ("mxfp4", 64)])
+@pytest.mark.parametrize("lens", [[2], [64, 1000]])
+def test_f16_weights_in_two_parts(T, storage, dim, lens):
+    """Values of one magnitude and alternating signs, weights almost alike: the result is a small part of
+    A = sum p |v| and shows what the weights lose in the product. 22 bits of a weight leave 2^-22 of A and
+    the sums 2^-18 as elsewhere; 11 bits would leave up to 2^-12."""
+    p = Problem(T, lens, 4, 1, dim, 16, storage, "f16", scale=2.0 ** -10)
+    v = np.ones_like(p.v)
+    v[1::2] = -1.0
+    refill(p, v=v)
+    q, out = ref.f64(p.q), ref.f64(p.run()[0])
+    at = 0
+    for b, n in enumerate(lens):
+        o, _, a, w = ref.attention(q[b], p.k[at:at + n], p.v[at:at + n], p.scale)
+        at += n
+        err = (dim + 8) * 2.0 ** -24 * w[:, None]
+        tol = ref.HALF_ULP["f16"] * np.abs(o) + a * (2 * err + 2.0 ** -22 + 2.0 ** -18) + ref.TINY["f16"]
+        assert (np.abs(out[b] - o) <= tol).all(), (np.abs(out[b] - o) / tol).max()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("keys", ["alike", "random"])
+def test_infinite_values_of_any_weight(T, dtype, keys):
+    """An infinite value makes its element infinite and no other, also where its weight is a power of 2
+    and the second part has nothing of it."""
+    n, dim = 300, 64
+    p = Problem(T, [n], 2, 1, dim, 16, "16bit", dtype)
+    k, v = (np.zeros_like(p.k) if keys == "alike" else p.k), p.v.copy()
+    v[7, 0, 3], v[250, 0, 9] = math.inf, -math.inf
+    refill(p, k=k, v=v)
+    out, _ = p.run()
+    assert torch.isposinf(out[0, :, 3]).all() and torch.isneginf(out[0, :, 9]).all()
+    rest = [e for e in range(dim) if e not in (3, 9)]
+    assert torch.isfinite(out[0][:, rest]).all()
