@@ -136,17 +136,24 @@ __device__ inline float across_sum(float x) {
 }
 
 // cap * tanh(s / cap) of a product x = q . k, in base 2, to a few roundings of the score itself however
-// far the cap is from it. With u = s / cap: from |u| = 1/2 on as (e^2u - 1) / (e^2u + 1), where the
-// subtraction loses a bit at most; below, where it would lose them all, as s times the fifth convergent of
-// Lambert's continued fraction of tanh(u) / u, 1 / (1 + u^2 / (3 + u^2 / (5 + ...))), 1e-10 off there.
-// A NaN takes the latter.
+// far the cap is from it. With u = s / cap: from |u| = 1/4 on as (e^2u - 1) / (e^2u + 1), where the
+// subtraction loses two bits at most; below, where it would lose them all, as s times the series of
+// tanh(u) / u, whose first term left out is 8e-9 there. ALL: no lane has a |u| from 1/4 on (or NaN, which
+// the series keeps).
+constexpr float kFar = 0.25f;
+template <bool ALL>
 __device__ inline float capped(const AttnParams& p, float x) {
   const float u = x * p.inv_cap, y = u * u;
-  const bool far = fabsf(u) >= 0.5f;
-  const float e = __builtin_amdgcn_exp2f(fminf(fabsf(u) * 2.88539008177792681f, 64.0f));
-  const float num = far ? e - 1.0f : fmaf(y, y + 105.0f, 945.0f);
-  const float den = far ? e + 1.0f : fmaf(y, fmaf(y, 15.0f, 420.0f), 945.0f);
-  return num * __builtin_amdgcn_rcpf(den) * (far ? copysignf(p.cap, u) : x * p.scale);
+  float r = fmaf(y, 62.0f / 2835.0f, -17.0f / 315.0f);
+  r = fmaf(y, r, 2.0f / 15.0f);
+  r = fmaf(y, r, -1.0f / 3.0f);
+  r = fmaf(y, r, 1.0f) * (x * p.scale);
+  if constexpr (!ALL) {
+    const float e = __builtin_amdgcn_exp2f(fminf(fabsf(u) * 2.88539008177792681f, 64.0f));
+    const float far = (e - 1.0f) * __builtin_amdgcn_rcpf(e + 1.0f) * copysignf(p.cap, u);
+    r = fabsf(u) >= kFar ? far : r;
+  }
+  return r;
 }
 
 // The head of a sequence's weights by the tokens that are attended to. (The other end, bf16: the
@@ -372,11 +379,24 @@ struct Wave {
   __device__ inline void weights(const AttnParams& p, uint64_t there, int up, f32x4 (&st)[R::kSub]) {
     float scale = p.scale;
     if (p.cap != 0.0f) {
+      // most scores are far below the cap: one branch for the wave leaves the exponential out
       scale = 1.0f;
+      float most = 0.0f;
 #pragma unroll
       for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) st[t][j] = capped(p, st[t][j]);
+        for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(st[t][j]));
+      if (__any(most * p.inv_cap >= kFar)) {
+#pragma unroll
+        for (int t = 0; t < R::kSub; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) st[t][j] = capped<false>(p, st[t][j]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < R::kSub; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) st[t][j] = capped<true>(p, st[t][j]);
+      }
     }
     if (there != kAll) {
       const int g = here(threadIdx.x & 63) >> 4;
