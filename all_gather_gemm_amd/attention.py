@@ -266,7 +266,8 @@ class PagedCache:
 
     def append(self, k, v, slots, stream=None):
         """Writes k and v [tokens, kv_heads, head_dim] to slots [tokens] (int64; page * page_size +
-        row; a slot out of range leaves its token out)."""
+        row; a slot out of range leaves its token out, one that two tokens share leaves its row
+        undefined)."""
         tokens = slots.shape[0]
         shape, td, device = (tokens, self.kv_heads, self.head_dim), self.torch_dtype, self.device
         _tensor(k, "k", td, shape, device)

@@ -122,7 +122,8 @@ typedef struct ag_kv_cache {
  *   k, v: device, 2-byte aligned; element (t, h, e) at t * token + h * head + e. v may be a view
  *         of the same tensor as k.
  *   slots: device int64 [tokens]. A slot < 0 or >= num_pages * page_size: that token is left out.
- *         Two tokens with one slot: either may stay.
+ *         Two tokens of one call with one slot leave that row undefined (parts of either, and in a
+ *         quantised cache one's codes under the other's scales), and no other.
  * Returns AGMM_OK, INVALID_ARG, UNSUPPORTED or HIP. */
 int ag_kv_append(const ag_kv_cache* cache, const void* k, int64_t k_token, int64_t k_head,
                  const void* v, int64_t v_token, int64_t v_head, const int64_t* slots,
