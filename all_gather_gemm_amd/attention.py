@@ -17,6 +17,8 @@ import torch
 
 from . import BF16, F16, AgmmError, AGMM_OK, lib
 
+AGMM_ERR_WRONG_DEVICE = -6
+
 ROPE_HALF, ROPE_INTERLEAVED = 0, 1
 ROPE_NONE, ROPE_LINEAR, ROPE_BASE, ROPE_TURNS, ROPE_INDEX = range(5)
 KV_16BIT, KV_MXFP8, KV_MXFP4 = range(3)
@@ -101,7 +103,15 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _stream(stream, index: int) -> int:
+    """The stream of a launch on the tensors' device. That has to be the current one: a kernel is launched
+    on the current device, whatever its pointers and its stream belong to."""
+    if index != _current() or \
+            (stream is not None and getattr(stream, "device_index", index) != index):
+        raise AgmmError(AGMM_ERR_WRONG_DEVICE, f"tensors on device {index}")
     return stream.cuda_stream if stream is not None else _raw_stream(index)
 
 

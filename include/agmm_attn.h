@@ -13,7 +13,9 @@
  *
  * Types: q, k, v and the outputs share one 16-bit type (AGMM_F16 or AGMM_BF16); every sum, angle
  * and softmax statistic is held in 32 bits or more. Strides are counted in elements of the tensor
- * unless they say bytes; a head's values are always contiguous. Codes and threading are those of
+ * unless they say bytes; a head's values are always contiguous. Kernels are launched on the current
+ * device: memory and stream of a call belong to it (handles are checked; the cache's calls have none, and
+ * pointers' devices are not looked up). Codes and threading are those of
  * agmm.h (ag_matmul_strerror and ag_matmul_last_hip_error serve these functions too). The
  * creates and destroys wait for the device; the runs, appends and reads do not, and may be captured
  * into a HIP graph and replayed.
