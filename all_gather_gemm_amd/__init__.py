@@ -294,6 +294,22 @@ def ag_matmul_debug_fill_staging(handle: int, pattern: int, stream: int = 0) -> 
 
 # ---- torch convenience wrapper (pointers and the current stream only) ----
 
+def _result(make, stream, device):
+    """make() for a result that `stream` writes: allocated from that stream's memory, where what is free
+    is in use by no other stream, and given back only when the current stream, on which its user reads
+    it, is done with it as well."""
+    if stream is None:
+        return make()
+    import torch
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return make()
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(current)
+    return t
+
+
 class AgMatmul:
     """One handle for one problem shape. run() takes D shard tensors [M/D, K], B [K, N],
     an optional bias [N] and an output [M, N], all contiguous on the handle's device.

@@ -7,6 +7,10 @@ bits) and reads them back, `DecodeAttention` attends with one new token of every
 package's main module, this one only marshals arguments: tensors' pointers and strides and torch's
 current stream go to the library's kernels, error codes come back as AgmmError, and there is no
 fallback path.
+
+With `stream`, a run is launched there instead: what it reads has to be ready on that stream, and
+whoever reads its results waits for that stream (`wait_stream`). Results that a run allocates are
+safe on the stream that was current as well; its inputs the caller keeps, or records on `stream`.
 """
 from __future__ import annotations
 
@@ -15,7 +19,7 @@ from typing import Optional, Sequence
 
 import torch
 
-from . import BF16, F16, AgmmError, AGMM_OK, lib
+from . import BF16, F16, AgmmError, AGMM_OK, _result, lib
 
 AGMM_ERR_WRONG_DEVICE = -6
 
@@ -115,6 +119,10 @@ def _stream(stream, index: int) -> int:
     return stream.cuda_stream if stream is not None else _raw_stream(index)
 
 
+def _like(x, stream):
+    return _result(lambda: torch.empty_like(x), stream, x.device)
+
+
 def _pick(table, key, what):
     if key not in table:
         raise ValueError(f"{what} is one of {', '.join(table)}: got {key!r}")
@@ -196,20 +204,21 @@ class Rope:
         if dims not in (3, 4):
             raise ValueError("x must be [tokens, heads, head_dim] or [batch, tokens, heads, head_dim]")
         _tensor(x, "x", self.torch_dtype, shape[:-1] + (self.head_dim,), device)
+        shared = positions.dim() == 1
+        _tensor(positions, "positions", torch.int64, shape[-3:-2] if shared else shape[:-2], device)
+        where = _stream(stream, device.index)
         if out is None:
-            out = torch.empty_like(x)
+            out = _like(x, stream)
         else:
             _tensor(out, "out", self.torch_dtype, shape, device)
         ys, batch, xb, yb, pb = out.stride(), 1, 0, 0, 0
         if dims == 4:
             batch, xb, yb = shape[0], xs[0], ys[0]
-        shared = positions.dim() == 1
-        _tensor(positions, "positions", torch.int64, shape[-3:-2] if shared else shape[:-2], device)
         if not shared:
             pb = positions.stride(0)
         rc = lib.ag_rope_run(self.handle, x.data_ptr(), xb, xs[-3], xs[-2], out.data_ptr(), yb,
                              ys[-3], ys[-2], positions.data_ptr(), pb, batch, shape[-3], shape[-2],
-                             gradient, _stream(stream, device.index))
+                             gradient, where)
         _checked(rc, "ag_rope_run")
         return out
 
@@ -298,15 +307,16 @@ class PagedCache:
         _tensor(v, "v", td, shape, device)
         _tensor(slots, "slots", torch.int64, (tokens,), device)
         _tensor(positions, "positions", torch.int64, (tokens,), device)
+        where = _stream(stream, device.index)
         if q_out is None:
-            q_out = torch.empty_like(q)
+            q_out = _like(q, stream)
         else:
             _tensor(q_out, "q_out", td, q.shape, device)
         qs, os, ks, vs = q.stride(), q_out.stride(), k.stride(), v.stride()
         rc = lib.ag_kv_append_rope(self._ref, rope.handle, q.data_ptr(), qs[0], qs[1], q.shape[1],
                                    q_out.data_ptr(), os[0], os[1], k.data_ptr(), ks[0], ks[1],
                                    v.data_ptr(), vs[0], vs[1], positions.data_ptr(),
-                                   slots.data_ptr(), tokens, _stream(stream, device.index))
+                                   slots.data_ptr(), tokens, where)
         _checked(rc, "ag_kv_append_rope")
         return q_out
 
@@ -316,12 +326,13 @@ class PagedCache:
         tokens = slots.shape[0]
         shape, td, device = (tokens, self.kv_heads, self.head_dim), self.torch_dtype, self.device
         _tensor(slots, "slots", torch.int64, (tokens,), device)
-        k = slots.new_empty(shape, dtype=td) if k_out is None else \
-            _tensor(k_out, "k_out", td, shape, device)
-        v = torch.empty_like(k) if v_out is None else _tensor(v_out, "v_out", td, shape, device)
+        where = _stream(stream, device.index)
+        new = lambda: _result(lambda: slots.new_empty(shape, dtype=td), stream, device)  # noqa: E731
+        k = new() if k_out is None else _tensor(k_out, "k_out", td, shape, device)
+        v = new() if v_out is None else _tensor(v_out, "v_out", td, shape, device)
         ks, vs = k.stride(), v.stride()
         rc = lib.ag_kv_read(self._ref, slots.data_ptr(), tokens, k.data_ptr(), ks[0], ks[1],
-                            v.data_ptr(), vs[0], vs[1], _stream(stream, device.index))
+                            v.data_ptr(), vs[0], vs[1], where)
         _checked(rc, "ag_kv_read")
         return k, v
 
@@ -366,16 +377,17 @@ class DecodeAttention:
         _tensor(page_table, "page_table", torch.int32,
                 (batch, page_table.shape[1] if page_table.dim() == 2 else None), device)
         _tensor(lens, "lens", torch.int32, (batch,), device)
+        where = _stream(stream, device.index)
         if out is None:
-            out = torch.empty_like(q)
+            out = _like(q, stream)
         else:
             _tensor(out, "out", self.torch_dtype, q.shape, device)
-        lse = q.new_empty((batch, self.q_heads), dtype=torch.float32) if return_lse else None
+        lse = _result(lambda: q.new_empty((batch, self.q_heads), dtype=torch.float32), stream,
+                      device) if return_lse else None
         qs, os = q.stride(), out.stride()
         rc = lib.ag_attn_run(self.handle, cache._ref, q.data_ptr(), qs[0], qs[1],
                              page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
                              lens.data_ptr(), batch, out.data_ptr(), os[0], os[1],
-                             lse.data_ptr() if return_lse else None,
-                             _stream(stream, device.index))
+                             lse.data_ptr() if return_lse else None, where)
         _checked(rc, "ag_attn_run")
         return (out, lse) if return_lse else out
