@@ -358,12 +358,13 @@ class AgMatmul:
         for t in list(shards) + [B] + ([bias] if bias is not None else []):
             if t.dtype != tdt or not t.is_cuda or not t.is_contiguous():
                 raise ValueError("inputs must be contiguous device tensors of the handle's dtype")
+        new = lambda *n: _result(lambda: torch.empty(n, dtype=tdt, device=B.device), stream, B.device)  # noqa: E731
         if out is None:
-            out = torch.empty((d.M, d.N), dtype=tdt, device=B.device)
+            out = new(d.M, d.N)
         s = stream if stream is not None else torch.cuda.current_stream(B.device)
         if d.gather_a:
             if a_out is None:
-                a_out = torch.empty((d.M, d.K), dtype=tdt, device=B.device)
+                a_out = new(d.M, d.K)
             if a_out.dtype != tdt or not a_out.is_cuda or not a_out.is_contiguous() or \
                     tuple(a_out.shape) != (d.M, d.K):
                 raise ValueError("a_out must be a contiguous [M, K] device tensor of the handle's dtype")
@@ -528,7 +529,8 @@ class GemmAllReduce:
         import torch
         tdt = torch.float16 if self.dtype == "f16" else torch.bfloat16
         if out is None:
-            out = torch.empty((self.M, self.N), dtype=tdt, device=C.device)
+            out = _result(lambda: torch.empty((self.M, self.N), dtype=tdt, device=C.device), stream,
+                          C.device)
         s = stream if stream is not None else torch.cuda.current_stream(C.device)
         rc = lib.ag_gemm_ar_finalize(ctypes.c_void_p(self.handle), ctypes.c_void_p(C.data_ptr()),
                                      ctypes.c_void_p(bias.data_ptr()) if bias is not None else None,
@@ -571,7 +573,8 @@ class GemmAllReduceFlags:
             if t.dtype != tdt or not t.is_cuda or not t.is_contiguous():
                 raise ValueError("inputs must be contiguous device tensors of the handle's type")
         if out is None:
-            out = torch.empty((self.M, self.N), dtype=tdt, device=A_parts[0].device)
+            device = A_parts[0].device
+            out = _result(lambda: torch.empty((self.M, self.N), dtype=tdt, device=device), stream, device)
         s = stream if stream is not None else torch.cuda.current_stream(out.device)
         ap = (ctypes.c_void_p * self.D)(*[ctypes.c_void_p(t.data_ptr()) for t in A_parts])
         bp = (ctypes.c_void_p * self.D)(*[ctypes.c_void_p(t.data_ptr()) for t in B_parts])

@@ -67,3 +67,23 @@ def check(call):
 @pytest.mark.parametrize("name", ["rope", "grad", "append_rope", "read", "attention"])
 def test_serving_results(T, name):
     check(serving_calls(T)[name])
+
+
+@pytest.mark.parametrize("name", ["gather", "finalize", "flags"])
+def test_product_results(name):
+    import all_gather_gemm_amd as A
+    g = torch.Generator().manual_seed(2)
+    draw = lambda *n: torch.randn(n, generator=g).half().to(DEV)     # noqa: E731
+    D, M, N, K = 2, 256, 256, 256
+    if name == "gather":
+        op = A.AgMatmul(D, M, N, K, gather_a=True)
+        shards, B = [draw(M // D, K) for _ in range(D)], draw(K, N)
+        check(lambda s: list(op.run(shards, B, stream=s)))
+    elif name == "finalize":
+        op = A.GemmAllReduce(D, 0, M, N, K)
+        C = torch.randn((M, N), generator=g).to(DEV)
+        check(lambda s: [op.finalize(C, stream=s)])
+    else:
+        op = A.GemmAllReduceFlags(D, M, N, K)
+        a, b = [draw(M, K) for _ in range(D)], [draw(K, N) for _ in range(D)]
+        check(lambda s: [op.run(a, b, stream=s)])
