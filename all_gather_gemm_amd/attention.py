@@ -160,7 +160,8 @@ class Rope:
         d = ag_rope_desc()
         lib.ag_rope_desc_init(ctypes.byref(d))
         d.dtype, self.torch_dtype = _pick(_DTYPES, dtype, "dtype")
-        d.head_dim, d.rot_dim, d.rot_start = head_dim, rot_dim or head_dim, rot_start
+        d.head_dim, d.rot_start = head_dim, rot_start
+        d.rot_dim = head_dim if rot_dim is None else rot_dim
         d.pairing = _pick(_PAIRINGS, pairing, "pairing")
         d.scaling = _pick(_SCALINGS, scaling, "scaling")
         d.base, d.factor, d.original_len = base, factor, original_len

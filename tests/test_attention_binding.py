@@ -100,3 +100,11 @@ def test_tensors_on_another_device_than_the_current(T, monkeypatch, lib, i):
         call(stream=Stream(0))
     assert lib.names == [name, name]
     lib.names.clear()
+
+
+def test_no_rotated_elements(T):
+    """A rotated part of 0 elements is refused, as any other that the header does not allow."""
+    for rot in (0, 3, -2, 66):
+        with pytest.raises(T.AgmmError) as e:
+            T.Rope(64, rot_dim=rot)
+        assert e.value.code == -1
