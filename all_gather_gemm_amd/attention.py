@@ -11,6 +11,8 @@ fallback path.
 With `stream`, a run is launched there instead: what it reads has to be ready on that stream, and
 whoever reads its results waits for that stream (`wait_stream`). Results that a run allocates are
 safe on the stream that was current as well; its inputs the caller keeps, or records on `stream`.
+
+`Rope` takes part in autograd. The cache and the attention serve: no gradient passes through them.
 """
 from __future__ import annotations
 
@@ -143,13 +145,30 @@ def _tensor(t, name, dtype, shape, device=None):
     return t
 
 
+class _Rotation(torch.autograd.Function):
+    """R x or R^T x, and the other one as its gradient."""
+
+    @staticmethod
+    def forward(ctx, x, rope, positions, gradient):
+        ctx.rope, ctx.gradient = rope, gradient
+        ctx.save_for_backward(positions)
+        return rope._run(x.detach(), positions, None, None, gradient)
+
+    @staticmethod
+    def backward(ctx, dy):
+        if dy.stride(-1) != 1:      # as that of a sum, which is one expanded element
+            dy = dy.contiguous()
+        return ctx.rope._run(dy, ctx.saved_tensors[0], None, None, 1 - ctx.gradient), None, None, None
+
+
 class Rope:
     """Rotary positions of one head geometry and set of frequencies (ag_rope_desc).
 
     run(x, positions) returns R x for x [tokens, heads, head_dim] and positions [tokens], or with
     a batch in front of both ([batch, tokens, heads, head_dim]; positions [tokens] are then
     shared); any strides but the last dimension's. grad(dy, positions) returns R^T dy: the
-    gradient of x. out may be x itself."""
+    gradient of x, which autograd takes by itself where x requires it. out may be x itself; an
+    x that requires a gradient takes none."""
 
     def __init__(self, head_dim: int, rot_dim: Optional[int] = None, rot_start: int = 0,
                  pairing: str = "half", dtype: str = "bf16", scaling: str = "none",
@@ -200,6 +219,11 @@ class Rope:
         return self._run(dy, positions, out, stream, 1)
 
     def _run(self, x, positions, out, stream, gradient):
+        if x.requires_grad and torch.is_grad_enabled():
+            if out is not None:
+                raise ValueError("out takes no part in autograd: x must not require a gradient")
+            run = lambda: _Rotation.apply(x, self, positions, gradient)  # noqa: E731
+            return _result(run, stream, x.device)   # (backward runs on the same stream)
         shape, xs, device = x.shape, x.stride(), x.device
         dims = len(shape)
         if dims not in (3, 4):

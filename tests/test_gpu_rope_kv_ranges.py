@@ -38,3 +38,62 @@ def test_slots_that_tokens_share(T, storage):
         for x, y in zip(cache.read(slots), (k, v)):
             for a, b in shared:
                 assert ((x[a] == y[a]) | (x[a] == y[b])).all()
+
+
+@pytest.mark.parametrize("pairing", ["half", "interleaved"])
+def test_rope_in_autograd(T, pairing):
+    """A result of an input that requires a gradient has one: R^T of what comes back, and R of R^T's."""
+    r = T.Rope(80, rot_dim=40, rot_start=8, pairing=pairing, dtype="f16")
+    x, dy = normal(23, (30, 3, 80), "f16"), normal(24, (30, 3, 80), "f16")
+    pos = torch.arange(30, device=DEV) * 31
+    for there, back in ((r.run, r.grad), (r.grad, r.run)):
+        want, dx = there(x, pos), back(dy, pos)
+        leaf = x.clone().requires_grad_()
+        y = there(leaf, pos)
+        assert y.requires_grad and torch.equal(y, want)
+        y.backward(dy)
+        assert torch.equal(leaf.grad, dx)
+        leaf.grad = None                    # a sum's gradient is one expanded element; through views
+        there(leaf * 1, pos)[:, 1:].sum().backward()
+        ones = torch.ones_like(x)
+        ones[:, 0] = 0
+        assert torch.equal(leaf.grad, back(ones, pos))
+        # on another stream, backward there too
+        s = torch.cuda.Stream()
+        leaf.grad = None
+        s.wait_stream(torch.cuda.current_stream())
+        y = there(leaf, pos, stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+        y.backward(dy)
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(leaf.grad, dx)
+        # the gradient's own gradient
+        dleaf = dy.clone().requires_grad_()
+        g, = torch.autograd.grad(there(leaf, pos), leaf, dleaf, create_graph=True)
+        g.backward(x)
+        assert torch.equal(dleaf.grad, want)
+        with pytest.raises(ValueError):
+            there(leaf, pos, out=torch.empty_like(x))
+        with torch.no_grad():
+            assert not there(leaf, pos).requires_grad
+            assert torch.equal(there(leaf, pos, out=torch.empty_like(x)), want)
+    # a batch that shares its positions
+    leaf = normal(25, (2, 30, 3, 80), "f16").requires_grad_()
+    r.run(leaf, pos).backward(dy.expand(2, 30, 3, 80))
+    assert torch.equal(leaf.grad[0], r.grad(dy, pos)) and torch.equal(leaf.grad[1], leaf.grad[0])
+
+
+def test_rope_gradient_by_differences(T):
+    """(L(x + h e) - L(x - h e)) / 2h of L(x) = sum(w R x): exact but for the roundings of the results, which
+    are half an ulp of magnitudes up to 3 each, 16 of them over 2h = 2."""
+    r = T.Rope(16, rot_dim=12, rot_start=2, dtype="f16")
+    x = (torch.arange(32, device=DEV).view(1, 2, 16) / 16 - 1).half().requires_grad_()
+    w = torch.linspace(-1, 1, 32, device=DEV).view(1, 2, 16).half()
+    pos = torch.tensor([777], device=DEV)
+    (r.run(x, pos).double() * w.double()).sum().backward()
+    for i in range(32):
+        h = torch.zeros(32, device=DEV, dtype=torch.float16)
+        h[i] = 1.0
+        with torch.no_grad():
+            d = [(r.run(x + s * h.view(1, 2, 16), pos).double() * w.double()).sum() for s in (1, -1)]
+        assert abs(float(d[0] - d[1]) / 2 - float(x.grad.view(-1)[i])) <= 2 * 16 * 3 * 2.0 ** -11 / 2
