@@ -114,6 +114,9 @@ agmm::RopePlan plan_of(const ag_rope_handle& h) {
   return r;
 }
 
+// Whether two strides lead to the same n places: that of a dimension of one says nothing.
+bool same_step(int64_t n, int64_t a, int64_t b) { return n <= 1 || a == b; }
+
 // The units that threads take of a head.
 void rope_units(const ag_rope_desc& d, int64_t heads, RopeParams* p) {
   p->rot_units = d.pairing == AG_ROPE_HALF ? (d.rot_dim / 2 + 7) / 8 : (d.rot_dim / 2 + 3) / 4;
@@ -320,7 +323,8 @@ int ag_rope_run(ag_rope_handle* h, const void* x, int64_t x_batch, int64_t x_tok
   p.y_token = y_token;
   p.y_head = y_head;
   p.pos_batch = pos_batch;
-  p.in_place = x == y && x_batch == y_batch && x_token == y_token && x_head == y_head;
+  p.in_place = x == y && same_step(batch, x_batch, y_batch) && same_step(tokens, x_token, y_token) &&
+               same_step(heads, x_head, y_head);
   rope_units(h->desc, heads, &p);
   const uint64_t per_token = (uint64_t)p.units.d * p.heads.d;
   const int64_t step = tokens_per_launch(per_token), bstep = 65535;
@@ -384,7 +388,7 @@ int ag_kv_append_rope(const ag_kv_cache* cache, ag_rope_handle* rope, const void
   r.x_head = q_head;
   r.y_token = qo_token;
   r.y_head = qo_head;
-  r.in_place = q == q_out && q_token == qo_token && q_head == qo_head;
+  r.in_place = q == q_out && same_step(tokens, q_token, qo_token) && same_step(q_heads, q_head, qo_head);
   rope_units(rope->desc, std::max<int64_t>(1, q_heads), &r);
   const uint64_t q_threads = q_heads ? (uint64_t)r.units.d * r.heads.d : 0;
   const int64_t step = tokens_per_launch(

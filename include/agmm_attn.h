@@ -82,8 +82,8 @@ int ag_rope_destroy(ag_rope_handle* h); /* synchronizes the device; NULL-safe */
 
 /* y = R x for `batch` x `tokens` x `heads` heads, or, with gradient = 1, y = R^T x.
  *   x, y: device, 2-byte aligned; element (b, t, h, e) at b * batch + t * token + h * head + e of
- *         the given strides (x's may be 0 or negative). y is x with equal strides (in place), or
- *         does not overlap it; y's own elements must not overlap.
+ *         the given strides (x's may be 0 or negative). y is x with equal strides (in place; those of
+ *         a size of 1 count for nothing), or does not overlap it; y's own elements must not overlap.
  *   positions: device int64, element (b, t) at b * pos_batch + t (pos_batch 0: shared).
  * Returns AGMM_OK, INVALID_ARG, WRONG_DEVICE or HIP; zero sizes enqueue nothing. */
 int ag_rope_run(ag_rope_handle* h, const void* x, int64_t x_batch, int64_t x_token, int64_t x_head,

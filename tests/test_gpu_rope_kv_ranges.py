@@ -97,3 +97,29 @@ def test_rope_gradient_by_differences(T):
         with torch.no_grad():
             d = [(r.run(x + s * h.view(1, 2, 16), pos).double() * w.double()).sum() for s in (1, -1)]
         assert abs(float(d[0] - d[1]) / 2 - float(x.grad.view(-1)[i])) <= 2 * 16 * 3 * 2.0 ** -11 / 2
+
+
+@pytest.mark.parametrize("pairing,rot", [("half", 40), ("half", 20), ("interleaved", 20)])
+def test_rope_in_place_through_other_strides(T, pairing, rot):
+    """A size of 1 has any stride: an output that is the input's memory is in place whatever it says, and
+    pairs that two threads would share otherwise are read before they are written."""
+    heads, dim = 70, 96
+    r = T.Rope(dim, rot_dim=rot, pairing=pairing, dtype="bf16")
+    pos = torch.tensor([4321], device=DEV)
+    x = normal(26, (1, heads, dim), "bf16")
+    want = r.run(x, pos)
+    y = x.clone()
+    r.run(y, pos, out=y.as_strided((1, heads, dim), (1, dim, 1)))
+    assert torch.equal(y, want)
+    one = x[:, :1].clone()      # one head, in a batch of one
+    r.run(one, pos, out=one.as_strided((1, 1, dim), (7, 7, 1)))
+    assert torch.equal(one, want[:, :1])
+    y = x.clone()
+    r.run(y[None], pos, out=y.as_strided((1, 1, heads, dim), (3, 5, dim, 1)))
+    assert torch.equal(y, want)
+    # and in the step in front of the attention
+    cache = T.PagedCache.empty(2, 16, 2, dim)
+    k, slots = normal(27, (1, 2, dim), "bf16"), torch.tensor([3], device=DEV)
+    y = x.clone()
+    cache.append_rope(r, y, k, k, pos, slots, q_out=y.as_strided((1, heads, dim), (1, dim, 1)))
+    assert torch.equal(y, want)
