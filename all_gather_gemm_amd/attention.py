@@ -275,6 +275,8 @@ class PagedCache:
             if k_scale is not None or v_scale is not None:
                 raise ValueError("a 16-bit cache has no scales")
         else:
+            if k_scale is None or v_scale is None:
+                raise ValueError(f"a cache in {storage} needs k_scale and v_scale")
             shape = tuple(k.shape[:3]) + (self.scale_bytes(c.head_dim),)
             _tensor(k_scale, "k_scale", torch.uint8, shape, k.device)
             _tensor(v_scale, "v_scale", torch.uint8, shape, k.device)

@@ -108,3 +108,13 @@ def test_no_rotated_elements(T):
         with pytest.raises(T.AgmmError) as e:
             T.Rope(64, rot_dim=rot)
         assert e.value.code == -1
+
+
+@pytest.mark.parametrize("storage,row", [("mxfp8", 64), ("mxfp4", 32)])
+def test_coded_cache_without_scales(T, storage, row):
+    pool = Fake((4, 2, 16, row), torch.uint8)
+    scale = Fake((4, 2, 16, 4), torch.uint8)
+    for scales in ((), (scale,), (None, scale)):
+        with pytest.raises(ValueError):
+            T.PagedCache(pool, pool, *scales, storage=storage)
+    assert T.PagedCache(pool, pool, scale, scale, storage=storage).head_dim == 64
