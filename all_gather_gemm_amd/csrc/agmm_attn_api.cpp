@@ -61,7 +61,7 @@ bool valid_rope(const ag_rope_desc* d) {
   if (d->rot_dim < 2 || d->rot_dim > std::min(d->head_dim, kRotMax) || d->rot_dim % 2) return false;
   if (d->rot_start < 0 || d->rot_start > d->head_dim - d->rot_dim) return false;
   if (d->pairing != AG_ROPE_HALF && d->pairing != AG_ROPE_INTERLEAVED) return false;
-  if (!isfinite(d->magnitude)) return false;
+  if (!isfinite((float)d->magnitude)) return false;  // as the kernels take it
   if (d->thetas) {
     for (int i = 0; i < d->rot_dim / 2; ++i)
       if (!isfinite(d->thetas[i])) return false;

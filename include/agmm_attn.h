@@ -60,7 +60,7 @@ typedef struct ag_rope_desc {
   double factor;       /* > 0 (scaling != NONE) */
   double original_len; /* > 0, and low < high, both > 0 (TURNS, INDEX) */
   double low, high;
-  double magnitude;    /* factor of the cosines and sines; finite */
+  double magnitude;    /* factor of the cosines and sines; finite in 32 bits */
   const double* thetas; /* host, rot_dim / 2 angles per position in radians in the place of all of
                            the above, or NULL; read by create only */
 } ag_rope_desc;
@@ -85,7 +85,8 @@ int ag_rope_destroy(ag_rope_handle* h); /* synchronizes the device; NULL-safe */
  *         the given strides (x's may be 0 or negative). y is x with equal strides (in place; those of
  *         a size of 1 count for nothing), or does not overlap it; y's own elements must not overlap.
  *   positions: device int64, element (b, t) at b * pos_batch + t (pos_batch 0: shared).
- * Returns AGMM_OK, INVALID_ARG, WRONG_DEVICE or HIP; zero sizes enqueue nothing. */
+ * Returns AGMM_OK, INVALID_ARG, UNSUPPORTED (over 2^20 heads), WRONG_DEVICE or HIP; zero sizes
+ * enqueue nothing. */
 int ag_rope_run(ag_rope_handle* h, const void* x, int64_t x_batch, int64_t x_token, int64_t x_head,
                 void* y, int64_t y_batch, int64_t y_token, int64_t y_head, const int64_t* positions,
                 int64_t pos_batch, int64_t batch, int64_t tokens, int64_t heads, int gradient,
@@ -134,7 +135,8 @@ int ag_kv_append(const ag_kv_cache* cache, const void* k, int64_t k_token, int64
 /* The step in front of the attention in one launch: q_out = R q for q_heads heads (as ag_rope_run),
  * and the cache's slots get R k and v (as ag_rope_run into a tensor of `dtype` and then
  * ag_kv_append would leave them, bit for bit). rope must have the cache's dtype and head_dim.
- *   positions: device int64 [tokens]. A token whose slot is left out still has its q rotated. */
+ *   positions: device int64 [tokens]. A token whose slot is left out still has its q rotated.
+ * Returns AGMM_OK, INVALID_ARG, UNSUPPORTED, WRONG_DEVICE or HIP. */
 int ag_kv_append_rope(const ag_kv_cache* cache, ag_rope_handle* rope, const void* q,
                       int64_t q_token, int64_t q_head, int64_t q_heads, void* q_out,
                       int64_t qo_token, int64_t qo_head, const void* k, int64_t k_token,
@@ -143,7 +145,8 @@ int ag_kv_append_rope(const ag_kv_cache* cache, ag_rope_handle* rope, const void
                       void* hip_stream);
 
 /* Reads the rows at `slots` back as values of `dtype`: k_out and v_out, element (t, h, e) at
- * t * token + h * head + e, 2-byte aligned. A slot out of range (above) gives zeros. */
+ * t * token + h * head + e, 2-byte aligned. A slot out of range (above) gives zeros.
+ * Returns AGMM_OK, INVALID_ARG, UNSUPPORTED or HIP. */
 int ag_kv_read(const ag_kv_cache* cache, const int64_t* slots, int64_t tokens, void* k_out,
                int64_t k_token, int64_t k_head, void* v_out, int64_t v_token, int64_t v_head,
                void* hip_stream);

@@ -118,3 +118,10 @@ def test_coded_cache_without_scales(T, storage, row):
         with pytest.raises(ValueError):
             T.PagedCache(pool, pool, *scales, storage=storage)
     assert T.PagedCache(pool, pool, scale, scale, storage=storage).head_dim == 64
+
+
+def test_magnitude_past_32_bits(T):
+    for m in (1e39, -1e300):
+        with pytest.raises(T.AgmmError) as e:
+            T.Rope(64, magnitude=m)
+        assert e.value.code == -1
