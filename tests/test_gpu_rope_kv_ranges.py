@@ -123,3 +123,100 @@ def test_rope_in_place_through_other_strides(T, pairing, rot):
     y = x.clone()
     cache.append_rope(r, y, k, k, pos, slots, q_out=y.as_strided((1, heads, dim), (1, dim, 1)))
     assert torch.equal(y, want)
+
+
+# More threads than one launch takes (2^30), more batch entries than one grid has: the call is cut into
+# launches, the later of which start in the middle of every argument.
+PER_LAUNCH = 1 << 30
+
+
+def test_rope_in_two_launches(T):
+    n = PER_LAUNCH + 9
+    r = T.Rope(2, dtype="bf16")
+    x = torch.empty((n, 1, 2), dtype=torch.bfloat16, device=DEV).normal_(
+        generator=torch.Generator(device=DEV).manual_seed(1))
+    pos = torch.arange(n, device=DEV)
+    y = r.run(x, pos)
+    for part in (slice(0, n // 2 + 5), slice(n // 2 + 5, n)):
+        assert torch.equal(y[part], r.run(x[part], pos[part]))
+
+
+def test_rope_of_many_batch_entries(T):
+    batch, tokens, heads, dim = 65535 + 70, 3, 2, 16
+    r = T.Rope(dim, dtype="f16", rot_dim=12, rot_start=2)
+    x = normal(31, (batch, tokens, heads, dim), "f16")
+    pos = torch.arange(batch * tokens, device=DEV).view(batch, tokens)
+    flat = x.view(-1, heads, dim)
+    assert torch.equal(r.run(x, pos).view_as(flat), r.run(flat, pos.view(-1)))
+    shared = pos[0].expand(batch, tokens).reshape(-1)
+    assert torch.equal(r.grad(x, pos[0]).view_as(flat), r.grad(flat, shared))
+
+
+def overlapping(n, seed):
+    """n rows of 8 elements in n + 7: row t begins at element t."""
+    flat = torch.empty(n + 7, dtype=torch.bfloat16, device=DEV).normal_(
+        generator=torch.Generator(device=DEV).manual_seed(seed))
+    return flat.as_strided((n, 1, 8), (1, 8, 1))
+
+
+def test_cache_in_two_launches(T):
+    n, page, pages = PER_LAUNCH + 40, 16, 20
+    k, v = overlapping(n, 2), overlapping(n, 3)
+    cache = T.PagedCache.empty(pages, page, 1, 8)
+    kept = torch.cat((torch.arange(50), torch.arange(PER_LAUNCH - 50, n))).to(DEV)
+    slots = torch.full((n,), -1, dtype=torch.int64, device=DEV)
+    slots[kept] = torch.randperm(pages * page, device=DEV)[:len(kept)]
+    cache.append(k, v, slots)
+    want = cache.read(slots[kept])
+    assert torch.equal(want[0], k[kept]) and torch.equal(want[1], v[kept])
+    out = cache.read(slots)
+    for x, y in zip(out, want):
+        assert torch.equal(x[kept], y)
+        x[kept] = 0
+        assert not any(bool(part.any()) for part in x.split(1 << 27))
+
+
+def test_append_rope_in_two_launches(T):
+    n = PER_LAUNCH // 2 + 40        # two threads a token: a unit of pairs, and one that passes through
+    r = T.Rope(8, rot_dim=2, rot_start=6, dtype="bf16")
+    q, k, v = (overlapping(n, s) for s in (4, 5, 6))
+    pos = torch.arange(n, device=DEV)
+    page, pages = 16, 20
+    a, b = (T.PagedCache.empty(pages, page, 1, 8) for _ in "ab")
+    kept = torch.cat((torch.arange(50), torch.arange(n - 90, n))).to(DEV)
+    slots = torch.full((n,), -1, dtype=torch.int64, device=DEV)
+    slots[kept] = torch.randperm(pages * page, device=DEV)[:len(kept)]
+    q_out = a.append_rope(r, q, k, v, pos, slots, q_out=torch.empty((n, 1, 8), dtype=q.dtype, device=DEV))
+    for part in (slice(0, n // 2 + 5), slice(n // 2 + 5, n)):
+        assert torch.equal(q_out[part], r.run(q[part].contiguous(), pos[part]))
+    b.append(r.run(k[kept], pos[kept]), v[kept], slots[kept])
+    assert torch.equal(a.k, b.k) and torch.equal(a.v, b.v)
+
+
+@pytest.mark.parametrize("storage,dim", [("mxfp8", 256), ("mxfp4", 64)])
+def test_scales_past_32_bits(T, storage, dim):
+    """Scale bytes of pages whose distance from the pool's start does not fit 32 bits."""
+    pages, heads, page, apart, tokens = 40, 2, 16, 1 << 28, 500
+    near = T.PagedCache.empty(pages, page, heads, dim, storage=storage)
+    row = T.PagedCache.scale_bytes(dim)
+    pools = [torch.empty(pages * apart, dtype=torch.uint8, device=DEV) for _ in "kv"]
+    far = [p.as_strided((pages, heads, page, row), (apart, page * row, row, 1)) for p in pools]
+    for t in far:
+        t.fill_(255)
+    cache = T.PagedCache(torch.zeros_like(near.k), torch.zeros_like(near.v), *far, storage=storage)
+    k, v = normal(32, (tokens, heads, dim), "bf16"), normal(33, (tokens, heads, dim), "bf16")
+    slots = torch.randperm(pages * page, generator=torch.Generator().manual_seed(7))[:tokens].to(DEV)
+    for c in (near, cache):
+        c.append(k, v, slots)
+    for x, y in zip(near.read(slots), cache.read(slots)):
+        assert torch.equal(x, y)
+    attn = T.DecodeAttention(4, heads, dim, storage=storage)
+    table = torch.arange(pages, dtype=torch.int32, device=DEV)[None].contiguous()
+    lens = torch.tensor([pages * page], dtype=torch.int32, device=DEV)
+    q = normal(34, (1, 4, dim), "bf16")
+    every = torch.arange(pages * page, device=DEV)
+    empty = every[~torch.isin(every, slots)]
+    for c in (near, cache):     # rows that nothing wrote: zeros in both
+        c.append(torch.zeros((len(empty), heads, dim), dtype=k.dtype, device=DEV),
+                 torch.zeros((len(empty), heads, dim), dtype=k.dtype, device=DEV), empty)
+    assert torch.equal(attn.run(q, near, table, lens), attn.run(q, cache, table, lens))
