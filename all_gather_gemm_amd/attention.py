@@ -107,22 +107,28 @@ def _checked(rc: int, where: str):
 # The current stream's handle without a torch.cuda.Stream object made for it (2 us of a call's 7).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
 _current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream, index: int) -> int:
     """The stream of a launch on the tensors' device. That has to be the current one: a kernel is launched
     on the current device, whatever its pointers and its stream belong to."""
-    if index != _current() or \
-            (stream is not None and getattr(stream, "device_index", index) != index):
-        raise AgmmError(AGMM_ERR_WRONG_DEVICE, f"tensors on device {index}")
-    return stream.cuda_stream if stream is not None else _raw_stream(index)
+    if index == _current():
+        if stream is None:
+            return _raw_stream(index)
+        if getattr(stream, "device_index", index) == index:
+            return stream.cuda_stream
+    raise AgmmError(AGMM_ERR_WRONG_DEVICE, f"tensors on device {index}")
 
 
 def _like(x, stream):
-    return _result(lambda: torch.empty_like(x), stream, x.device)
+    return torch.empty_like(x) if stream is None else \
+        _result(lambda: torch.empty_like(x), stream, x.device)
+
+
+def _empty(x, shape, dtype, stream):
+    return x.new_empty(shape, dtype=dtype) if stream is None else \
+        _result(lambda: x.new_empty(shape, dtype=dtype), stream, x.device)
 
 
 def _pick(table, key, what):
@@ -354,9 +360,9 @@ class PagedCache:
         shape, td, device = (tokens, self.kv_heads, self.head_dim), self.torch_dtype, self.device
         _tensor(slots, "slots", torch.int64, (tokens,), device)
         where = _stream(stream, device.index)
-        new = lambda: _result(lambda: slots.new_empty(shape, dtype=td), stream, device)  # noqa: E731
-        k = new() if k_out is None else _tensor(k_out, "k_out", td, shape, device)
-        v = new() if v_out is None else _tensor(v_out, "v_out", td, shape, device)
+        k = _empty(slots, shape, td, stream) if k_out is None else \
+            _tensor(k_out, "k_out", td, shape, device)
+        v = _like(k, stream) if v_out is None else _tensor(v_out, "v_out", td, shape, device)
         ks, vs = k.stride(), v.stride()
         rc = lib.ag_kv_read(self._ref, slots.data_ptr(), tokens, k.data_ptr(), ks[0], ks[1],
                             v.data_ptr(), vs[0], vs[1], where)
@@ -409,8 +415,7 @@ class DecodeAttention:
             out = _like(q, stream)
         else:
             _tensor(out, "out", self.torch_dtype, q.shape, device)
-        lse = _result(lambda: q.new_empty((batch, self.q_heads), dtype=torch.float32), stream,
-                      device) if return_lse else None
+        lse = _empty(q, (batch, self.q_heads), torch.float32, stream) if return_lse else None
         qs, os = q.stride(), out.stride()
         rc = lib.ag_attn_run(self.handle, cache._ref, q.data_ptr(), qs[0], qs[1],
                              page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
