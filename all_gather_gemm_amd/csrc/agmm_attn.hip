@@ -56,7 +56,6 @@ constexpr int kSingle = 32;
 constexpr int kJoin = 16;
 constexpr int kChunk = 16;           // pieces whose loads are in flight together
 constexpr int kRaise = 4;            // raise the maximum when a tile's is above it by this
-constexpr float kRounded = 0x1p16f;  // maxima from here on are taken from rounded scores
 
 // Partial results pass between workgroups that may sit on different XCDs, whose L2s are not coherent.
 // They are stored and loaded as relaxed atomics of agent scope, which write through and read past
@@ -104,18 +103,14 @@ __device__ inline int thread() {
   return NW == 1 ? (int)(threadIdx.x & 63) : (int)threadIdx.x;
 }
 
-// The factor that brings a sum with maximum m to the maximum `top` >= m. A sum without a finite score
-// keeps its own: it is 0, or NaN.
-__device__ inline float weight(float m, float top) {
-  return m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+// The factor that brings a sum with maximum m to the maximum `top` >= m, units of `scale` in base 2. A
+// sum without a finite score keeps its own: it is 0, or NaN.
+__device__ inline float weight(float m, float top, float scale) {
+  return m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f((m - top) * scale);
 }
 
-// A product that is rounded by itself, in no multiply-add.
-__device__ inline float scaled(float x, float scale) {
-  float y = x * scale;
-  asm("" : "+v"(y));
-  return y;
-}
+// What a unit of the maxima is in base 2: they are products q . k, or capped scores.
+__device__ inline float unit(const AttnParams& p) { return p.cap != 0.0f ? 1.0f : p.scale; }
 
 // Sum or maximum over the 4 lane groups of 16 (lanes l, l ^ 16, l ^ 32, l ^ 48), by exchanges of rows
 // between registers; a shuffle through LDS takes some 100 clocks, and every tile waits for one.
@@ -135,11 +130,17 @@ __device__ inline float across_sum(float x) {
   return across(x, [](float a, float b) { return a + b; });
 }
 
+// Stops the compiler from moving what is computed from x out of a loop, into registers that the loop
+// needs for its loads.
+__device__ inline int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // cap * tanh(s / cap) of a product x = q . k, in base 2, to a few roundings of the score itself however
 // far the cap is from it. With u = s / cap: from |u| = 1/4 on as (e^2u - 1) / (e^2u + 1), where the
-// subtraction loses two bits at most; below, where it would lose them all, as s times the series of
-// tanh(u) / u, whose first term left out is 8e-9 there. ALL: no lane has a |u| from 1/4 on (or NaN, which
-// the series keeps).
+// subtraction loses two bits at most; below, where it would lose them all, as s times the series of tanh(u) / u, whose
+// first term left out is 8e-9 there. ALL: no lane has a |u| from 1/4 on (or NaN, which the series keeps).
 constexpr float kFar = 0.25f;
 template <bool ALL>
 __device__ inline float capped(const AttnParams& p, float x) {
@@ -149,26 +150,24 @@ __device__ inline float capped(const AttnParams& p, float x) {
   r = fmaf(y, r, -1.0f / 3.0f);
   r = fmaf(y, r, 1.0f) * (x * p.scale);
   if constexpr (!ALL) {
-    const float e = __builtin_amdgcn_exp2f(fminf(fabsf(u) * 2.88539008177792681f, 64.0f));
-    const float far = (e - 1.0f) * __builtin_amdgcn_rcpf(e + 1.0f) * copysignf(p.cap, u);
+    const float e = __builtin_amdgcn_exp2f(__builtin_amdgcn_fmed3f(u * 2.88539008177792681f, -64.0f, 64.0f));
+    const float far = (e - 1.0f) * __builtin_amdgcn_rcpf(e + 1.0f) * p.cap;
     r = fabsf(u) >= kFar ? far : r;
   }
   return r;
 }
 
+// Keeps the compiler from working on many of a tile's scores at once, in registers that it spills for.
+__device__ inline float in_turn(float x) {
+  return __builtin_bit_cast(float, here(__builtin_bit_cast(int, x)));
+}
+
 // The head of a sequence's weights by the tokens that are attended to. (The other end, bf16: the
-// products of values below 2^-118, and 2^-101 of 131072 tokens, are subnormal and may lose bits.)
+// products of values below 2^-122, and 2^-105 of 131072 tokens, are subnormal and may lose bits.)
 template <int DT>
 __device__ inline int head_of(int64_t tokens) {
   if (DT == AGMM_F16) return 11;
   return -kRaise - (tokens > 1 ? 32 - __builtin_clz((uint32_t)(tokens - 1)) : 0);
-}
-
-// Stops the compiler from moving what is computed from x out of a loop, into registers that the loop
-// needs for its loads.
-__device__ inline int here(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
 }
 
 // What one wave loads of a tile of tokens, as it comes from memory.
@@ -177,7 +176,8 @@ struct Raw {
   // Sub-tiles of 16 tokens. 64 tokens share the cost of placing a tile and of its softmax; a tile's
   // registers are loaded again while it is worked on (32 x 8192 tokens, e2m1: rows of 64 44 us, 58 with
   // 32 tokens; of 128 61, 67). kTwo: for 16-bit rows of 128 those registers spill (4.6 TB/s); 32
-  // tokens in each of two tiles' registers reach 6.0. e4m3 rows of 256 spill with 64 tokens too.
+  // tokens in each of two tiles' registers reach 6.0. e4m3 rows of 256 spill with 64 tokens too. Rows of
+  // 256 in e4m3 and e2m1 spill 8 and 13 registers as they are (5.4 and 4.7 TB/s, rows of 128 5.2 and 4.9).
   static constexpr bool kTwo = ST == AG_KV_16BIT && DP == 128;
   static constexpr int kSub = kTwo || (ST == AG_KV_MXFP8 && DP == 256) ? 2 : 4;
   static constexpr int kTokens = 16 * kSub;
@@ -235,7 +235,7 @@ struct Shared {
   uint32_t last[2];
 };
 
-template <int DT, int ST, int DP>
+template <int DT, int ST, int DP, bool CAP>
 struct Wave {
   typedef Raw<ST, DP> R;
   static constexpr int kAcc = R::kElems * R::kChunks;
@@ -243,7 +243,7 @@ struct Wave {
 
   u32x4 q[R::kSteps];
   f32x4 acc[kAcc];
-  float m, l;  // of this lane's q head; l of this lane's tokens alone
+  float m, l;  // of this lane's q head, m in unit()s; l of this lane's tokens alone
 
   __device__ inline void start(const AttnParams& p, int64_t b, int head0, int n) {
     const int lane = here(threadIdx.x) & 63, col = lane & 15, g = lane >> 4;
@@ -374,28 +374,31 @@ struct Wave {
         st[t] = T16<DT>::mfma(key(r, t, i, g, kw[t]), q[i], st[t]);
   }
 
-  // Scores to weights: st becomes 2^(s - m + up), s the scores in base 2, with m raised and what is
-  // summed rescaled first where needed.
+  // Scores to weights: st, products or capped scores, becomes 2^((st - m) scale + up), with m raised and
+  // what is summed rescaled first where needed.
   __device__ inline void weights(const AttnParams& p, uint64_t there, int up, f32x4 (&st)[R::kSub]) {
     float scale = p.scale;
-    if (p.cap != 0.0f) {
-      // most scores are far below the cap: one branch for the wave leaves the exponential out
+    if constexpr (CAP) {
+      // Most scores are far below the cap: one branch for the wave leaves the exponential out (96 ragged
+      // sequences, e2m1 rows of 64, a cap of 30: 26.9 us, with it 30.7; without a cap 24.5). The other
+      // side is expected less so that what it spills in rows of 256 does not reach the rest (32 x 8192
+      // tokens, e4m3: 206 us, 213).
       scale = 1.0f;
       float most = 0.0f;
 #pragma unroll
       for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
         for (int j = 0; j < 4; ++j) most = fmaxf(most, fabsf(st[t][j]));
-      if (__any(most * p.inv_cap >= kFar)) {
+      if (__builtin_expect(__any(most * p.inv_cap >= kFar), 0)) {
 #pragma unroll
         for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) st[t][j] = capped<false>(p, st[t][j]);
+          for (int j = 0; j < 4; ++j) st[t][j] = in_turn(capped<false>(p, st[t][j]));
       } else {
 #pragma unroll
         for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) st[t][j] = capped<true>(p, st[t][j]);
+          for (int j = 0; j < 4; ++j) st[t][j] = in_turn(capped<true>(p, st[t][j]));
       }
     }
     if (there != kAll) {
@@ -414,10 +417,10 @@ struct Wave {
     for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) top = fmaxf(top, st[t][j]);
-    top = across_max(top) * scale;
-    if (__any(top - m > (float)kRaise)) {
+    top = across_max(top);
+    if (__any((top - m) * scale > (float)kRaise)) {
       const float raised = fmaxf(m, top);
-      const float f = weight(m, raised);
+      const float f = weight(m, raised, scale);
 #pragma unroll
       for (int i = 0; i < kAcc; ++i)
 #pragma unroll
@@ -425,22 +428,14 @@ struct Wave {
       l *= f;
       m = raised;
     }
-    // One multiply-add below takes the score from the exact product, m from a rounded one. Where an ulp
-    // of m is not small beside 1 the scores are rounded first as m was, or weights would be a power of 2
-    // too large or too small, and infinite or 0 from scores of 2^30 on.
-    if (__any(fabsf(m) >= kRounded)) {
-#pragma unroll
-      for (int t = 0; t < R::kSub; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) st[t][j] = scaled(st[t][j], scale);
-      scale = 1.0f;
-    }
-    const float ref = m == -INFINITY ? 0.0f : (float)up - m;
+    // The maximum is taken away before the scale comes in: rounded to base 2 first it would be up to half
+    // an ulp off, from 2^27 on more than all of a weight's head.
+    const float ref = m == -INFINITY ? 0.0f : m, head = (float)up;
 #pragma unroll
     for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        st[t][j] = __builtin_amdgcn_exp2f(fmaf(st[t][j], scale, ref));
+        st[t][j] = __builtin_amdgcn_exp2f(fmaf(st[t][j] - ref, scale, head));
         l += st[t][j];
       }
   }
@@ -513,7 +508,7 @@ struct Wave {
   }
 };
 
-// A partial result: p.rows rows of DP sums, then the rows' maxima (base 2) and sums in pairs.
+// A partial result: p.rows rows of DP sums, then the rows' maxima and sums in pairs.
 template <int DP>
 __device__ inline float* partial(const AttnParams& p, uint32_t slot) {
   return p.partials + (int64_t)slot * (p.rows * (DP + 2));
@@ -560,7 +555,7 @@ __device__ inline void finish(const AttnParams& p, int64_t b, int head, int e, f
   if (e == 0 && p.lse)
     p.lse[b * p.q_heads + head] =
         l == 0.0f ? -INFINITY
-                  : (m + __builtin_amdgcn_logf(ldexpf(l, -up))) * 0.69314718055994531f;
+                  : (m * unit(p) + __builtin_amdgcn_logf(ldexpf(l, -up))) * 0.69314718055994531f;
 }
 
 // A head's part that a workgroup does not have all of.
@@ -599,14 +594,14 @@ __device__ inline void join(const AttnParams& p, Shared<DP, NW>& sh, const Piece
       float top = m;
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) top = fmaxf(top, mi[i]);
-      const float f = weight(m, top);
+      const float f = weight(m, top, unit(p));
       l *= f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) o[w] *= f;
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) {
         if (c + i < count) {
-          const float g = weight(mi[i], top);
+          const float g = weight(mi[i], top, unit(p));
           l = fmaf(g, li[i], l);
 #pragma unroll
           for (int w = 0; w < 4; ++w) o[w] = fmaf(g, x[i][w], o[w]);
@@ -655,8 +650,8 @@ __device__ inline void settle() {
 
 // The waves' results of tokens of one head, put together: the output if that was all of the head,
 // else a partial result in the workgroup's slot.
-template <int DT, int ST, int DP, int NW>
-__device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
+template <int DT, int ST, int DP, bool CAP, int NW>
+__device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP, CAP>& w,
                                Shared<DP, NW>& sh, const Piece& h,
                                uint32_t me) {
   const int tid = here(thread<NW>());
@@ -670,7 +665,7 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
   float m = sh.m[0][col];
 #pragma unroll
   for (int i = 1; i < NW; ++i) m = fmaxf(m, sh.m[i][col]);
-  const float f = weight(w.m, m);
+  const float f = weight(w.m, m, unit(p));
   if (col < h.n) {
     constexpr int kElems = Raw<ST, DP>::kElems;
 #pragma unroll
@@ -693,7 +688,7 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
     f32x4 o = {0, 0, 0, 0};
 #pragma unroll
     for (int i = 0; i < NW; ++i) {
-      rl += sh.l[i][row] * weight(sh.m[i][row], rm);
+      rl += sh.l[i][row] * weight(sh.m[i][row], rm, unit(p));
 #pragma unroll
       for (int k = 0; k < 4; ++k) o[k] += sh.acc[i][row][e + k];
     }
@@ -709,10 +704,10 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP>& w,
 
 // The run of tiles of worker `me` of `wgs` (NW = 4: workgroups, NW = 1: waves), out of the `total` tiles
 // of all sequences and heads.
-template <int DT, int ST, int DP, int NW>
+template <int DT, int ST, int DP, bool CAP, int NW>
 __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me, uint32_t wgs,
                             uint32_t total, uint32_t least, uint32_t whole) {
-  typedef Wave<DT, ST, DP> W;
+  typedef Wave<DT, ST, DP, CAP> W;
   typedef typename W::R R;
   const int tid = thread<NW>(), lane = threadIdx.x & 63;
   const int wave = NW == 1 ? 0 : __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -896,7 +891,7 @@ __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me
   }
 }
 
-template <int DT, int ST, int DP>
+template <int DT, int ST, int DP, bool CAP>
 __global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(AttnParams p) {
   __shared__ union {
     Shared<DP, 4> together;
@@ -936,23 +931,33 @@ __global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(Att
   // 17.6.)
   if (__builtin_expect(tiles * heads > kCus * whole, 0) && 3 * short_ones * heads >= gridDim.x) {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    work<DT, ST, DP, 1>(p, sh.alone[wave], 4 * blockIdx.x + wave, 4 * gridDim.x, tiles * heads,
+    work<DT, ST, DP, CAP, 1>(p, sh.alone[wave], 4 * blockIdx.x + wave, 4 * gridDim.x, tiles * heads,
                         tiles == sequences ? 1 : 2, 1);
   } else {
-    work<DT, ST, DP, 4>(p, sh.together, blockIdx.x, gridDim.x, tiles * heads,
+    work<DT, ST, DP, CAP, 4>(p, sh.together, blockIdx.x, gridDim.x, tiles * heads,
                         tiles > kLong * sequences ? kLeast : 1, whole);
   }
+}
+
+// Kernels with a cap are their own: its code in the others' way costs a call of one token 0.3 us of 5.7, and
+// ragged sequences to 9000, f16, 39.6 us instead of 39.2.
+template <int DT, int ST, int DP>
+void by_cap(const AttnParams& p, int grid, hipStream_t s) {
+  if (p.cap != 0.0f)
+    attn_kernel<DT, ST, DP, true><<<grid, kThreads, 0, s>>>(p);
+  else
+    attn_kernel<DT, ST, DP, false><<<grid, kThreads, 0, s>>>(p);
 }
 
 template <int DT, int ST>
 void by_width(const AttnParams& p, int grid, hipStream_t s) {
   const int dp = attn_padded(p.c.head_dim);
   if (dp == 64)
-    attn_kernel<DT, ST, 64><<<grid, kThreads, 0, s>>>(p);
+    by_cap<DT, ST, 64>(p, grid, s);
   else if (dp == 128)
-    attn_kernel<DT, ST, 128><<<grid, kThreads, 0, s>>>(p);
+    by_cap<DT, ST, 128>(p, grid, s);
   else
-    attn_kernel<DT, ST, 256><<<grid, kThreads, 0, s>>>(p);
+    by_cap<DT, ST, 256>(p, grid, s);
 }
 
 template <int DT>
