@@ -137,29 +137,26 @@ __device__ inline int here(int x) {
   return x;
 }
 
-// cap * tanh(s / cap) of a product x = q . k, in base 2, to a few roundings of the score itself however
-// far the cap is from it. With u = s / cap: from |u| = 1/4 on as (e^2u - 1) / (e^2u + 1), where the
-// subtraction loses two bits at most; below, where it would lose them all, as s times the series of tanh(u) / u, whose
-// first term left out is 8e-9 there. ALL: no lane has a |u| from 1/4 on (or NaN, which the series keeps).
-constexpr float kFar = 0.25f;
+// cap * tanh(s / cap) of a product x = q . k, in base 2, to ten roundings of the score itself however far
+// the cap is from it. With u = s / cap: from |u| = 5/16 on as 1 - 2 / (e^2u + 1), where the subtraction
+// loses two bits at most; below, where it would lose them all, as s times the series of tanh(u) / u, whose
+// first term left out is 8e-8 there. z is 2u in base 2. ALL: no lane has a |u| from 5/16 on (or NaN,
+// which the series keeps).
+constexpr float kPerU = 2.88539008177792681f, kFar = 0.3125f * kPerU;  // 2 log2 e
 template <bool ALL>
 __device__ inline float capped(const AttnParams& p, float x) {
-  const float u = x * p.inv_cap, y = u * u;
-  float r = fmaf(y, 62.0f / 2835.0f, -17.0f / 315.0f);
-  r = fmaf(y, r, 2.0f / 15.0f);
-  r = fmaf(y, r, -1.0f / 3.0f);
+  constexpr float k2 = kPerU * kPerU;
+  const float z = x * p.inv_cap, y = z * z;
+  float r = fmaf(y, 62.0f / 2835.0f / (k2 * k2 * k2 * k2), -17.0f / 315.0f / (k2 * k2 * k2));
+  r = fmaf(y, r, 2.0f / 15.0f / (k2 * k2));
+  r = fmaf(y, r, -1.0f / 3.0f / k2);
   r = fmaf(y, r, 1.0f) * (x * p.scale);
   if constexpr (!ALL) {
-    const float e = __builtin_amdgcn_exp2f(__builtin_amdgcn_fmed3f(u * 2.88539008177792681f, -64.0f, 64.0f));
-    const float far = (e - 1.0f) * __builtin_amdgcn_rcpf(e + 1.0f) * p.cap;
-    r = fabsf(u) >= kFar ? far : r;
+    const float e = __builtin_amdgcn_exp2f(z);
+    const float far = fmaf(__builtin_amdgcn_rcpf(e + 1.0f), -2.0f, 1.0f) * p.cap;
+    r = fabsf(z) >= kFar ? far : r;
   }
   return r;
-}
-
-// Keeps the compiler from working on many of a tile's scores at once, in registers that it spills for.
-__device__ inline float in_turn(float x) {
-  return __builtin_bit_cast(float, here(__builtin_bit_cast(int, x)));
 }
 
 // The head of a sequence's weights by the tokens that are attended to. (The other end, bf16: the
@@ -380,9 +377,9 @@ struct Wave {
     float scale = p.scale;
     if constexpr (CAP) {
       // Most scores are far below the cap: one branch for the wave leaves the exponential out (96 ragged
-      // sequences, e2m1 rows of 64, a cap of 30: 26.9 us, with it 30.7; without a cap 24.5). The other
-      // side is expected less so that what it spills in rows of 256 does not reach the rest (32 x 8192
-      // tokens, e4m3: 206 us, 213).
+      // sequences, e2m1 rows of 64, a cap of 30: 27.0 us, one of 2: 29.7; none: 24.4). The other side is
+      // expected less so that it does not make rows of 256 spill more (32 x 8192 tokens, e2m1, a cap of
+      // 30: 122 us, 128).
       scale = 1.0f;
       float most = 0.0f;
 #pragma unroll
@@ -393,12 +390,12 @@ struct Wave {
 #pragma unroll
         for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) st[t][j] = in_turn(capped<false>(p, st[t][j]));
+          for (int j = 0; j < 4; ++j) st[t][j] = capped<false>(p, st[t][j]);
       } else {
 #pragma unroll
         for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) st[t][j] = in_turn(capped<true>(p, st[t][j]));
+          for (int j = 0; j < 4; ++j) st[t][j] = capped<true>(p, st[t][j]);
       }
     }
     if (there != kAll) {
@@ -927,15 +924,13 @@ __global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(Att
   // 96 ragged sequences (8 kv heads, e2m1, window) 26.5 us, together 45; 256 of 50 tokens (bf16) 15 us,
   // together 20. Else together: 64 of 512 (e2m1) 12 us, by themselves 17; 64 of 8192 (bf16) 355, 376;
   // and where the compute units suffice for a workgroup each: 32 of 200 (bf16, 8 kv heads) 8.0, 13.5.
-  // (Expected not to be, for where the code lies: the other way 131072 tokens in e4m3 take 18.1 us, so
-  // 17.6.)
-  if (__builtin_expect(tiles * heads > kCus * whole, 0) && 3 * short_ones * heads >= gridDim.x) {
+  if (tiles * heads > kCus * whole && 3 * short_ones * heads >= gridDim.x) {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
     work<DT, ST, DP, CAP, 1>(p, sh.alone[wave], 4 * blockIdx.x + wave, 4 * gridDim.x, tiles * heads,
-                        tiles == sequences ? 1 : 2, 1);
+                             tiles == sequences ? 1 : 2, 1);
   } else {
     work<DT, ST, DP, CAP, 4>(p, sh.together, blockIdx.x, gridDim.x, tiles * heads,
-                        tiles > kLong * sequences ? kLeast : 1, whole);
+                             tiles > kLong * sequences ? kLeast : 1, whole);
   }
 }
 

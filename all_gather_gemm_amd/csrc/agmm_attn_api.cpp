@@ -537,9 +537,10 @@ int ag_attn_run(ag_attn_handle* h, const ag_kv_cache* cache, const void* q, int6
   // (finite, and the cap's above 0, at the ends of their ranges)
   p.scale = (float)std::min(scale * log2e, (double)FLT_MAX);
   p.cap = (float)std::min(d.soft_cap * log2e, (double)FLT_MAX);
-  p.inv_cap = d.soft_cap != 0.0f ? (float)std::min(std::max(scale / d.soft_cap, (double)FLT_MIN),
-                                                   (double)FLT_MAX)
-                                 : 0.0f;
+  p.inv_cap = d.soft_cap != 0.0f
+                  ? (float)std::min(std::max(2.0 * log2e * scale / d.soft_cap, (double)FLT_MIN),
+                                    (double)FLT_MAX)
+                  : 0.0f;
   const int64_t grid = std::min<int64_t>(h->num_wgs, std::max<int64_t>(1, tiles * heads * batch));
   ATTN_HIP(agmm::launch_attn(p, d.dtype, d.storage, (int)grid, (hipStream_t)hip_stream));
   return AGMM_OK;

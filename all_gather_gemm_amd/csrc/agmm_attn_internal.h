@@ -84,7 +84,7 @@ struct AttnParams {
   int32_t group, q_groups; // q heads of a kv head; 16-wide groups of them
   int32_t rows;            // of a partial result: q heads in the largest of these groups
   float scale;             // times log2 e
-  float cap, inv_cap;      // cap * log2 e, and scale / cap; cap 0 = none
+  float cap, inv_cap;      // cap * log2 e, and 2 log2 e * scale / cap; cap 0 = none
 };
 
 hipError_t launch_rope(const RopeParams& p, int dtype, int pairing, int gradient, int64_t batch,
