@@ -31,12 +31,13 @@
 // pieces are joined by the last worker to finish one, in the order of the pieces (over 32 of them: 16
 // at a time, and then the groups of 16), so results do not depend on timing.
 //
-// Measured, warm: 64 sequences of 8192 tokens, 64/8 heads of 128, bf16: 355 us, 6.05 TB/s of cache
-// read once (a copy of 4 GiB runs at 4.7 TB/s, reads and writes together); 32 such sequences in e4m3
-// 107 us, 5.2 TB/s, in e2m1 60 us, 4.8 TB/s, where turning codes into values bounds it: half of the
-// vector unit's issue slots, and its waits. One token takes 5.7 us (launch, length, page, keys and
-// values, output: four reads that each wait for the one before), 300 8.4; 2048 tokens of e4m3, which
-// workgroups share and join, 11.4.
+// Measured, warm, the same call again and again: 64 sequences of 8192 tokens, 64/8 heads of 128, bf16:
+// 355 us, 6.05 TB/s of cache read once (a copy of 4 GiB runs at 4.7 TB/s, reads and writes together); 32
+// such sequences in e4m3 107 us, 5.2 TB/s, in e2m1 58 us, 4.9 TB/s, where turning codes into values bounds
+// it: over half of the vector unit's issue slots, and its waits. In a trace one token takes 5.8 us
+// (launch, length, page, keys and values, output: four reads that each wait for the one before), 300 8.5;
+// 2048 tokens of e4m3, which workgroups share and join, 11.4. Times beside the constants and rules below
+// are of the step that chose them, both sides in one run; since then they have moved by up to 3%.
 #include "agmm_attn_device.h"
 
 namespace agmm {
@@ -916,7 +917,8 @@ __global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(Att
       }
     }
   // Heads that all have 2 or all have 3 tiles are not cut: one workgroup's second step costs less than
-  // joining (300 tokens, bf16 8.6 us, cut 9.5; 200 7.6, 9.5). With 4 tiles neither wins (9.7, 9.6).
+  // joining (300 tokens, bf16 8.6 us, cut 9.5; 200 7.6, 9.5). With 4 tiles neither wins (9.7, 9.6). All
+  // shares are alike, so none leaves heads of 2 and of 3 tiles whole both: those are cut as any others.
   const bool twos = short_ones == sequences && tiles == 2 * sequences;
   const uint32_t whole = threes == sequences ? 3 : twos ? 2 : 1;
   // Where many heads have but a tile or two, a workgroup's waves would wait for each other at every
