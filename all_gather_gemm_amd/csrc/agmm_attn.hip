@@ -161,7 +161,8 @@ __device__ inline float capped(const AttnParams& p, float x) {
 }
 
 // The head of a sequence's weights by the tokens that are attended to. (The other end, bf16: the
-// products of values below 2^-122, and 2^-105 of 131072 tokens, are subnormal and may lose bits.)
+// products of values below 2^-122, and 2^-105 of 131072 tokens, are subnormal and lose bits one by one:
+// a sharp softmax over 9000 values is exact to the output's rounding down to 2^-120, to 3% at 2^-126.)
 template <int DT>
 __device__ inline int head_of(int64_t tokens) {
   if (DT == AGMM_F16) return 11;
