@@ -94,6 +94,9 @@ def _declare():
     lib.ag_attn_destroy.argtypes = [vp]
     lib.ag_attn_run.argtypes = [vp, cache, vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, i64, vp,
                                 vp]
+    # of agmm_long.h: the attention with a page table for each kv head
+    lib.ag_attn_run_heads.argtypes = [vp, cache, vp, i64, i64, vp, i64, i64, i64, vp, i64, vp, i64, i64, vp,
+                                      vp]
 
 
 _declare()
@@ -374,8 +377,9 @@ class DecodeAttention:
     """Attention of one new token of every sequence over a PagedCache (ag_attn_desc).
 
     run(q, cache, page_table, lens): q [batch, q_heads, head_dim]; page_table int32 [batch,
-    pages]; lens int32 [batch], the new token counted in. Returns out like q, or (out, lse) with
-    lse float32 [batch, q_heads]. A handle serves one stream at a time."""
+    pages], or [batch, kv_heads, pages], a table for each kv head; lens int32 [batch], the new token
+    counted in. Returns out like q, or (out, lse) with lse float32 [batch, q_heads]. A handle serves
+    one stream at a time."""
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, dtype: str = "bf16",
                  storage: str = "16bit", scale: float = 0.0, window: int = 0,
@@ -407,7 +411,9 @@ class DecodeAttention:
             stream=None):
         batch, device = q.shape[0], cache.device
         _tensor(q, "q", self.torch_dtype, (batch, self.q_heads, self.head_dim), device)
+        heads = page_table.dim() == 3
         _tensor(page_table, "page_table", torch.int32,
+                (batch, self.desc.kv_heads, page_table.shape[2]) if heads else
                 (batch, page_table.shape[1] if page_table.dim() == 2 else None), device)
         _tensor(lens, "lens", torch.int32, (batch,), device)
         where = _stream(stream, device.index)
@@ -417,6 +423,14 @@ class DecodeAttention:
             _tensor(out, "out", self.torch_dtype, q.shape, device)
         lse = _empty(q, (batch, self.q_heads), torch.float32, stream) if return_lse else None
         qs, os = q.stride(), out.stride()
+        if heads:
+            ts = page_table.stride()
+            rc = lib.ag_attn_run_heads(self.handle, cache._ref, q.data_ptr(), qs[0], qs[1],
+                                       page_table.data_ptr(), ts[0], ts[1], page_table.shape[2],
+                                       lens.data_ptr(), batch, out.data_ptr(), os[0], os[1],
+                                       lse.data_ptr() if return_lse else None, where)
+            _checked(rc, "ag_attn_run_heads")
+            return (out, lse) if return_lse else out
         rc = lib.ag_attn_run(self.handle, cache._ref, q.data_ptr(), qs[0], qs[1],
                              page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
                              lens.data_ptr(), batch, out.data_ptr(), os[0], os[1],

@@ -13,6 +13,13 @@ using agmm::AttnParams;
 using agmm::CacheParams;
 using agmm::CacheView;
 using agmm::RopeParams;
+using agmm::align256;
+using agmm::aligned;
+using agmm::check_attn;
+using agmm::check_cache;
+using agmm::check_device;
+using agmm::hip_failed;
+using agmm::view_of;
 
 struct ag_rope_handle {
   ag_rope_desc desc;
@@ -27,26 +34,12 @@ struct ag_attn_handle {
   bool own_ws;
 };
 
-namespace {
-
-constexpr double kTwoPi = 6.283185307179586476925286766559;
-constexpr int kRotMax = 512;
-constexpr int kDefaultCus = 256;
-constexpr uint32_t kMaxThreads = 1u << 30;  // of one launch, so that thread numbers fit FastDiv
+namespace agmm {
 
 int hip_failed(hipError_t e) {
-  agmm::set_last_hip_error((int)e);
+  set_last_hip_error((int)e);
   return e == hipErrorOutOfMemory ? AGMM_ERR_OOM : AGMM_ERR_HIP;
 }
-#define ATTN_HIP(x)                               \
-  do {                                            \
-    const hipError_t e_ = (x);                    \
-    if (e_ != hipSuccess) return hip_failed(e_);  \
-  } while (0)
-
-bool aligned(const void* p, uintptr_t n) { return p != nullptr && ((uintptr_t)p & (n - 1)) == 0; }
-
-int64_t align256(int64_t x) { return (x + 255) & ~(int64_t)255; }
 
 // The handle's device has to be the current one.
 int check_device(int device) {
@@ -54,6 +47,79 @@ int check_device(int device) {
   ATTN_HIP(hipGetDevice(&cur));
   return cur == device ? AGMM_OK : AGMM_ERR_WRONG_DEVICE;
 }
+
+int check_cache(const ag_kv_cache* c) {
+  if (!c) return AGMM_ERR_INVALID_ARG;
+  if (c->dtype != AGMM_F16 && c->dtype != AGMM_BF16) return AGMM_ERR_INVALID_ARG;
+  if (c->storage < AG_KV_16BIT || c->storage > AG_KV_MXFP4) return AGMM_ERR_INVALID_ARG;
+  if (c->head_dim < 1 || c->kv_heads < 1 || c->page_size < 1 || c->num_pages < 0)
+    return AGMM_ERR_INVALID_ARG;
+  if (c->head_dim > 256 || c->head_dim % (c->storage == AG_KV_16BIT ? 8 : 32))
+    return AGMM_ERR_UNSUPPORTED;
+  if (c->num_pages >= ((int64_t)1 << 31) || c->num_pages * c->page_size >= ((int64_t)1 << 31))
+    return AGMM_ERR_UNSUPPORTED;
+  if (c->page_stride < 0 || c->head_stride < 0 || c->row_stride < 0 ||
+      (c->page_stride | c->head_stride | c->row_stride) & 15)
+    return AGMM_ERR_INVALID_ARG;
+  const int64_t wide = (int64_t)1 << 32;
+  if (c->page_stride >= wide || c->row_stride >= wide) return AGMM_ERR_UNSUPPORTED;
+  if (c->num_pages > 0 && (!aligned(c->k, 16) || !aligned(c->v, 16))) return AGMM_ERR_INVALID_ARG;
+  if (c->storage != AG_KV_16BIT) {
+    if (c->scale_page < 0 || c->scale_head < 0 || c->scale_row < 0 ||
+        (c->scale_page | c->scale_head | c->scale_row) & 3)
+      return AGMM_ERR_INVALID_ARG;
+    if (c->scale_page >= wide || c->scale_row >= wide) return AGMM_ERR_UNSUPPORTED;
+    if (c->num_pages > 0 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
+      return AGMM_ERR_INVALID_ARG;
+  } else if (c->k_scale || c->v_scale) {
+    return AGMM_ERR_INVALID_ARG;
+  }
+  return AGMM_OK;
+}
+
+CacheView view_of(const ag_kv_cache& c) {
+  CacheView v;
+  v.k = (char*)c.k;
+  v.v = (char*)c.v;
+  v.ks = (char*)c.k_scale;
+  v.vs = (char*)c.v_scale;
+  v.page = (uint32_t)c.page_stride;
+  v.head = c.head_stride;
+  v.row = (uint32_t)c.row_stride;
+  v.s_page = (uint32_t)c.scale_page;
+  v.s_head = c.scale_head;
+  v.s_row = (uint32_t)c.scale_row;
+  v.page_size = fast_div((uint32_t)c.page_size);
+  v.rows = (uint32_t)(c.num_pages * c.page_size);
+  v.head_dim = c.head_dim;
+  v.kv_heads = c.kv_heads;
+  return v;
+}
+
+int check_attn(const ag_attn_desc* d) {
+  if (!d) return AGMM_ERR_INVALID_ARG;
+  if (d->dtype != AGMM_F16 && d->dtype != AGMM_BF16) return AGMM_ERR_INVALID_ARG;
+  if (d->storage < AG_KV_16BIT || d->storage > AG_KV_MXFP4) return AGMM_ERR_INVALID_ARG;
+  if (d->head_dim < 1 || d->q_heads < 1 || d->kv_heads < 1 || d->q_heads % d->kv_heads ||
+      d->window < 0 || d->num_wgs < 0 || d->num_wgs > kAttnMaxWgs)
+    return AGMM_ERR_INVALID_ARG;
+  if (!(d->scale >= 0.0f) || !isfinite(d->scale) || !(d->soft_cap >= 0.0f) ||
+      !isfinite(d->soft_cap))
+    return AGMM_ERR_INVALID_ARG;
+  if (d->head_dim > 256 || d->head_dim % (d->storage == AG_KV_16BIT ? 8 : 32))
+    return AGMM_ERR_UNSUPPORTED;
+  if (d->q_heads > (1 << 20)) return AGMM_ERR_UNSUPPORTED;
+  return AGMM_OK;
+}
+
+}  // namespace agmm
+
+namespace {
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+constexpr int kRotMax = 512;
+constexpr int kDefaultCus = 256;
+constexpr uint32_t kMaxThreads = 1u << 30;  // of one launch, so that thread numbers fit FastDiv
 
 bool valid_rope(const ag_rope_desc* d) {
   if (!d || (d->dtype != AGMM_F16 && d->dtype != AGMM_BF16)) return false;
@@ -127,54 +193,6 @@ void rope_units(const ag_rope_desc& d, int64_t heads, RopeParams* p) {
   p->heads = agmm::fast_div((uint32_t)heads);
 }
 
-int check_cache(const ag_kv_cache* c) {
-  if (!c) return AGMM_ERR_INVALID_ARG;
-  if (c->dtype != AGMM_F16 && c->dtype != AGMM_BF16) return AGMM_ERR_INVALID_ARG;
-  if (c->storage < AG_KV_16BIT || c->storage > AG_KV_MXFP4) return AGMM_ERR_INVALID_ARG;
-  if (c->head_dim < 1 || c->kv_heads < 1 || c->page_size < 1 || c->num_pages < 0)
-    return AGMM_ERR_INVALID_ARG;
-  if (c->head_dim > 256 || c->head_dim % (c->storage == AG_KV_16BIT ? 8 : 32))
-    return AGMM_ERR_UNSUPPORTED;
-  if (c->num_pages >= ((int64_t)1 << 31) || c->num_pages * c->page_size >= ((int64_t)1 << 31))
-    return AGMM_ERR_UNSUPPORTED;
-  if (c->page_stride < 0 || c->head_stride < 0 || c->row_stride < 0 ||
-      (c->page_stride | c->head_stride | c->row_stride) & 15)
-    return AGMM_ERR_INVALID_ARG;
-  const int64_t wide = (int64_t)1 << 32;
-  if (c->page_stride >= wide || c->row_stride >= wide) return AGMM_ERR_UNSUPPORTED;
-  if (c->num_pages > 0 && (!aligned(c->k, 16) || !aligned(c->v, 16))) return AGMM_ERR_INVALID_ARG;
-  if (c->storage != AG_KV_16BIT) {
-    if (c->scale_page < 0 || c->scale_head < 0 || c->scale_row < 0 ||
-        (c->scale_page | c->scale_head | c->scale_row) & 3)
-      return AGMM_ERR_INVALID_ARG;
-    if (c->scale_page >= wide || c->scale_row >= wide) return AGMM_ERR_UNSUPPORTED;
-    if (c->num_pages > 0 && (!aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
-      return AGMM_ERR_INVALID_ARG;
-  } else if (c->k_scale || c->v_scale) {
-    return AGMM_ERR_INVALID_ARG;
-  }
-  return AGMM_OK;
-}
-
-CacheView view_of(const ag_kv_cache& c) {
-  CacheView v;
-  v.k = (char*)c.k;
-  v.v = (char*)c.v;
-  v.ks = (char*)c.k_scale;
-  v.vs = (char*)c.v_scale;
-  v.page = (uint32_t)c.page_stride;
-  v.head = c.head_stride;
-  v.row = (uint32_t)c.row_stride;
-  v.s_page = (uint32_t)c.scale_page;
-  v.s_head = c.scale_head;
-  v.s_row = (uint32_t)c.scale_row;
-  v.page_size = agmm::fast_div((uint32_t)c.page_size);
-  v.rows = (uint32_t)(c.num_pages * c.page_size);
-  v.head_dim = c.head_dim;
-  v.kv_heads = c.kv_heads;
-  return v;
-}
-
 // Tokens of one launch for `per_token` threads each.
 int64_t tokens_per_launch(uint64_t per_token) {
   return std::max<int64_t>(1, (int64_t)(kMaxThreads / std::max<uint64_t>(1, per_token)));
@@ -208,22 +226,6 @@ CacheParams traffic_of(const ag_kv_cache& c, const Traffic& t, int64_t t0, int64
   return p;
 }
 
-int check_attn(const ag_attn_desc* d) {
-  if (!d) return AGMM_ERR_INVALID_ARG;
-  if (d->dtype != AGMM_F16 && d->dtype != AGMM_BF16) return AGMM_ERR_INVALID_ARG;
-  if (d->storage < AG_KV_16BIT || d->storage > AG_KV_MXFP4) return AGMM_ERR_INVALID_ARG;
-  if (d->head_dim < 1 || d->q_heads < 1 || d->kv_heads < 1 || d->q_heads % d->kv_heads ||
-      d->window < 0 || d->num_wgs < 0 || d->num_wgs > agmm::kAttnMaxWgs)
-    return AGMM_ERR_INVALID_ARG;
-  if (!(d->scale >= 0.0f) || !isfinite(d->scale) || !(d->soft_cap >= 0.0f) ||
-      !isfinite(d->soft_cap))
-    return AGMM_ERR_INVALID_ARG;
-  if (d->head_dim > 256 || d->head_dim % (d->storage == AG_KV_16BIT ? 8 : 32))
-    return AGMM_ERR_UNSUPPORTED;
-  if (d->q_heads > (1 << 20)) return AGMM_ERR_UNSUPPORTED;
-  return AGMM_OK;
-}
-
 // Workgroups of a run: as many as the compute units hold at once.
 int workgroups(const ag_attn_desc& d, int num_cus) {
   return d.num_wgs ? d.num_wgs
@@ -240,6 +242,80 @@ int64_t attn_bytes(const ag_attn_desc& d, int wgs) {
 }
 
 }  // namespace
+
+namespace agmm {
+
+const ag_attn_desc& attn_desc(const ag_attn_handle* h) { return h->desc; }
+int attn_workgroups(const ag_attn_handle* h) { return h->num_wgs; }
+
+void attn_scales(const ag_attn_desc& d, AttnParams* out) {
+  AttnParams& p = *out;
+  const double log2e = 1.4426950408889634073599;
+  const double scale = d.scale != 0.0f ? d.scale : 1.0 / sqrt((double)d.head_dim);
+  // (finite, and the cap's above 0, at the ends of their ranges)
+  p.scale = (float)std::min(scale * log2e, (double)FLT_MAX);
+  p.cap = (float)std::min(d.soft_cap * log2e, (double)FLT_MAX);
+  p.inv_cap = d.soft_cap != 0.0f
+                  ? (float)std::min(std::max(2.0 * log2e * scale / d.soft_cap, (double)FLT_MIN),
+                                    (double)FLT_MAX)
+                  : 0.0f;
+}
+
+int attn_params(ag_attn_handle* h, const ag_kv_cache* cache, const void* q, int64_t q_batch, int64_t q_head,
+                const int32_t* page_table, int64_t table_row, int64_t table_len, const int32_t* lens,
+                int64_t batch, void* out, int64_t o_batch, int64_t o_head, float* lse,
+                AttnParams* out_params, int* grid) {
+  if (!h) return AGMM_ERR_INVALID_ARG;
+  int rc = check_cache(cache);
+  if (rc != AGMM_OK) return rc;
+  const ag_attn_desc& d = h->desc;
+  if (cache->dtype != d.dtype || cache->storage != d.storage || cache->head_dim != d.head_dim ||
+      cache->kv_heads != d.kv_heads || batch < 0 || table_len < 0)
+    return AGMM_ERR_INVALID_ARG;
+  *grid = 0;
+  if (batch == 0) return AGMM_OK;
+  if (!aligned(q, 2) || !aligned(out, 2) || !aligned(lens, 4) ||
+      (table_len > 0 && !aligned(page_table, 4)) || (lse && !aligned(lse, 4)))
+    return AGMM_ERR_INVALID_ARG;
+  const int64_t most = (int64_t)1 << 31;
+  if (batch >= most || table_len >= most || table_len * cache->page_size >= most)
+    return AGMM_ERR_UNSUPPORTED;
+  AttnParams& p = *out_params;
+  memset(&p, 0, sizeof(p));
+  p.c = view_of(*cache);
+  p.group = d.q_heads / d.kv_heads;
+  p.q_groups = (p.group + 15) / 16;
+  p.rows = attn_rows(d);
+  p.capacity = cache->num_pages > 0 ? (int32_t)(table_len * cache->page_size) : 0;
+  // every tile has a 32-bit number
+  const int64_t seen = d.window ? std::min(d.window, (int64_t)p.capacity) : p.capacity;
+  const int64_t tiles = (seen + 15 + kAttnTile - 1) / kAttnTile;
+  const int64_t heads = (int64_t)d.kv_heads * p.q_groups;
+  if ((double)tiles * heads * batch >= (double)most) return AGMM_ERR_UNSUPPORTED;
+  rc = check_device(h->device);
+  if (rc != AGMM_OK) return rc;
+  p.q = (const uint16_t*)q;
+  p.out = (uint16_t*)out;
+  p.lse = lse;
+  p.table = page_table;
+  p.lens = lens;
+  p.q_batch = q_batch;
+  p.q_head = q_head;
+  p.o_batch = o_batch;
+  p.o_head = o_head;
+  p.table_row = table_row;
+  p.partials = (float*)h->ws;
+  p.counters = (uint32_t*)(h->ws + partials_bytes(d, h->num_wgs));
+  p.window = d.window;
+  p.num_pages = (int32_t)cache->num_pages;
+  p.batch = (int32_t)batch;
+  p.q_heads = d.q_heads;
+  attn_scales(d, &p);
+  *grid = (int)std::min<int64_t>(h->num_wgs, std::max<int64_t>(1, tiles * heads * batch));
+  return AGMM_OK;
+}
+
+}  // namespace agmm
 
 extern "C" {
 
@@ -488,61 +564,12 @@ int ag_attn_run(ag_attn_handle* h, const ag_kv_cache* cache, const void* q, int6
                 int64_t q_head, const int32_t* page_table, int64_t table_row, int64_t table_len,
                 const int32_t* lens, int64_t batch, void* out, int64_t o_batch, int64_t o_head,
                 float* lse, void* hip_stream) {
-  if (!h) return AGMM_ERR_INVALID_ARG;
-  int rc = check_cache(cache);
-  if (rc != AGMM_OK) return rc;
-  const ag_attn_desc& d = h->desc;
-  if (cache->dtype != d.dtype || cache->storage != d.storage || cache->head_dim != d.head_dim ||
-      cache->kv_heads != d.kv_heads || batch < 0 || table_len < 0)
-    return AGMM_ERR_INVALID_ARG;
-  if (batch == 0) return AGMM_OK;
-  if (!aligned(q, 2) || !aligned(out, 2) || !aligned(lens, 4) ||
-      (table_len > 0 && !aligned(page_table, 4)) || (lse && !aligned(lse, 4)))
-    return AGMM_ERR_INVALID_ARG;
-  const int64_t most = (int64_t)1 << 31;
-  if (batch >= most || table_len >= most || table_len * cache->page_size >= most)
-    return AGMM_ERR_UNSUPPORTED;
   AttnParams p;
-  memset(&p, 0, sizeof(p));
-  p.c = view_of(*cache);
-  p.group = d.q_heads / d.kv_heads;
-  p.q_groups = (p.group + 15) / 16;
-  p.rows = attn_rows(d);
-  p.capacity = cache->num_pages > 0 ? (int32_t)(table_len * cache->page_size) : 0;
-  // every tile has a 32-bit number
-  const int64_t seen = d.window ? std::min(d.window, (int64_t)p.capacity) : p.capacity;
-  const int64_t tiles = (seen + 15 + agmm::kAttnTile - 1) / agmm::kAttnTile;
-  const int64_t heads = (int64_t)d.kv_heads * p.q_groups;
-  if ((double)tiles * heads * batch >= (double)most) return AGMM_ERR_UNSUPPORTED;
-  rc = check_device(h->device);
-  if (rc != AGMM_OK) return rc;
-  p.q = (const uint16_t*)q;
-  p.out = (uint16_t*)out;
-  p.lse = lse;
-  p.table = page_table;
-  p.lens = lens;
-  p.q_batch = q_batch;
-  p.q_head = q_head;
-  p.o_batch = o_batch;
-  p.o_head = o_head;
-  p.table_row = table_row;
-  p.partials = (float*)h->ws;
-  p.counters = (uint32_t*)(h->ws + partials_bytes(d, h->num_wgs));
-  p.window = d.window;
-  p.num_pages = (int32_t)cache->num_pages;
-  p.batch = (int32_t)batch;
-  p.q_heads = d.q_heads;
-  const double log2e = 1.4426950408889634073599;
-  const double scale = d.scale != 0.0f ? d.scale : 1.0 / sqrt((double)d.head_dim);
-  // (finite, and the cap's above 0, at the ends of their ranges)
-  p.scale = (float)std::min(scale * log2e, (double)FLT_MAX);
-  p.cap = (float)std::min(d.soft_cap * log2e, (double)FLT_MAX);
-  p.inv_cap = d.soft_cap != 0.0f
-                  ? (float)std::min(std::max(2.0 * log2e * scale / d.soft_cap, (double)FLT_MIN),
-                                    (double)FLT_MAX)
-                  : 0.0f;
-  const int64_t grid = std::min<int64_t>(h->num_wgs, std::max<int64_t>(1, tiles * heads * batch));
-  ATTN_HIP(agmm::launch_attn(p, d.dtype, d.storage, (int)grid, (hipStream_t)hip_stream));
+  int grid = 0;
+  const int rc = agmm::attn_params(h, cache, q, q_batch, q_head, page_table, table_row, table_len, lens, batch,
+                                   out, o_batch, o_head, lse, &p, &grid);
+  if (rc != AGMM_OK || grid == 0) return rc;
+  ATTN_HIP(agmm::launch_attn(p, h->desc.dtype, h->desc.storage, grid, (hipStream_t)hip_stream));
   return AGMM_OK;
 }
 

@@ -1,0 +1,15 @@
+// The kernels of the attention of one new token: agmm_attn_kernel.h, with a page table for each kv head and shared
+// prefixes.
+#include "agmm_attn_kernel.h"
+
+namespace agmm {
+
+hipError_t launch_attn_ext(const AttnParams& p, int dtype, int storage, int grid, hipStream_t s) {
+  if (dtype == AGMM_F16)
+    by_storage<AGMM_F16, true>(p, storage, grid, s);
+  else
+    by_storage<AGMM_BF16, true>(p, storage, grid, s);
+  return hipGetLastError();
+}
+
+}  // namespace agmm

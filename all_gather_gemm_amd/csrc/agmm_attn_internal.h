@@ -67,6 +67,27 @@ struct CacheParams {
   uint32_t q_blocks;         // leading workgroups that rotate q (RopeParams beside)
 };
 
+// What a prefix's kernel leaves for the sequences that share it (agmm_prefix.hip). Its rows are the q heads of
+// one kv head of all the sequences, kPrefixRows of them a strip; a strip's tiles of tokens, strip after
+// strip, are cut into runs of `quota`, one for each workgroup. Workgroup w's piece of strip s is in slot
+// w + s.
+constexpr int kPrefixRows = 128;
+struct PrefixGroup {
+  int32_t first, end;       // sequences
+  uint32_t tiles;           // of a strip
+  uint32_t row_tiles;       // strips of a kv head
+  uint32_t strip0, tile0;   // the first strip and tile
+  int32_t up;               // head of the weights
+  uint32_t quota;
+};
+struct PrefixView {
+  PrefixGroup* info;        // [groups]
+  float* sums;              // [slots][padded head_dim / 8][kPrefixRows][8]
+  float* stats;             // [slots][kPrefixRows][2]: maximum and sum
+  uint32_t groups;          // 0: no prefixes
+};
+constexpr int64_t prefix_at(int64_t row, int e) { return ((int64_t)(e / 8) * kPrefixRows + row) * 8 + e % 8; }
+
 struct AttnParams {
   CacheView c;
   const uint16_t* q;
@@ -85,6 +106,9 @@ struct AttnParams {
   int32_t rows;            // of a partial result: q heads in the largest of these groups
   float scale;             // times log2 e
   float cap, inv_cap;      // cap * log2 e, and 2 log2 e * scale / cap; cap 0 = none
+  // launch_attn_ext alone
+  int64_t table_head;      // from one kv head's page table to the next
+  PrefixView prefix;
 };
 
 hipError_t launch_rope(const RopeParams& p, int dtype, int pairing, int gradient, int64_t batch,
@@ -103,5 +127,28 @@ constexpr int attn_per_cu(int storage, int padded) {
   return storage == AG_KV_16BIT && padded == 256 ? 1 : 2;
 }
 hipError_t launch_attn(const AttnParams& p, int dtype, int storage, int grid, hipStream_t s);
+hipError_t launch_attn_ext(const AttnParams& p, int dtype, int storage, int grid, hipStream_t s);
+
+// Of agmm_attn_api.cpp, for the rest of the host side.
+int hip_failed(hipError_t e);                // remembers it; the ABI's code for it
+int check_device(int device);                // has to be the current one
+int check_cache(const ag_kv_cache* c);
+int check_attn(const ag_attn_desc* d);
+CacheView view_of(const ag_kv_cache& c);
+void attn_scales(const ag_attn_desc& d, AttnParams* p);
+// A run's arguments, checked, and its grid (0: nothing to do).
+int attn_params(ag_attn_handle* h, const ag_kv_cache* cache, const void* q, int64_t q_batch, int64_t q_head,
+                const int32_t* page_table, int64_t table_row, int64_t table_len, const int32_t* lens,
+                int64_t batch, void* out, int64_t o_batch, int64_t o_head, float* lse, AttnParams* p,
+                int* grid);
+const ag_attn_desc& attn_desc(const ag_attn_handle* h);
+int attn_workgroups(const ag_attn_handle* h);
+inline bool aligned(const void* p, uintptr_t n) { return p != nullptr && ((uintptr_t)p & (n - 1)) == 0; }
+inline int64_t align256(int64_t x) { return (x + 255) & ~(int64_t)255; }
+#define ATTN_HIP(x)                                    \
+  do {                                                 \
+    const hipError_t e_ = (x);                         \
+    if (e_ != hipSuccess) return agmm::hip_failed(e_); \
+  } while (0)
 
 }  // namespace agmm

@@ -1,0 +1,518 @@
+// gfx950 kernels of the page index, of choosing what is kept, and of moving rows (agmm_long.h).
+//
+// All of them read a stream of bytes and compute little on each, so many pages or tokens are bound by memory
+// bandwidth and few by the chain of a launch, the length, the page and its rows.
+#include "agmm_attn_kernel.h"
+#include "agmm_long_internal.h"
+
+namespace agmm {
+namespace {
+
+// ---------------------------------------------------------------- the index's entries
+
+template <int DT>
+__device__ inline float value_of(uint32_t w, int half) {
+  return half ? T16<DT>::hi(w) : T16<DT>::lo(w);
+}
+
+// Sum of whole numbers, or another combination, over the N lanes (8, 16 or 32) that work on one page.
+template <int N, class F>
+__device__ inline uint32_t over_lanes(uint32_t x, F f) {
+  x = f(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xf, 0xf, true));   // pairs
+  x = f(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xf, 0xf, true));   // fours
+  x = f(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xf, 0xf, true));  // eights, mirrored
+  if constexpr (N >= 16) x = f(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x140, 0xf, 0xf, true));
+  if constexpr (N >= 32) x = f(x, (uint32_t)__shfl_xor((int)x, 16));
+  return x;
+}
+__device__ inline uint32_t as_u(float x) { return __builtin_bit_cast(uint32_t, x); }
+__device__ inline float as_f(uint32_t x) { return __builtin_bit_cast(float, x); }
+template <int N>
+__device__ inline float max_over_lanes(float x) {
+  return as_f(over_lanes<N>(as_u(x), [](uint32_t a, uint32_t b) { return as_u(fmaxf(as_f(a), as_f(b))); }));
+}
+
+// 127 + the least e from -126 on with most <= 127 * 2^e, for most >= 0 and finite. With most = x 2^k, 1 <= x
+// < 2, 127 * 2^(k - 6) is enough for x <= 127 / 64.
+__device__ inline uint32_t least_exponent(float most) {
+  const uint32_t w = as_u(most);
+  const int e = (int)(w >> 23) - 6 + ((w & 0x7fffffu) > 0x7e0000u ? 1 : 0);
+  return (uint32_t)max(e, 1);
+}
+// 2^(127 - s), that is 1 / 2^e, exactly: s is 1..248.
+__device__ inline float one_over(uint32_t s) { return as_f((254u - s) << 23); }
+
+// A wave makes one entry at a time: LC = padded dim / 8 lanes on 8 elements each, 64 / LC rows at once.
+template <int DT, int ST, int LC>
+__global__ __launch_bounds__(kThreads) void update_kernel(IndexParams p) {
+  constexpr int kRows = 64 / LC, kUnroll = 4;
+  const int lane = threadIdx.x & 63, c = lane % LC, r0 = lane / LC;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const uint32_t bh = blockIdx.x / (uint32_t)p.splits, split = blockIdx.x - bh * (uint32_t)p.splits;
+  const int64_t b = bh / (uint32_t)p.c.kv_heads;
+  const int kv = (int)(bh - (uint32_t)b * p.c.kv_heads);
+  const int32_t ps = (int32_t)p.c.page_size.d, hd = p.c.head_dim;
+  const int64_t len = min((int64_t)max(p.lens[b], 0), (int64_t)p.pages * ps);
+  const int32_t start = p.starts ? max(p.starts[b], 0) : 0;
+  const uint32_t first = (uint32_t)start / p.c.page_size, end = (uint32_t)((len + ps - 1) / ps);
+  if (start >= len) return;
+  const bool in = 8 * c < hd;
+  const int e = in ? 8 * c : 0;
+  const int bytes = ST == AG_KV_16BIT ? 2 * e : ST == AG_KV_MXFP8 ? e : e / 2;
+  constexpr int kWords = ST == AG_KV_16BIT ? 4 : ST == AG_KV_MXFP8 ? 2 : 1;
+  for (uint32_t j = first + split * 4 + wave; j < end; j += 4 * p.splits) {
+    const int32_t page = p.table[b * p.table_row + j];
+    if ((uint32_t)page >= (uint32_t)p.num_pages) continue;
+    const int used = (int)min((int64_t)ps, len - (int64_t)j * ps);
+    float hi[8], lo[8];
+    bool odd = false;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      hi[k] = -INFINITY;
+      lo[k] = INFINITY;
+    }
+    for (int r = r0; r - r0 < used; r += kUnroll * kRows) {
+      uint32_t w[kUnroll][kWords], s[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {   // (past the last row: the last again)
+        const uint32_t row = (uint32_t)min(r + u * kRows, used - 1);
+        load_words<kWords>(w[u], p.c.k + kv * p.c.head + row_at(p.c, page, row) + bytes);
+        if (ST != AG_KV_16BIT)
+          s[u] = *(const uint8_t*)(p.c.ks + kv * p.c.s_head + scales_at(p.c, page, row) + e / 32);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        u32x4 x;
+        if constexpr (ST == AG_KV_16BIT)
+          x = u32x4{w[u][0], w[u][1], w[u][2], w[u][3]};
+        else if constexpr (ST == AG_KV_MXFP8)
+          x = from_fp8x8<DT>(w[u][0], w[u][1], scale_of(s[u]));
+        else
+          x = from_fp4x8<DT>(w[u][0], scale_of(s[u]));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float f = value_of<DT>(x[k / 2], k % 2);
+          odd = odd || !(fabsf(f) < INFINITY);
+          hi[k] = fmaxf(hi[k], f);
+          lo[k] = fminf(lo[k], f);
+        }
+      }
+    }
+    float most = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+#pragma unroll
+      for (int d = LC; d < 64; d *= 2) {
+        hi[k] = fmaxf(hi[k], __shfl_xor(hi[k], d));
+        lo[k] = fminf(lo[k], __shfl_xor(lo[k], d));
+      }
+      most = fmaxf(most, fmaxf(fabsf(hi[k]), fabsf(lo[k])));
+    }
+    const bool bad = __ballot(odd && in) != 0;
+    const uint32_t s = bad ? 255u : least_exponent(max_over_lanes<LC>(in ? most : 0.0f));
+    const float unit = bad ? 0.0f : one_over(s);
+    uint32_t up[2] = {0, 0}, down[2] = {0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // (a product that underflows is still above 0, or below)
+      int h = max((int)ceilf(hi[k] * unit), hi[k] > 0.0f ? 1 : -128);
+      int l = min((int)floorf(lo[k] * unit), lo[k] < 0.0f ? -1 : 128);
+      if (bad) h = l = 0;
+      up[k / 4] |= (uint32_t)(h & 255) << (8 * (k % 4));
+      down[k / 4] |= (uint32_t)(l & 255) << (8 * (k % 4));
+    }
+    const int64_t entry = (int64_t)page * p.c.kv_heads + kv;
+    if (in && r0 == 0) {
+      *reinterpret_cast<u32x2*>(p.codes + entry * 2 * hd + e) = u32x2{up[0], up[1]};
+      *reinterpret_cast<u32x2*>(p.codes + entry * 2 * hd + hd + e) = u32x2{down[0], down[1]};
+    }
+    if (lane == 0) p.scales[entry] = (uint8_t)s;
+  }
+}
+
+// ---------------------------------------------------------------- scores
+
+// Floats as whole numbers of the same order, from 1 on. -0 is 0; NaN, and what comes before all others, is
+// kMost; 0 is left for what cannot be chosen and kForced for what has to be.
+constexpr uint32_t kMost = 0xfffffffeu, kForced = 0xffffffffu;
+__device__ inline uint32_t order_key(float x) {
+  if (!(x == x)) return kMost;
+  const uint32_t w = as_u(x + 0.0f);
+  return w >> 31 ? ~w : w | 0x80000000u;
+}
+
+// The scores of a sequence's pages for one kv head. The sum over the q heads is taken first: a page's codes are
+// multiplied by a_d = sum of the positive codes of element d, and by that of the negative ones, which are
+// within 127 * 128; in two parts of 8 bits, 128 x + y, they go through v_dot4_i32_i8. LC lanes have 16 codes each.
+template <int DT, int LC>
+__global__ __launch_bounds__(kThreads) void score_kernel(IndexParams p) {
+  constexpr int kPages = 64 / LC, kUnroll = 4;
+  const int lane = threadIdx.x & 63, c = lane % LC, r0 = lane / LC;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const uint32_t bh = blockIdx.x / (uint32_t)p.splits, split = blockIdx.x - bh * (uint32_t)p.splits;
+  const int64_t b = bh / (uint32_t)p.c.kv_heads;
+  const int kv = (int)(bh - (uint32_t)b * p.c.kv_heads);
+  const int32_t ps = (int32_t)p.c.page_size.d, hd = p.c.head_dim, blocks = hd / 8;
+  const int64_t len = min((int64_t)max(p.lens[b], 0), (int64_t)p.pages * ps);
+  const int32_t end = (int32_t)((len + ps - 1) / ps);
+  const int32_t stride = (p.pages + 3) & ~3;
+  uint32_t* keys = p.keys + (int64_t)bh * stride;
+  const int32_t step = (int32_t)p.splits * 4 * kPages;
+  int32_t j0 = (int32_t)(split * 4 + wave) * kPages;
+  if (j0 >= end) return;
+
+  const bool in = 2 * c < 2 * blocks;   // a chunk of 16 codes is two blocks of 8
+  const uint16_t* q = p.q + b * p.q_batch + (int64_t)kv * p.group * p.q_head;
+  float most = 0.0f;
+  for (int h = 0; h < p.group; ++h)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int block = 2 * c + k;
+      if (!in) continue;
+      const u32x4 x = load16(q + h * p.q_head + 8 * (block < blocks ? block : block - blocks));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float f = fabsf(value_of<DT>(x[i / 2], i % 2));
+        most = fmaxf(most, f < INFINITY ? f : 0.0f);
+      }
+    }
+  const float unit = one_over(least_exponent(max_over_lanes<LC>(most)));
+  uint32_t w0[4] = {0, 0, 0, 0}, w1[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    int sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    const int block = 2 * c + k;
+    const bool upper = block < blocks;
+    if (in)
+      for (int h = 0; h < p.group; ++h) {
+        const u32x4 x = load16(q + h * p.q_head + 8 * (upper ? block : block - blocks));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float f = value_of<DT>(x[i / 2], i % 2);
+          const int code = fabsf(f) < INFINITY ? (int)rintf(f * unit) : 0;
+          sum[i] += upper ? max(code, 0) : min(code, 0);
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int hi = sum[i] / 128, lo = sum[i] - 128 * hi;
+      w1[2 * k + i / 4] |= (uint32_t)(hi & 255) << (8 * (i % 4));
+      w0[2 * k + i / 4] |= (uint32_t)(lo & 255) << (8 * (i % 4));
+    }
+  }
+  const int32_t* table = p.table + b * p.table_row;
+  for (; j0 < end; j0 += kUnroll * step) {
+    int32_t page[kUnroll];
+    u32x4 x[kUnroll];
+    uint32_t s[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int32_t j = j0 + u * step + r0;
+      page[u] = j < end ? table[j] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const bool ok = (uint32_t)page[u] < (uint32_t)p.num_pages;
+      const int64_t entry = (int64_t)(ok ? page[u] : 0) * p.c.kv_heads + kv;
+      x[u] = *reinterpret_cast<const u32x4*>(p.codes + entry * 2 * hd + (in ? 16 * c : 0));
+      s[u] = p.scales[entry];
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      int t0 = 0, t1 = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        t0 = __builtin_amdgcn_sdot4((int)x[u][i], (int)w0[i], t0, false);
+        t1 = __builtin_amdgcn_sdot4((int)x[u][i], (int)w1[i], t1, false);
+      }
+      const int total =
+          (int)over_lanes<LC>((uint32_t)(128 * t1 + t0), [](uint32_t a, uint32_t b) { return a + b; });
+      const int32_t j = j0 + u * step + r0;
+      if (c == 0 && j < end) {
+        const bool ok = (uint32_t)page[u] < (uint32_t)p.num_pages;
+        const uint32_t key = s[u] == 255u ? kMost : order_key((float)total * as_f(s[u] << 23));
+        keys[j] = ok ? key : 0u;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- choosing
+
+template <int T>
+struct ChooseShared {
+  uint32_t hist[2048];
+  uint32_t waves[T / 64];
+  uint32_t bin, left;
+};
+
+// Sum over the workgroup's threads in front of this one, and over all.
+template <int T>
+__device__ inline uint32_t block_scan(uint32_t x, uint32_t* waves, uint32_t& all) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t s = wave_scan(x);
+  if (lane == 63) waves[wave] = s;
+  __syncthreads();
+  uint32_t before = 0, total = 0;
+#pragma unroll
+  for (int i = 0; i < T / 64; ++i) {
+    const uint32_t w = waves[i];
+    before += i < wave ? w : 0;
+    total += w;
+  }
+  __syncthreads();
+  all = total;
+  return before + s - x;
+}
+
+// One workgroup chooses for one sequence and head: the keys of all items, the `budget`-th largest found by
+// three histograms of 11, 11 and 10 bits, then the chosen items written in order. A thread has K consecutive
+// items, in registers where the workgroup has all of them at once.
+template <int T, int K, bool TOKENS>
+__global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
+  __shared__ ChooseShared<T> sh;
+  const int tid = threadIdx.x;
+  const int64_t b = blockIdx.x / (uint32_t)p.heads;
+  const int head = (int)(blockIdx.x - (uint32_t)b * p.heads);
+  const int32_t ps = (int32_t)p.page_size.d;
+  const int64_t len = min((int64_t)max(p.lens[b], 0), (int64_t)p.pages * ps);
+  const int32_t n = TOKENS ? (int32_t)min(len, (int64_t)p.items) : (int32_t)((len + ps - 1) / ps);
+  const int32_t* table = p.table + b * p.table_row;
+  const uint32_t* keys = TOKENS ? nullptr : p.keys + (int64_t)blockIdx.x * p.key_stride;
+  const float* mass = TOKENS ? p.mass + b * p.mass_batch + head * p.mass_head : nullptr;
+  auto there = [&](int32_t page) { return (uint32_t)page < (uint32_t)p.num_pages; };
+
+  uint32_t k[K];
+  auto load = [&](int32_t base) {
+    const int32_t i0 = base + tid * K;
+    if constexpr (TOKENS) {
+      typedef f32x4 f32x4_any __attribute__((aligned(4)));
+#pragma unroll
+      for (int i = 0; i < K; i += 4) {
+        f32x4 x = {0, 0, 0, 0};
+        if (i0 + i + 4 <= n)
+          x = *reinterpret_cast<const f32x4_any*>(mass + i0 + i);
+        else
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (i0 + i + u < n) x[u] = mass[i0 + i + u];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) k[i + u] = order_key(x[u]);
+      }
+#pragma unroll
+      for (int i = 0; i < K; ++i)
+        if (i0 + i >= n || !there(table[(uint32_t)(i0 + i) / p.page_size])) k[i] = 0;
+    } else {
+#pragma unroll
+      for (int i = 0; i < K; i += 4) {
+        u32x4 x = {0, 0, 0, 0};
+        if (i0 + i < n) x = *reinterpret_cast<const u32x4*>(keys + i0 + i);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) k[i + u] = i0 + i + u < n ? x[u] : 0;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if (k[i] != 0 && (i0 + i < p.sink || i0 + i >= n - p.recent)) k[i] = kForced;
+  };
+  const bool once = n <= T * K;
+  if (once) load(0);
+  uint32_t present = 0;
+  for (int32_t base = 0; base < n; base += T * K) {
+    if (!once) load(base);
+    uint32_t mine = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) mine += k[i] != 0;
+    block_scan<T>(mine, sh.waves, all);
+    present += all;
+  }
+  const uint32_t keep = min((uint32_t)p.budget, present);
+  uint32_t least = 0, ties = 0;   // chosen: keys above `least`, and the first `ties` that equal it
+  if (keep < present) {
+    uint32_t left = keep;
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+      for (int i = tid; i < 2048; i += T) sh.hist[i] = 0;
+      __syncthreads();
+      for (int32_t base = 0; base < n; base += T * K) {
+        if (!once) load(base);
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+          if (k[i] != 0 && (pass == 0 || k[i] >> (shift + bits) == least >> (shift + bits)))
+            atomicAdd(&sh.hist[k[i] >> shift & ((1u << bits) - 1)], 1u);
+      }
+      __syncthreads();
+      constexpr int kBins = 2048 / T;
+      const int top = (1 << bits) - 1;
+      uint32_t h[kBins], mine = 0, all = 0;
+#pragma unroll
+      for (int i = 0; i < kBins; ++i) {   // from the largest down
+        const int bin = top - (tid * kBins + i);
+        h[i] = bin >= 0 ? sh.hist[bin] : 0;
+        mine += h[i];
+      }
+      uint32_t before = block_scan<T>(mine, sh.waves, all);
+#pragma unroll
+      for (int i = 0; i < kBins; ++i) {
+        if (before < left && left <= before + h[i]) {
+          sh.bin = (uint32_t)(top - (tid * kBins + i));
+          sh.left = left - before;
+        }
+        before += h[i];
+      }
+      __syncthreads();
+      least |= sh.bin << shift;
+      left = sh.left;
+      __syncthreads();
+    }
+    ties = left;
+  }
+  int32_t* out = p.out + (int64_t)blockIdx.x * p.budget;
+  float* out_mass = TOKENS && p.out_mass ? p.out_mass + (int64_t)blockIdx.x * p.budget : nullptr;
+  uint32_t above = 0, equal = 0;   // so far
+  for (int32_t base = 0; base < n; base += T * K) {
+    if (!once) load(base);
+    uint32_t mine = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i) mine += (k[i] > least ? 1u : 0u) + (k[i] == least && least ? 0x10000u : 0u);
+    const uint32_t before = block_scan<T>(mine, sh.waves, all);
+    uint32_t a = above + (before & 0xffffu), e = equal + (before >> 16);
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      const bool more = k[i] > least, same = least && k[i] == least;
+      if (more || (same && e < ties)) {
+        const int32_t item = base + tid * K + i;
+        const uint32_t at = a + min(e, ties);
+        out[at] = TOKENS ? item : table[item];
+        if (TOKENS && out_mass) out_mass[at] = mass[item];
+      }
+      a += more ? 1 : 0;
+      e += same ? 1 : 0;
+    }
+    above += all & 0xffffu;
+    equal += all >> 16;
+  }
+  for (uint32_t i = keep + tid; i < (uint32_t)p.budget; i += T) {
+    out[i] = -1;
+    if (TOKENS && out_mass) out_mass[i] = 0.0f;
+  }
+  if (head == 0 && tid == 0) {
+    if (TOKENS) {
+      p.out_lens[b] = (int32_t)keep;
+    } else {
+      // all pages are full but the sequence's last, which is chosen if it is there
+      const bool last = n > 0 && there(table[n - 1]);
+      p.out_lens[b] = (int32_t)((int64_t)keep * ps - (last ? (int64_t)n * ps - len : 0));
+    }
+  }
+}
+
+// ---------------------------------------------------------------- moving
+
+// A thread moves one 16-byte chunk of a row's keys and of its values; the first ones also the scales.
+__global__ __launch_bounds__(kThreads) void move_kernel(MoveParams p) {
+  const int64_t bh = p.bh0 + blockIdx.y;
+  const uint32_t i = blockIdx.x * (uint32_t)kThreads + threadIdx.x;
+  const uint32_t j = i / p.chunks, chunk = i - j * p.chunks.d;
+  const int64_t b = bh / p.from.kv_heads;
+  const int kv = (int)(bh - b * p.from.kv_heads);
+  if (j >= (uint32_t)max(0, min(p.lens[b], p.budget))) return;
+  const int32_t t = p.kept[bh * p.budget + j];
+  const uint32_t fj = (uint32_t)t / p.from.page_size, tj = j / p.to.page_size;
+  if (t < 0 || fj >= (uint32_t)p.from_len || tj >= (uint32_t)p.to_len) return;
+  const int32_t fp = p.from_table[b * p.from_row + fj], tp = p.to_table[b * p.to_row + tj];
+  if ((uint32_t)fp >= (uint32_t)p.from_pages || (uint32_t)tp >= (uint32_t)p.to_pages) return;
+  const uint32_t fr = (uint32_t)t - fj * p.from.page_size.d, tr = j - tj * p.to.page_size.d;
+  const int64_t src = kv * p.from.head + row_at(p.from, fp, fr) + 16 * chunk;
+  const int64_t dst = kv * p.to.head + row_at(p.to, tp, tr) + 16 * chunk;
+  const u32x4 k = *reinterpret_cast<const u32x4*>(p.from.k + src);
+  const u32x4 v = *reinterpret_cast<const u32x4*>(p.from.v + src);
+  *reinterpret_cast<u32x4*>(p.to.k + dst) = k;
+  *reinterpret_cast<u32x4*>(p.to.v + dst) = v;
+  if (4 * (int)chunk < p.scale_bytes) {
+    const int64_t s = kv * p.from.s_head + scales_at(p.from, fp, fr) + 4 * chunk;
+    const int64_t d = kv * p.to.s_head + scales_at(p.to, tp, tr) + 4 * chunk;
+    *reinterpret_cast<uint32_t*>(p.to.ks + d) = *reinterpret_cast<const uint32_t*>(p.from.ks + s);
+    *reinterpret_cast<uint32_t*>(p.to.vs + d) = *reinterpret_cast<const uint32_t*>(p.from.vs + s);
+  }
+}
+
+template <int DT, int ST>
+void update_by_width(const IndexParams& p, int grid, hipStream_t s) {
+  const int dp = attn_padded(p.c.head_dim);
+  if (dp == 64)
+    update_kernel<DT, ST, 8><<<grid, kThreads, 0, s>>>(p);
+  else if (dp == 128)
+    update_kernel<DT, ST, 16><<<grid, kThreads, 0, s>>>(p);
+  else
+    update_kernel<DT, ST, 32><<<grid, kThreads, 0, s>>>(p);
+}
+
+template <int DT>
+void update_by_storage(const IndexParams& p, int storage, int grid, hipStream_t s) {
+  if (storage == AG_KV_16BIT)
+    update_by_width<DT, AG_KV_16BIT>(p, grid, s);
+  else if (storage == AG_KV_MXFP8)
+    update_by_width<DT, AG_KV_MXFP8>(p, grid, s);
+  else
+    update_by_width<DT, AG_KV_MXFP4>(p, grid, s);
+}
+
+template <int DT>
+void score_by_width(const IndexParams& p, int grid, hipStream_t s) {
+  const int dp = attn_padded(p.c.head_dim);
+  if (dp == 64)
+    score_kernel<DT, 8><<<grid, kThreads, 0, s>>>(p);
+  else if (dp == 128)
+    score_kernel<DT, 16><<<grid, kThreads, 0, s>>>(p);
+  else
+    score_kernel<DT, 32><<<grid, kThreads, 0, s>>>(p);
+}
+
+template <bool TOKENS>
+hipError_t choose(const ChooseParams& p, int64_t batch, hipStream_t s) {
+  const int grid = (int)(batch * p.heads);
+  if (p.items <= 256 * 8)
+    choose_kernel<256, 8, TOKENS><<<grid, 256, 0, s>>>(p);
+  else
+    choose_kernel<1024, 16, TOKENS><<<grid, 1024, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_index_update(const IndexParams& p, int dtype, int storage, int64_t batch, hipStream_t s) {
+  const int grid = (int)(batch * p.c.kv_heads * p.splits);
+  if (dtype == AGMM_F16)
+    update_by_storage<AGMM_F16>(p, storage, grid, s);
+  else
+    update_by_storage<AGMM_BF16>(p, storage, grid, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_index_score(const IndexParams& p, int dtype, int64_t batch, hipStream_t s) {
+  const int grid = (int)(batch * p.c.kv_heads * p.splits);
+  if (dtype == AGMM_F16)
+    score_by_width<AGMM_F16>(p, grid, s);
+  else
+    score_by_width<AGMM_BF16>(p, grid, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_choose_pages(const ChooseParams& p, int64_t batch, hipStream_t s) {
+  return choose<false>(p, batch, s);
+}
+hipError_t launch_choose_tokens(const ChooseParams& p, int64_t batch, hipStream_t s) {
+  return choose<true>(p, batch, s);
+}
+
+hipError_t launch_move(MoveParams p, int64_t batch, hipStream_t s) {
+  const uint32_t blocks = ((uint32_t)p.budget * p.chunks.d + kThreads - 1) / kThreads;
+  const int64_t heads = batch * p.from.kv_heads, most = 65535;
+  for (p.bh0 = 0; p.bh0 < heads; p.bh0 += most)
+    move_kernel<<<dim3(blocks, (uint32_t)min(most, heads - p.bh0)), kThreads, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace agmm

@@ -1,0 +1,517 @@
+// gfx950 kernel of the attention over prefixes that sequences share (agmm_long.h).
+//
+// Mathematics: for one prefix and kv head the q heads of all its sequences are the rows of one matrix Q
+// (rows x dim), and the prefix is read once for all of them: S^T = K Q^T (tokens x rows), a softmax over
+// the tokens with a running maximum and sum in 32 bits, O^T = V^T P^T. That is 4 rows x tokens x dim
+// operations for 4 tokens x dim bytes (16-bit cache), so from a few hundred rows on the matrix units bound
+// it, and the vector units, which make 2 rows x tokens exponentials and roundings meanwhile.
+//
+//  - A workgroup has 128 rows, 32 a wave, and goes through tiles of tokens (8192 elements of K, as many of
+//    V), which all of its waves read from LDS. A wave whose rows do not exist leaves the products out.
+//  - Matrix instructions of 32 tokens x 32 rows: S^T's accumulators (lane = row, 4 consecutive tokens) are
+//    P^T's operands for O^T, in the order of tokens {16 s + 4 h ..+3, 16 s + 8 + 4 h ..+3} for lane half h, so
+//    P never moves between lanes. V^T's operand in that order is two runs of 4 tokens of one element:
+//    V goes into LDS transposed, 4 tokens (8 bytes) of an element together.
+//  - Codes become values of the 16-bit type on the way into LDS, so all storages share the rest.
+//  - The next tile is loaded into registers while one is worked on, and goes to the other half of LDS
+//    behind it: one barrier a tile.
+//  - Swizzles: 16-byte chunk c of K's row t is in place c ^ (low bits of t); run q of 4 tokens of element d in
+//    place q ^ f(d). Both ways of access then touch every bank equally often.
+//
+// Work: a strip is 128 rows of one kv head and prefix; strips' tiles, strip after strip, are cut into equal runs,
+// one for each workgroup, from the lengths on the device. Every piece of a strip leaves its sums, maxima and
+// sums of weights in the scratch; the kernel of the sequences' own tokens joins them, in the order of the
+// pieces, with those (finish_shared in agmm_attn_kernel.h). Consecutive runs go to workgroups of one XCD, so that
+// strips of one kv head find its tiles in one L2.
+#include "agmm_attn_kernel.h"
+#include "agmm_long_internal.h"
+
+namespace agmm {
+namespace {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+template <int DT>
+__device__ inline f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (DT == AGMM_F16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8_t, a), __builtin_bit_cast(h8_t, b), c,
+                                                  0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8_t, a), __builtin_bit_cast(b8_t, b),
+                                                   c, 0, 0, 0);
+}
+
+template <int DP>
+struct Tile {
+  static constexpr int kTokens = 8192 / DP;       // 128, 64 or 32
+  static constexpr int kChunks = DP / 8;          // of 8 elements a row
+  static constexpr int kSub = kTokens / 32;       // blocks of 32 tokens
+  static constexpr int kMasks = (kTokens + 63) / 64;
+  static constexpr int kLoads = kTokens * kChunks / kThreads;  // chunks a thread loads of K, and of V: 4
+  static_assert(kLoads == 4, "a thread loads 4 tokens' chunks of V");
+
+  // Word of chunk c of token t's row in K's tile.
+  __device__ static inline int key(int t, int c) {
+    const int s = DP == 64 ? (t >> 1) & 7 : t & 15;
+    return t * (DP / 2) + 4 * (c ^ s);
+  }
+  // Word of element d's tokens 4 q .. 4 q + 3 in V's tile, transposed. Its rows are 64, 32 and 16 words: f takes
+  // all places both over 32 consecutive elements (less the bits that choose a row's banks), as they are
+  // read, and over elements 8 apart, as they are written.
+  __device__ static inline int value(int d, int q) {
+    const int f = DP == 64    ? (d & 31) ^ ((d >> 5) << 1)
+                  : DP == 128 ? ((d >> 1) & 15) ^ ((d >> 5) & 3)
+                              : ((d >> 2) & 7) ^ ((d >> 5) & 7);
+    return d * (kTokens / 2) + 2 * (q ^ f);
+  }
+};
+
+template <int DP>
+struct PrefixShared {
+  uint32_t k[2][4096], v[2][4096];
+  int64_t at[4][Tile<DP>::kTokens][2];  // the tokens' places: data and scale offsets, for each wave
+};
+
+// A thread's chunks of a tile as they come from memory.
+template <int ST>
+struct Staged {
+  static constexpr int kWords = ST == AG_KV_16BIT ? 4 : ST == AG_KV_MXFP8 ? 2 : 1;
+  uint32_t k[4][kWords], v[4][kWords];
+  uint32_t ks[4], vs[4];
+};
+
+struct PrefixScan {  // of one lane's group
+  int32_t first, end;
+  uint32_t tiles, row_tiles, strips, strip0, tile0;
+  int32_t len;
+};
+
+// What one wave of the workgroup knows about groups base .. base + 63, given what came before.
+struct PrefixCarry {
+  int32_t last;            // the sequences up to here are in some group
+  uint32_t strips, tiles;
+};
+
+__device__ inline uint32_t last_lane(uint32_t x) { return (uint32_t)__builtin_amdgcn_readlane((int)x, 63); }
+
+template <int DP>
+__device__ inline PrefixScan scan_groups(const PrefixParams& p, uint32_t base, PrefixCarry& c) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t g = base + lane;
+  const AttnParams& a = p.a;
+  PrefixScan r = {};
+  // A group ends where the next begins, and none begins before another's end: whatever `starts` holds,
+  // sequences are in one group at most.
+  int32_t end = 0;
+  if (g < p.groups) {
+    end = p.starts ? max(0, min(p.starts[g + 1], a.batch)) : a.batch;
+    r.len = max(0, min(p.lens[g], a.capacity));
+  }
+  int32_t run = end;  // the largest end up to this lane
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int32_t o = __shfl_up(run, d);
+    if (lane >= d) run = max(run, o);
+  }
+  int32_t before = __shfl_up(run, 1);
+  before = lane == 0 ? 0 : before;
+  const int32_t floor0 = base == 0 && p.starts ? max(0, min(p.starts[0], a.batch)) : 0;
+  const int32_t lowest = max(c.last, floor0);
+  r.first = max(before, lowest);
+  r.end = max(run, lowest);
+  if (g < p.groups && r.len > 0 && r.end > r.first) {
+    r.tiles = (uint32_t)((r.len + Tile<DP>::kTokens - 1) / Tile<DP>::kTokens);
+    r.row_tiles = ((uint32_t)(r.end - r.first) * a.group + kPrefixRows - 1) / kPrefixRows;
+    r.strips = r.row_tiles * a.c.kv_heads;
+  }
+  const uint32_t s = wave_scan(r.strips), t = wave_scan(r.strips * r.tiles);
+  r.strip0 = c.strips + s - r.strips;
+  r.tile0 = c.tiles + t - r.strips * r.tiles;
+  c.last = max(c.last, __shfl(r.end, 63));
+  c.strips += last_lane(s);
+  c.tiles += last_lane(t);
+  return r;
+}
+
+template <int DT, int ST, int DP, bool CAP>
+struct PrefixWave {
+  typedef Tile<DP> T;
+  typedef Staged<ST> S;
+  static constexpr int kSteps = DP / 16;   // matrix instructions over the head for 32 tokens
+  static constexpr int kParts = DP / 32;   // accumulators
+
+  u32x4 q[kSteps];
+  f32x16 acc[kParts];
+  float m, l;  // of this lane's row, m in unit()s; l of this lane's tokens alone
+
+  __device__ inline void start(const AttnParams& p, int32_t first, int kv, int row, int rows) {
+    const int lane = threadIdx.x & 63, h = lane >> 5;
+    const int i = row < rows ? row : 0;
+    const int b = first + i / p.group, head = kv * p.group + i % p.group;
+    const uint16_t* from = p.q + b * p.q_batch + head * p.q_head;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      const int e = 16 * s + 8 * h;
+      q[s] = u32x4{0, 0, 0, 0};
+      if (row < rows && e < p.c.head_dim) q[s] = load16(from + e);
+    }
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+#pragma unroll
+      for (int w = 0; w < 16; ++w) acc[i][w] = 0.0f;
+    m = -INFINITY;
+    l = 0.0f;
+  }
+
+  // The loads of the tile whose tokens' places are in `at`; tokens that are absent have the place of the
+  // pools' first row, and chunks past the head's end read its first.
+  __device__ static inline void load(S& r, const AttnParams& p, const int64_t (*at)[2], int64_t head,
+                                     int64_t s_head) {
+    const int tid = threadIdx.x, hd = p.c.head_dim;
+    const int c = tid % T::kChunks, e = 8 * c < hd ? 8 * c : 0;
+    const int bytes = ST == AG_KV_16BIT ? 2 * e : ST == AG_KV_MXFP8 ? e : e / 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = tid / T::kChunks + (kThreads / T::kChunks) * i;
+      load_words<S::kWords>(r.k[i], p.c.k + head + at[t][0] + bytes);
+      if (ST != AG_KV_16BIT) r.ks[i] = *(const uint8_t*)(p.c.ks + s_head + at[t][1] + e / 32);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 4 * (tid / T::kChunks) + i;
+      load_words<S::kWords>(r.v[i], p.c.v + head + at[t][0] + bytes);
+      if (ST != AG_KV_16BIT) r.vs[i] = *(const uint8_t*)(p.c.vs + s_head + at[t][1] + e / 32);
+    }
+  }
+
+  __device__ static inline u32x4 chunk(const uint32_t (&w)[S::kWords], uint32_t scale) {
+    if constexpr (ST == AG_KV_16BIT)
+      return u32x4{w[0], w[1], w[2], w[3]};
+    else if constexpr (ST == AG_KV_MXFP8)
+      return from_fp8x8<DT>(w[0], w[1], scale_of(scale));
+    else
+      return from_fp4x8<DT>(w[0], scale_of(scale));
+  }
+
+  // Into LDS; the values of absent tokens, and all elements past the head's end, are zeros.
+  __device__ static inline void store(const S& r, const AttnParams& p, const uint64_t (&there)[T::kMasks],
+                                      uint32_t* k, uint32_t* v) {
+    const int tid = threadIdx.x, c = tid % T::kChunks, row = tid / T::kChunks;
+    const bool in = 8 * c < p.c.head_dim;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const u32x4 x = chunk(r.k[i], r.ks[i]);
+      *reinterpret_cast<u32x4*>(k + T::key(row + (kThreads / T::kChunks) * i, c)) =
+          in ? x : u32x4{0, 0, 0, 0};
+    }
+    u32x4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = 4 * row + i;
+      const uint64_t mask = T::kMasks == 2 && t >= 64 ? there[T::kMasks - 1] : there[0];
+      const bool ok = in && (mask >> (t & 63) & 1);
+      x[i] = chunk(r.v[i], r.vs[i]);
+      if (!ok) x[i] = u32x4{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t sel = e % 2 ? 0x07060302u : 0x05040100u;
+      *reinterpret_cast<u32x2*>(v + T::value(8 * c + e, row)) =
+          u32x2{__builtin_amdgcn_perm(x[1][e / 2], x[0][e / 2], sel),
+                __builtin_amdgcn_perm(x[3][e / 2], x[2][e / 2], sel)};
+    }
+  }
+
+  __device__ inline void work(const AttnParams& p, const uint64_t (&there)[T::kMasks], bool all, int up,
+                              const uint32_t* k, const uint32_t* v) {
+    const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
+    f32x16 st[T::kSub];
+#pragma unroll
+    for (int u = 0; u < T::kSub; ++u) {
+#pragma unroll
+      for (int w = 0; w < 16; ++w) st[u][w] = 0.0f;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        st[u] = mfma32<DT>(*reinterpret_cast<const u32x4*>(k + T::key(32 * u + col, 2 * s + h)), q[s], st[u]);
+    }
+    float scale = p.scale;
+    if constexpr (CAP) {
+      scale = 1.0f;
+      float most = 0.0f;
+#pragma unroll
+      for (int u = 0; u < T::kSub; ++u)
+#pragma unroll
+        for (int w = 0; w < 16; ++w) most = fmaxf(most, fabsf(st[u][w]));
+      if (__any(most * p.inv_cap >= kFar)) {
+#pragma unroll
+        for (int u = 0; u < T::kSub; ++u)
+#pragma unroll
+          for (int w = 0; w < 16; ++w) st[u][w] = capped<false>(p, st[u][w]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < T::kSub; ++u)
+#pragma unroll
+          for (int w = 0; w < 16; ++w) st[u][w] = capped<true>(p, st[u][w]);
+      }
+    }
+    if (!all) {
+#pragma unroll
+      for (int u = 0; u < T::kSub; ++u) {
+        const uint32_t mine = (uint32_t)(there[u / 2] >> (32 * (u & 1))) >> (4 * here(h));
+#pragma unroll
+        for (int w = 0; w < 16; ++w)
+          st[u][w] = __builtin_bit_cast(
+              float, here(__builtin_bit_cast(int, mine >> (8 * (w / 4) + w % 4) & 1u ? st[u][w] : -INFINITY)));
+      }
+    }
+    float top = st[0][0];
+#pragma unroll
+    for (int u = 0; u < T::kSub; ++u)
+#pragma unroll
+      for (int w = 0; w < 16; ++w) top = fmaxf(top, st[u][w]);
+    {
+      const auto x = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, top),
+                                                      __builtin_bit_cast(uint32_t, top), false, false);
+      top = fmaxf(__builtin_bit_cast(float, (uint32_t)x[0]), __builtin_bit_cast(float, (uint32_t)x[1]));
+    }
+    if (__any((top - m) * scale > (float)kRaise)) {
+      const float raised = fmaxf(m, top);
+      const float f = weight(m, raised, scale);
+#pragma unroll
+      for (int i = 0; i < kParts; ++i)
+#pragma unroll
+        for (int w = 0; w < 16; ++w) acc[i][w] *= f;
+      l *= f;
+      m = raised;
+    }
+    const float ref = m == -INFINITY ? 0.0f : m, head = (float)up;
+#pragma unroll
+    for (int u = 0; u < T::kSub; ++u) {
+#pragma unroll
+      for (int w = 0; w < 16; ++w) {
+        st[u][w] = __builtin_amdgcn_exp2f(fmaf(st[u][w] - ref, scale, head));
+        l += st[u][w];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < T::kSub; ++u)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        u32x4 hi, lo;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const u32x2 w = T16<DT>::split(st[u][8 * s + 2 * j], st[u][8 * s + 2 * j + 1]);
+          hi[j] = w[0];
+          lo[j] = w[1];
+        }
+        const int run = 8 * u + 4 * s + h;
+#pragma unroll
+        for (int i = 0; i < kParts; ++i) {
+          const u32x2 x = *reinterpret_cast<const u32x2*>(v + T::value(32 * i + col, run));
+          const u32x2 y = *reinterpret_cast<const u32x2*>(v + T::value(32 * i + col, run + 2));
+          const u32x4 a = {x[0], x[1], y[0], y[1]};
+          acc[i] = mfma32<DT>(a, hi, acc[i]);
+          acc[i] = mfma32<DT>(a, lo, acc[i]);
+        }
+      }
+  }
+
+  // The piece's sums, maxima and sums of weights.
+  __device__ inline void leave(const PrefixParams& p, uint32_t slot, int row) const {
+    const int h = (threadIdx.x & 63) >> 5;
+    float* to = p.a.prefix.sums + (int64_t)slot * kPrefixRows * DP;
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        *reinterpret_cast<f32x4*>(to + prefix_at(row, 32 * i + 8 * w + 4 * h)) =
+            f32x4{acc[i][4 * w], acc[i][4 * w + 1], acc[i][4 * w + 2], acc[i][4 * w + 3]};
+    const auto x = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, l),
+                                                    __builtin_bit_cast(uint32_t, l), false, false);
+    const float sum = __builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]);
+    if (h == 0) {
+      float* s = p.a.prefix.stats + ((int64_t)slot * kPrefixRows + row) * 2;
+      s[0] = m;
+      s[1] = sum;
+    }
+  }
+};
+
+template <int DT, int ST, int DP, bool CAP>
+__global__ __launch_bounds__(kThreads, prefix_per_cu(DP)) void prefix_kernel(PrefixParams p) {
+  typedef Tile<DP> T;
+  typedef PrefixWave<DT, ST, DP, CAP> W;
+  __shared__ PrefixShared<DP> sh;
+  const AttnParams& a = p.a;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const uint32_t wgs = gridDim.x;
+  // consecutive numbers to the workgroups of an XCD, which are 8 apart
+  const uint32_t xcd = blockIdx.x % 8, each = wgs / 8, more = wgs % 8;
+  const uint32_t me = xcd * each + min(xcd, more) + blockIdx.x / 8;
+
+  PrefixCarry c = {0, 0, 0};
+  for (uint32_t g = 0; g < p.groups; g += 64) scan_groups<DP>(p, g, c);
+  const uint32_t total = c.tiles;
+  // runs of p.least tiles at least, as long as every compute unit gets one
+  const uint32_t quota = max(max((total + wgs - 1) / wgs, 1u),
+                             min(p.least, (total + kCus - 1) / kCus));
+  if (me == 0 && wave == 0) {
+    c = {0, 0, 0};
+    for (uint32_t g = 0; g < p.groups; g += 64) {
+      const PrefixScan r = scan_groups<DP>(p, g, c);
+      if (g + lane < p.groups)
+        a.prefix.info[g + lane] =
+            PrefixGroup{r.first, r.end, r.tiles, r.row_tiles, r.strip0, r.tile0, head_of<DT>(r.len), quota};
+    }
+  }
+  uint32_t cur = me * quota;
+  if (cur >= total) return;
+  const uint32_t end = min(cur + quota, total);
+
+  while (cur < end) {
+    // the group and strip of tile `cur`
+    c = {0, 0, 0};
+    PrefixScan r = {};
+    uint32_t group = 0;
+    for (uint32_t g = 0; g < p.groups; g += 64) {
+      const PrefixScan s = scan_groups<DP>(p, g, c);
+      const uint64_t hit = __ballot(s.strips * s.tiles != 0 && cur >= s.tile0 &&
+                                    cur < s.tile0 + s.strips * s.tiles);
+      if (hit) {
+        const int at = __builtin_ctzll(hit);
+        group = g + at;
+        r.first = __shfl(s.first, at);
+        r.end = __shfl(s.end, at);
+        r.tiles = __shfl(s.tiles, at);
+        r.row_tiles = __shfl(s.row_tiles, at);
+        r.strip0 = __shfl(s.strip0, at);
+        r.tile0 = __shfl(s.tile0, at);
+        r.strips = __shfl(s.strips, at);
+        r.len = __shfl(s.len, at);
+        break;
+      }
+    }
+    group = __builtin_amdgcn_readfirstlane(group);
+    const uint32_t tiles = __builtin_amdgcn_readfirstlane(r.tiles);
+    const uint32_t tile0 = __builtin_amdgcn_readfirstlane(r.tile0);
+    const uint32_t strip0 = __builtin_amdgcn_readfirstlane(r.strip0);
+    const uint32_t strips = __builtin_amdgcn_readfirstlane(r.strips);
+    const uint32_t row_tiles = __builtin_amdgcn_readfirstlane(r.row_tiles);
+    const int32_t first = __builtin_amdgcn_readfirstlane(r.first);
+    const int32_t rows = (__builtin_amdgcn_readfirstlane(r.end) - first) * a.group;
+    const int32_t len = __builtin_amdgcn_readfirstlane(r.len);
+    const int32_t* table = a.table + (int64_t)group * a.table_row;
+    const int up = head_of<DT>(len);
+    for (uint32_t strip = (cur - tile0) / tiles; strip < strips && cur < end; ++strip) {
+      const uint32_t begin = tile0 + strip * tiles, stop = min(end, begin + tiles);
+      const int kv = (int)(strip / row_tiles);
+      const int row0 = (int)(strip - kv * row_tiles) * kPrefixRows;
+      const int row = 32 * wave + (lane & 31);
+      const bool some = row0 + 32 * wave < rows;
+      const int64_t head = kv * a.c.head, s_head = kv * a.c.s_head;
+      W w;
+      w.start(a, first, kv, row0 + row, rows);
+      int64_t(*at)[2] = sh.at[wave];
+      auto page_of = [&](int64_t t) { return table[(uint32_t)min(t, (int64_t)len - 1) / a.c.page_size]; };
+      // Puts the places of a tile's tokens into LDS; bit t: token base + t is attended to.
+      auto place = [&](int64_t base, const int32_t (&page)[T::kMasks], uint64_t (&there)[T::kMasks]) {
+#pragma unroll
+        for (int i = 0; i < T::kMasks; ++i) {
+          const int64_t tok = base + 64 * i + lane;
+          const bool ok = (uint32_t)page[i] < (uint32_t)a.num_pages && tok < len &&
+                          (T::kTokens >= 64 || lane < T::kTokens);
+          there[i] = __ballot(ok);
+          const uint32_t t = (uint32_t)tok;
+          const uint32_t r = t - (t / a.c.page_size) * a.c.page_size.d;
+          if (T::kTokens >= 64 || lane < T::kTokens) {
+            at[64 * i + lane][0] = ok ? row_at(a.c, page[i], r) : 0;
+            if (ST != AG_KV_16BIT) at[64 * i + lane][1] = ok ? scales_at(a.c, page[i], r) : 0;
+          }
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      };
+      auto pages = [&](int64_t base, int32_t (&page)[T::kMasks]) {
+#pragma unroll
+        for (int i = 0; i < T::kMasks; ++i) page[i] = page_of(base + 64 * i + lane);
+      };
+      constexpr uint64_t kAll = T::kTokens >= 64 ? ~0ull : (1ull << (T::kTokens & 63)) - 1;
+      int64_t base = (int64_t)(cur - begin) * T::kTokens;
+      const int64_t behind = (int64_t)(stop - begin) * T::kTokens;
+      int32_t page[T::kMasks];
+      uint64_t there[T::kMasks], next[T::kMasks];
+      typename W::S staged;
+      pages(base, page);
+      place(base, page, there);
+      pages(base + T::kTokens, page);
+      W::load(staged, a, at, head, s_head);
+      W::store(staged, a, there, sh.k[0], sh.v[0]);
+      __syncthreads();
+      for (int buf = 0; base < behind; buf ^= 1) {
+        base += T::kTokens;
+        const bool more_tiles = base < behind;
+        if (more_tiles) {
+          place(base, page, next);
+          pages(base + T::kTokens, page);
+          W::load(staged, a, at, head, s_head);
+        }
+        if (some) {
+          bool all = true;
+#pragma unroll
+          for (int i = 0; i < T::kMasks; ++i) all = all && there[i] == kAll;
+          w.work(a, there, all, up, sh.k[buf], sh.v[buf]);
+        }
+        if (more_tiles) {
+          W::store(staged, a, next, sh.k[buf ^ 1], sh.v[buf ^ 1]);
+#pragma unroll
+          for (int i = 0; i < T::kMasks; ++i) there[i] = next[i];
+        }
+        __syncthreads();
+      }
+      if (some) w.leave(p, me + strip0 + strip, row);
+      cur = stop;
+    }
+  }
+}
+
+template <int DT, int ST, int DP>
+void prefix_by_cap(const PrefixParams& p, int grid, hipStream_t s) {
+  if (p.a.cap != 0.0f)
+    prefix_kernel<DT, ST, DP, true><<<grid, kThreads, 0, s>>>(p);
+  else
+    prefix_kernel<DT, ST, DP, false><<<grid, kThreads, 0, s>>>(p);
+}
+
+template <int DT, int ST>
+void prefix_by_width(const PrefixParams& p, int grid, hipStream_t s) {
+  const int dp = attn_padded(p.a.c.head_dim);
+  if (dp == 64)
+    prefix_by_cap<DT, ST, 64>(p, grid, s);
+  else if (dp == 128)
+    prefix_by_cap<DT, ST, 128>(p, grid, s);
+  else
+    prefix_by_cap<DT, ST, 256>(p, grid, s);
+}
+
+template <int DT>
+void prefix_by_storage(const PrefixParams& p, int storage, int grid, hipStream_t s) {
+  if (storage == AG_KV_16BIT)
+    prefix_by_width<DT, AG_KV_16BIT>(p, grid, s);
+  else if (storage == AG_KV_MXFP8)
+    prefix_by_width<DT, AG_KV_MXFP8>(p, grid, s);
+  else
+    prefix_by_width<DT, AG_KV_MXFP4>(p, grid, s);
+}
+
+}  // namespace
+
+hipError_t launch_prefix(const PrefixParams& p, int dtype, int storage, int grid, hipStream_t s) {
+  if (dtype == AGMM_F16)
+    prefix_by_storage<AGMM_F16>(p, storage, grid, s);
+  else
+    prefix_by_storage<AGMM_BF16>(p, storage, grid, s);
+  return hipGetLastError();
+}
+
+}  // namespace agmm
