@@ -570,14 +570,14 @@ __device__ inline Share prefix_share(const AttnParams& p, int64_t b, int head, i
     float top = r.m;
 #pragma unroll
     for (int k = 0; k < kIn; ++k) top = fmaxf(top, m[k]);
-    const float f = weight(r.m, top, unit(p));
+    const float f = weight(r.m, top, 1.0f);
     r.l *= f;
 #pragma unroll
     for (int w = 0; w < 4; ++w) r.o[w] *= f;
 #pragma unroll
     for (int k = 0; k < kIn; ++k)
       if (c + k < pieces) {
-        const float f = weight(m[k], top, unit(p));
+        const float f = weight(m[k], top, 1.0f);
         r.l = fmaf(f, l[k], r.l);
 #pragma unroll
         for (int w = 0; w < 4; ++w) r.o[w] = fmaf(f, o[k][w], r.o[w]);
@@ -598,8 +598,10 @@ __device__ inline void finish_shared(const AttnParams& p, int64_t b, int head, i
                                      float l, int up) {
   const Share s = prefix_share<DP>(p, b, head, e);
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const float top = fmaxf(m, s.m);
-  const float mine = ldexpf(l, -up) * weight(m, top, unit(p)), other = s.l * weight(s.m, top, unit(p));
+  // (the prefix's maximum is in base 2, the other in unit()s of it)
+  const float top = fmaxf(m * unit(p), s.m);
+  const float mine = m == -INFINITY ? l : ldexpf(l, -up) * __builtin_amdgcn_exp2f(fmaf(m, unit(p), -top));
+  const float other = s.l * weight(s.m, top, 1.0f);
   const float sum = mine + other;
   const float a = sum == 0.0f ? 0.0f : mine / sum, c = sum == 0.0f ? 0.0f : other / sum;
   float r[4];
@@ -610,7 +612,7 @@ __device__ inline void finish_shared(const AttnParams& p, int64_t b, int head, i
       u32x2{T16<DT>::pack(r[0], r[1]), T16<DT>::pack(r[2], r[3])};
   if (e == 0 && p.lse)
     p.lse[b * p.q_heads + head] =
-        sum == 0.0f ? -INFINITY : (top * unit(p) + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
+        sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
 }
 
 template <int CTRL, int ROWS>

@@ -41,38 +41,43 @@ __device__ inline f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c) {
                                                    c, 0, 0, 0);
 }
 
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char lds_char;
+typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
 template <int DP>
 struct Tile {
   static constexpr int kTokens = 8192 / DP;       // 128, 64 or 32
-  static constexpr int kChunks = DP / 8;          // of 8 elements a row
+  static constexpr int kRow = 2 * DP;             // bytes of a row
+  static constexpr int kChunks = DP / 8;          // of 16 bytes a row
   static constexpr int kSub = kTokens / 32;       // blocks of 32 tokens
   static constexpr int kMasks = (kTokens + 63) / 64;
-  static constexpr int kLoads = kTokens * kChunks / kThreads;  // chunks a thread loads of K, and of V: 4
-  static_assert(kLoads == 4, "a thread loads 4 tokens' chunks of V");
+  static constexpr int kLines = 64 / kChunks;     // rows that a wave fills at once
+  static constexpr int kBytes = 16384;            // of K's tile, and of V's
 
-  // Word of chunk c of token t's row in K's tile.
-  __device__ static inline int key(int t, int c) {
-    const int s = DP == 64 ? (t >> 1) & 7 : t & 15;
-    return t * (DP / 2) + 4 * (c ^ s);
-  }
-  // Word of element d's tokens 4 q .. 4 q + 3 in V's tile, transposed. Its rows are 64, 32 and 16 words: f takes
-  // all places both over 32 consecutive elements (less the bits that choose a row's banks), as they are
-  // read, and over elements 8 apart, as they are written.
-  __device__ static inline int value(int d, int q) {
-    const int f = DP == 64    ? (d & 31) ^ ((d >> 5) << 1)
-                  : DP == 128 ? ((d >> 1) & 15) ^ ((d >> 5) & 3)
-                              : ((d >> 2) & 7) ^ ((d >> 5) & 7);
-    return d * (kTokens / 2) + 2 * (q ^ f);
-  }
+  // Chunk c of row t is in place c ^ key(t), or c ^ value(t). Keys are read by 16 lanes at once, one chunk of
+  // 16 rows; values by 32 lanes, two neighbouring chunks of 4 rows twice. Rows are 32, 64 and 128 words: the
+  // places are such that the lanes that read together find different banks.
+  __device__ static inline int key(int t) { return DP == 64 ? (t >> 1) & 7 : t & 15; }
+  __device__ static inline int value(int t) { return DP == 64 ? 4 * ((t >> 1) & 1) : 4 * (t & 3); }
 };
 
 template <int DP>
 struct PrefixShared {
-  uint32_t k[2][4096], v[2][4096];
+  char k[2][Tile<DP>::kBytes], v[2][Tile<DP>::kBytes];
   int64_t at[4][Tile<DP>::kTokens][2];  // the tokens' places: data and scale offsets, for each wave
 };
 
-// A thread's chunks of a tile as they come from memory.
+// 16 bytes a lane from `from` into LDS at byte m0 + 16 * lane (m0 is wave-uniform). Written as inline asm so that
+// the compiler adds no waits for it: it cannot tell which half of LDS is written, and would wait before every
+// read of the other.
+__device__ inline void dma16(const char* from, uint32_t m0) {
+  asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(from), "{m0}"(m0) : "memory");
+}
+__device__ inline void dma_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// A thread's chunks of a tile as they come from memory, where they do not go to LDS directly.
 template <int ST>
 struct Staged {
   static constexpr int kWords = ST == AG_KV_16BIT ? 4 : ST == AG_KV_MXFP8 ? 2 : 1;
@@ -133,16 +138,23 @@ __device__ inline PrefixScan scan_groups(const PrefixParams& p, uint32_t base, P
   return r;
 }
 
-template <int DT, int ST, int DP, bool CAP>
+// The next `n` instructions of this kind, in the order of these calls.
+constexpr int kAlu = 0x402, kMatrix = 0x8, kReads = 0x100;
+#define order(kind, n) __builtin_amdgcn_sched_group_barrier(kind, n, 0)
+
+// DMA: 16-bit rows of all of DP elements, which go from memory to LDS directly.
+template <int DT, int ST, int DP, bool CAP, bool DMA>
 struct PrefixWave {
   typedef Tile<DP> T;
   typedef Staged<ST> S;
   static constexpr int kSteps = DP / 16;   // matrix instructions over the head for 32 tokens
   static constexpr int kParts = DP / 32;   // accumulators
+  static constexpr int kKeys = kSteps < 8 ? kSteps : 8, kValues = kParts < 4 ? kParts : 4;
 
   u32x4 q[kSteps];
   f32x16 acc[kParts];
-  float m, l;  // of this lane's row, m in unit()s; l of this lane's tokens alone
+  float m, l;  // of this lane's row: reference of the weights, a whole number, base 2; l of this lane's tokens
+  uint32_t k_at[kKeys], v_at[kValues];  // LDS bytes of this lane's operands
 
   __device__ inline void start(const AttnParams& p, int32_t first, int kv, int row, int rows) {
     const int lane = threadIdx.x & 63, h = lane >> 5;
@@ -161,26 +173,46 @@ struct PrefixWave {
       for (int w = 0; w < 16; ++w) acc[i][w] = 0.0f;
     m = -INFINITY;
     l = 0.0f;
+    const int t = lane & 31, i16 = lane & 15, half = (lane >> 4) & 1;
+#pragma unroll
+    for (int s = 0; s < kKeys; ++s) k_at[s] = (uint32_t)(t * T::kRow + 16 * ((2 * s + h) ^ T::key(t)));
+    // transposing reads: 16 lanes get 16 elements of 4 tokens from addresses of 4 elements of one
+#pragma unroll
+    for (int i = 0; i < kValues; ++i)
+      v_at[i] = (uint32_t)((4 * h + i16 / 4) * T::kRow +
+                           16 * ((4 * i + 2 * half + i16 % 4 / 2) ^ T::value(i16 / 4)) + 8 * (i16 % 2));
   }
 
+  // Rows line(i) of a tile are this lane's to fetch, chunk lane % kChunks.
+  __device__ static inline int line(int i) {
+    return (((int)threadIdx.x >> 6) * 4 + i) * T::kLines + (int)(threadIdx.x & 63) / T::kChunks;
+  }
+  __device__ static inline int bytes_of(int e) { return ST == AG_KV_16BIT ? 2 * e : ST == AG_KV_MXFP8 ? e : e / 2; }
+
   // The loads of the tile whose tokens' places are in `at`; tokens that are absent have the place of the
-  // pools' first row, and chunks past the head's end read its first.
+  // pools' first row, and chunks past the head's end read its first. k and v: LDS bytes of the tile's halves.
   __device__ static inline void load(S& r, const AttnParams& p, const int64_t (*at)[2], int64_t head,
-                                     int64_t s_head) {
-    const int tid = threadIdx.x, hd = p.c.head_dim;
-    const int c = tid % T::kChunks, e = 8 * c < hd ? 8 * c : 0;
-    const int bytes = ST == AG_KV_16BIT ? 2 * e : ST == AG_KV_MXFP8 ? e : e / 2;
+                                     int64_t s_head, uint32_t k, uint32_t v) {
+    const int c = (int)(threadIdx.x & 63) % T::kChunks, hd = p.c.head_dim;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int t = tid / T::kChunks + (kThreads / T::kChunks) * i;
-      load_words<S::kWords>(r.k[i], p.c.k + head + at[t][0] + bytes);
-      if (ST != AG_KV_16BIT) r.ks[i] = *(const uint8_t*)(p.c.ks + s_head + at[t][1] + e / 32);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = 4 * (tid / T::kChunks) + i;
-      load_words<S::kWords>(r.v[i], p.c.v + head + at[t][0] + bytes);
-      if (ST != AG_KV_16BIT) r.vs[i] = *(const uint8_t*)(p.c.vs + s_head + at[t][1] + e / 32);
+      const int t = line(i);
+      const int64_t data = head + at[t][0];
+      if constexpr (DMA) {
+        const uint32_t to = (uint32_t)(1024 * (4 * wave + i));
+        dma16(p.c.k + data + 16 * (c ^ T::key(t)), k + to);
+        dma16(p.c.v + data + 16 * (c ^ T::value(t)), v + to);
+      } else {
+        const int e = 8 * c < hd ? 8 * c : 0;
+        load_words<S::kWords>(r.k[i], p.c.k + data + bytes_of(e));
+        load_words<S::kWords>(r.v[i], p.c.v + data + bytes_of(e));
+        if (ST != AG_KV_16BIT) {
+          const int64_t scale = s_head + at[t][1] + e / 32;
+          r.ks[i] = *(const uint8_t*)(p.c.ks + scale);
+          r.vs[i] = *(const uint8_t*)(p.c.vs + scale);
+        }
+      }
     }
   }
 
@@ -193,47 +225,60 @@ struct PrefixWave {
       return from_fp4x8<DT>(w[0], scale_of(scale));
   }
 
-  // Into LDS; the values of absent tokens, and all elements past the head's end, are zeros.
+  // The loaded tile in LDS; the values of absent tokens, and all elements past the head's end, are zeros.
   __device__ static inline void store(const S& r, const AttnParams& p, const uint64_t (&there)[T::kMasks],
-                                      uint32_t* k, uint32_t* v) {
-    const int tid = threadIdx.x, c = tid % T::kChunks, row = tid / T::kChunks;
-    const bool in = 8 * c < p.c.head_dim;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const u32x4 x = chunk(r.k[i], r.ks[i]);
-      *reinterpret_cast<u32x4*>(k + T::key(row + (kThreads / T::kChunks) * i, c)) =
-          in ? x : u32x4{0, 0, 0, 0};
+                                      bool all, lds_char* k, lds_char* v) {
+    const int c = (int)(threadIdx.x & 63) % T::kChunks;
+    const u32x4 zero = {0, 0, 0, 0};
+    if constexpr (DMA) {
+      dma_done();
+      if (all) return;
     }
-    u32x4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int t = 4 * row + i;
+      const int t = line(i);
       const uint64_t mask = T::kMasks == 2 && t >= 64 ? there[T::kMasks - 1] : there[0];
-      const bool ok = in && (mask >> (t & 63) & 1);
-      x[i] = chunk(r.v[i], r.vs[i]);
-      if (!ok) x[i] = u32x4{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t sel = e % 2 ? 0x07060302u : 0x05040100u;
-      *reinterpret_cast<u32x2*>(v + T::value(8 * c + e, row)) =
-          u32x2{__builtin_amdgcn_perm(x[1][e / 2], x[0][e / 2], sel),
-                __builtin_amdgcn_perm(x[3][e / 2], x[2][e / 2], sel)};
+      const bool ok = mask >> (t & 63) & 1;
+      if constexpr (DMA) {
+        if (!ok) *(lds_u32x4*)(v + t * T::kRow + 16 * c) = zero;
+      } else {
+        const bool in = 8 * c < p.c.head_dim;
+        const u32x4 x = chunk(r.k[i], r.ks[i]), y = chunk(r.v[i], r.vs[i]);
+        *(lds_u32x4*)(k + t * T::kRow + 16 * (c ^ T::key(t))) = in ? x : zero;
+        *(lds_u32x4*)(v + t * T::kRow + 16 * (c ^ T::value(t))) = in && ok ? y : zero;
+      }
     }
   }
 
-  __device__ inline void work(const AttnParams& p, const uint64_t (&there)[T::kMasks], bool all, int up,
-                              const uint32_t* k, const uint32_t* v) {
-    const int lane = threadIdx.x & 63, col = lane & 31, h = lane >> 5;
+  // k, v: the tile.
+  __device__ __attribute__((always_inline)) inline void work(const AttnParams& p, const uint64_t (&there)[T::kMasks], bool all, int up,
+                              const lds_char* k, const lds_char* v) {
+    const int h = (int)(threadIdx.x & 63) >> 5;
     f32x16 st[T::kSub];
 #pragma unroll
-    for (int u = 0; u < T::kSub; ++u) {
+    for (int u = 0; u < T::kSub; ++u)
 #pragma unroll
       for (int w = 0; w < 16; ++w) st[u][w] = 0.0f;
+    // Operands kAhead instructions ahead, so that the matrix unit does not wait for LDS.
+    constexpr int kAll = kSteps * T::kSub, kAhead = 6;
+    u32x4 key[kAll];
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-        st[u] = mfma32<DT>(*reinterpret_cast<const u32x4*>(k + T::key(32 * u + col, 2 * s + h)), q[s], st[u]);
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int u = 0; u < T::kSub; ++u)
+        key[s * T::kSub + u] =
+            *(const lds_u32x4*)(k + k_at[s % kKeys] + 16 * 16 * (s / kKeys) + 32 * u * T::kRow);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int u = 0; u < T::kSub; ++u) st[u] = mfma32<DT>(key[s * T::kSub + u], q[s], st[u]);
+    order(kReads, kAhead);
+#pragma unroll
+    for (int i = 0; i < kAll - kAhead; ++i) {
+      order(kMatrix, 1);
+      order(kReads, 1);
     }
+    order(kMatrix, kAhead);
     float scale = p.scale;
     if constexpr (CAP) {
       scale = 1.0f;
@@ -274,9 +319,12 @@ struct PrefixWave {
                                                       __builtin_bit_cast(uint32_t, top), false, false);
       top = fmaxf(__builtin_bit_cast(float, (uint32_t)x[0]), __builtin_bit_cast(float, (uint32_t)x[1]));
     }
-    if (__any((top - m) * scale > (float)kRaise)) {
-      const float raised = fmaxf(m, top);
-      const float f = weight(m, raised, scale);
+    // Weights are 2^(score - m + head) with a whole number m: scaling by one multiply-add is then exact up to the
+    // exponent's own rounding however large the scores are, and what is summed is rescaled by powers of 2.
+    top *= scale;
+    if (__any(top - m > (float)kRaise)) {
+      const float raised = fmaxf(m, ceilf(top));
+      const float f = weight(m, raised, 1.0f);
 #pragma unroll
       for (int i = 0; i < kParts; ++i)
 #pragma unroll
@@ -284,36 +332,57 @@ struct PrefixWave {
       l *= f;
       m = raised;
     }
-    const float ref = m == -INFINITY ? 0.0f : m, head = (float)up;
+    const float less = (float)up - (m == -INFINITY ? 0.0f : m);
+    // 16 tokens at a time; the weights of the next ones are made between the products of these.
+    constexpr int kTimes = 2 * T::kSub, kVector = 56 / (2 * kParts);
+    u32x4 hi[2], lo[2], value[2][kParts];
+    auto weigh = [&](int g) __attribute__((always_inline)) {
 #pragma unroll
-    for (int u = 0; u < T::kSub; ++u) {
+      for (int j = 0; j < 4; ++j) {
+        float w[2];
 #pragma unroll
-      for (int w = 0; w < 16; ++w) {
-        st[u][w] = __builtin_amdgcn_exp2f(fmaf(st[u][w] - ref, scale, head));
-        l += st[u][w];
+        for (int i = 0; i < 2; ++i) {
+          w[i] = __builtin_amdgcn_exp2f(fmaf(st[g / 2][8 * (g % 2) + 2 * j + i], scale, less));
+          l += w[i];
+        }
+        const u32x2 x = T16<DT>::split(w[0], w[1]);
+        hi[g % 2][j] = x[0];
+        lo[g % 2][j] = x[1];
+      }
+    };
+    auto read = [&](int g) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) {
+        const lds_char* at = v + v_at[i % kValues] + 16 * 16 * (i / kValues) + 16 * g * T::kRow;
+        const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at));
+        const u32x2 y =
+            __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(at + 8 * T::kRow)));
+        value[g % 2][i] = u32x4{x[0], x[1], y[0], y[1]};
+      }
+    };
+    read(0);
+    weigh(0);
+    order(kReads, 2 * kParts);
+    order(kAlu, 56);
+#pragma unroll
+    for (int g = 0; g < kTimes; ++g) {
+      if (g + 1 < kTimes) {
+        read(g + 1);
+        weigh(g + 1);
+      }
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) acc[i] = mfma32<DT>(value[g % 2][i], hi[g % 2], acc[i]);
+#pragma unroll
+      for (int i = 0; i < kParts; ++i) acc[i] = mfma32<DT>(value[g % 2][i], lo[g % 2], acc[i]);
+#pragma unroll
+      for (int i = 0; i < 2 * kParts; ++i) {
+        order(kMatrix, 1);
+        if (g + 1 < kTimes) {
+          order(kReads, 1);
+          order(kAlu, kVector);
+        }
       }
     }
-#pragma unroll
-    for (int u = 0; u < T::kSub; ++u)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        u32x4 hi, lo;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const u32x2 w = T16<DT>::split(st[u][8 * s + 2 * j], st[u][8 * s + 2 * j + 1]);
-          hi[j] = w[0];
-          lo[j] = w[1];
-        }
-        const int run = 8 * u + 4 * s + h;
-#pragma unroll
-        for (int i = 0; i < kParts; ++i) {
-          const u32x2 x = *reinterpret_cast<const u32x2*>(v + T::value(32 * i + col, run));
-          const u32x2 y = *reinterpret_cast<const u32x2*>(v + T::value(32 * i + col, run + 2));
-          const u32x4 a = {x[0], x[1], y[0], y[1]};
-          acc[i] = mfma32<DT>(a, hi, acc[i]);
-          acc[i] = mfma32<DT>(a, lo, acc[i]);
-        }
-      }
   }
 
   // The piece's sums, maxima and sums of weights.
@@ -337,10 +406,10 @@ struct PrefixWave {
   }
 };
 
-template <int DT, int ST, int DP, bool CAP>
+template <int DT, int ST, int DP, bool CAP, bool DMA>
 __global__ __launch_bounds__(kThreads, prefix_per_cu(DP)) void prefix_kernel(PrefixParams p) {
   typedef Tile<DP> T;
-  typedef PrefixWave<DT, ST, DP, CAP> W;
+  typedef PrefixWave<DT, ST, DP, CAP, DMA> W;
   __shared__ PrefixShared<DP> sh;
   const AttnParams& a = p.a;
   const int lane = threadIdx.x & 63;
@@ -442,32 +511,43 @@ __global__ __launch_bounds__(kThreads, prefix_per_cu(DP)) void prefix_kernel(Pre
       int32_t page[T::kMasks];
       uint64_t there[T::kMasks], next[T::kMasks];
       typename W::S staged;
+      auto whole = [&](const uint64_t (&x)[T::kMasks]) {
+        bool all = x[0] == kAll;
+        if (T::kMasks == 2) all = all && x[T::kMasks - 1] == kAll;
+        return all;
+      };
+      lds_char* const k = (lds_char*)&sh.k[0][0];
+      lds_char* const v = (lds_char*)&sh.v[0][0];
+      auto fetch = [&](int buf) {
+        W::load(staged, a, at, head, s_head, (uint32_t)(size_t)k + buf * T::kBytes,
+                (uint32_t)(size_t)v + buf * T::kBytes);
+      };
       pages(base, page);
       place(base, page, there);
       pages(base + T::kTokens, page);
-      W::load(staged, a, at, head, s_head);
-      W::store(staged, a, there, sh.k[0], sh.v[0]);
+      fetch(0);
+      W::store(staged, a, there, whole(there), k, v);
       __syncthreads();
-      for (int buf = 0; base < behind; buf ^= 1) {
+      // The next tile is under way to one half of LDS while the other is worked on.
+      auto step = [&](auto buf) __attribute__((always_inline)) {
+        constexpr int now = decltype(buf)::value, after = 1 - now;
         base += T::kTokens;
         const bool more_tiles = base < behind;
         if (more_tiles) {
           place(base, page, next);
           pages(base + T::kTokens, page);
-          W::load(staged, a, at, head, s_head);
+          fetch(after);
         }
-        if (some) {
-          bool all = true;
-#pragma unroll
-          for (int i = 0; i < T::kMasks; ++i) all = all && there[i] == kAll;
-          w.work(a, there, all, up, sh.k[buf], sh.v[buf]);
-        }
+        if (some) w.work(a, there, whole(there), up, k + now * T::kBytes, v + now * T::kBytes);
         if (more_tiles) {
-          W::store(staged, a, next, sh.k[buf ^ 1], sh.v[buf ^ 1]);
+          W::store(staged, a, next, whole(next), k + after * T::kBytes, v + after * T::kBytes);
 #pragma unroll
           for (int i = 0; i < T::kMasks; ++i) there[i] = next[i];
         }
         __syncthreads();
+        return more_tiles;
+      };
+      while (step(std::integral_constant<int, 0>{}) && step(std::integral_constant<int, 1>{})) {
       }
       if (some) w.leave(p, me + strip0 + strip, row);
       cur = stop;
@@ -475,23 +555,34 @@ __global__ __launch_bounds__(kThreads, prefix_per_cu(DP)) void prefix_kernel(Pre
   }
 }
 
-template <int DT, int ST, int DP>
+template <int DT, int ST, int DP, bool DMA>
 void prefix_by_cap(const PrefixParams& p, int grid, hipStream_t s) {
   if (p.a.cap != 0.0f)
-    prefix_kernel<DT, ST, DP, true><<<grid, kThreads, 0, s>>>(p);
+    prefix_kernel<DT, ST, DP, true, DMA><<<grid, kThreads, 0, s>>>(p);
   else
-    prefix_kernel<DT, ST, DP, false><<<grid, kThreads, 0, s>>>(p);
+    prefix_kernel<DT, ST, DP, false, DMA><<<grid, kThreads, 0, s>>>(p);
+}
+
+template <int DT, int ST, int DP>
+void prefix_by_rows(const PrefixParams& p, int grid, hipStream_t s) {
+  if constexpr (ST == AG_KV_16BIT) {
+    if (p.a.c.head_dim == DP) {
+      prefix_by_cap<DT, ST, DP, true>(p, grid, s);
+      return;
+    }
+  }
+  prefix_by_cap<DT, ST, DP, false>(p, grid, s);
 }
 
 template <int DT, int ST>
 void prefix_by_width(const PrefixParams& p, int grid, hipStream_t s) {
   const int dp = attn_padded(p.a.c.head_dim);
   if (dp == 64)
-    prefix_by_cap<DT, ST, 64>(p, grid, s);
+    prefix_by_rows<DT, ST, 64>(p, grid, s);
   else if (dp == 128)
-    prefix_by_cap<DT, ST, 128>(p, grid, s);
+    prefix_by_rows<DT, ST, 128>(p, grid, s);
   else
-    prefix_by_cap<DT, ST, 256>(p, grid, s);
+    prefix_by_rows<DT, ST, 256>(p, grid, s);
 }
 
 template <int DT>
