@@ -16,8 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libagmm.so")
 RESOURCES = os.path.join(HERE, "kernel_resources.json")
 SOURCES = ["agmm_kernels.hip", "agmm_static.hip", "agmm_api.cpp", "agmm_rope_kv.hip",
-           "agmm_attn.hip", "agmm_attn_ext.hip", "agmm_attn_api.cpp",
-           "agmm_prefix.hip", "agmm_index.hip", "agmm_mass.hip", "agmm_long_api.cpp"]
+           "agmm_attn.hip", "agmm_attn_heads.hip", "agmm_attn_api.cpp",
+           "agmm_prefix_f16.hip", "agmm_prefix_bf16.hip", "agmm_index.hip", "agmm_mass.hip", "agmm_long_api.cpp"]
 LLVM_BIN = "/opt/rocm/llvm/bin"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -67,10 +67,10 @@ struct CacheParams {
   uint32_t q_blocks;         // leading workgroups that rotate q (RopeParams beside)
 };
 
-// What a prefix's kernel leaves for the sequences that share it (agmm_prefix.hip). Its rows are the q heads of
-// one kv head of all the sequences, kPrefixRows of them a strip; a strip's tiles of tokens, strip after
-// strip, are cut into runs of `quota`, one for each workgroup. Workgroup w's piece of strip s is in slot
-// w + s.
+// What the kernel of shared prefixes leaves for the joining (agmm_prefix_kernel.h). The rows of a prefix are the q
+// heads of one kv head of all the sequences, kPrefixRows of them a strip; a strip's tiles of tokens, strip
+// after strip, are cut into runs of `quota`, one for each workgroup that works on prefixes. Workgroup w's piece of
+// strip s is in slot w + s.
 constexpr int kPrefixRows = 128;
 struct PrefixGroup {
   int32_t first, end;       // sequences
@@ -83,8 +83,10 @@ struct PrefixGroup {
 struct PrefixView {
   PrefixGroup* info;        // [groups]
   float* sums;              // [slots][padded head_dim / 8][kPrefixRows][8]
-  float* stats;             // [slots][kPrefixRows][2]: maximum and sum
-  uint32_t groups;          // 0: no prefixes
+  float* stats;             // [slots][kPrefixRows][2]: reference of the weights, and their sum
+  float* own;               // [batch][q_heads][padded head_dim]: the average of the own tokens' values
+  float* own_stats;         // [batch][q_heads][2]: maximum and sum
+  uint32_t groups;
 };
 constexpr int64_t prefix_at(int64_t row, int e) { return ((int64_t)(e / 8) * kPrefixRows + row) * 8 + e % 8; }
 
@@ -106,9 +108,8 @@ struct AttnParams {
   int32_t rows;            // of a partial result: q heads in the largest of these groups
   float scale;             // times log2 e
   float cap, inv_cap;      // cap * log2 e, and 2 log2 e * scale / cap; cap 0 = none
-  // launch_attn_ext alone
-  int64_t table_head;      // from one kv head's page table to the next
-  PrefixView prefix;
+  int64_t table_head;      // from one kv head's page table to the next (launch_attn_heads)
+  PrefixView prefix;       // (launch_prefix)
 };
 
 hipError_t launch_rope(const RopeParams& p, int dtype, int pairing, int gradient, int64_t batch,
@@ -127,7 +128,7 @@ constexpr int attn_per_cu(int storage, int padded) {
   return storage == AG_KV_16BIT && padded == 256 ? 1 : 2;
 }
 hipError_t launch_attn(const AttnParams& p, int dtype, int storage, int grid, hipStream_t s);
-hipError_t launch_attn_ext(const AttnParams& p, int dtype, int storage, int grid, hipStream_t s);
+hipError_t launch_attn_heads(const AttnParams& p, int dtype, int storage, int grid, hipStream_t s);
 
 // Of agmm_attn_api.cpp, for the rest of the host side.
 int hip_failed(hipError_t e);                // remembers it; the ABI's code for it

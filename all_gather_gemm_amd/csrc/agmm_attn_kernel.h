@@ -46,6 +46,9 @@ namespace agmm {
 namespace {
 
 constexpr int kCus = 256;
+// What a kernel's tokens and results are: kPlain, those of ag_attn_run; kHeads, with a page table for each kv
+// head; kPieces, the tokens behind a shared prefix, whose results are left for the joining with it.
+constexpr int kPlain = 0, kHeads = 1, kPieces = 2;
 // Tiles of a workgroup's share, at least, as long as every compute unit gets one, where sequences have more
 // than kLong tiles on the average: fewer pieces to join (131072 tokens, one kv head, e4m3: 17.7 us, 20.8
 // with 2). Of shorter ones a share would hold ends of two heads more often than it saves pieces (32
@@ -531,90 +534,6 @@ __device__ inline uint32_t tiles_of(const AttnParams& p, int32_t len) {
   return r.first == r.end ? 0 : (uint32_t)((r.end - r.from + kAttnTile - 1) / kAttnTile);
 }
 
-// A prefix's part of a row, which a kernel before this one has left in pieces (agmm_prefix.hip): elements
-// e .. e + 3 over the weights' sum, the maximum m, and the sum of the weights 2^((s - m) unit).
-struct Share {
-  f32x4 o;
-  float m, l;
-};
-
-template <int DP>
-__device__ inline Share prefix_share(const AttnParams& p, int64_t b, int head, int e) {
-  const PrefixView& x = p.prefix;
-  Share r = {{0, 0, 0, 0}, -INFINITY, 0.0f};
-  uint32_t lo = 0, hi = x.groups;  // the last group that begins at b or before
-  while (hi - lo > 1) {
-    const uint32_t mid = (lo + hi) / 2;
-    (x.info[mid].first <= b ? lo : hi) = mid;
-  }
-  const PrefixGroup g = x.info[lo];
-  if (b < g.first || b >= g.end || g.tiles == 0) return r;
-  const uint32_t kv = (uint32_t)head / p.group, i = (uint32_t)(b - g.first) * p.group + (head - kv * p.group);
-  const uint32_t strip = kv * g.row_tiles + i / kPrefixRows, row = i % kPrefixRows;
-  const uint32_t start = g.tile0 + strip * g.tiles;
-  const uint32_t begin = start / g.quota, pieces = (start + g.tiles - 1) / g.quota - begin + 1;
-  const uint32_t slot = begin + g.strip0 + strip;
-  constexpr int kIn = 4;  // pieces whose loads are in flight together
-#pragma unroll 1
-  for (uint32_t c = 0; c < pieces; c += kIn) {
-    f32x4 o[kIn];
-    float m[kIn], l[kIn];
-#pragma unroll
-    for (int k = 0; k < kIn; ++k) {
-      const int64_t at = (int64_t)(slot + min(c + k, pieces - 1));
-      const float* s = x.stats + (at * kPrefixRows + row) * 2;
-      m[k] = s[0];
-      l[k] = c + k < pieces ? s[1] : 0.0f;
-      o[k] = *reinterpret_cast<const f32x4*>(x.sums + at * kPrefixRows * DP + prefix_at(row, e));
-    }
-    float top = r.m;
-#pragma unroll
-    for (int k = 0; k < kIn; ++k) top = fmaxf(top, m[k]);
-    const float f = weight(r.m, top, 1.0f);
-    r.l *= f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) r.o[w] *= f;
-#pragma unroll
-    for (int k = 0; k < kIn; ++k)
-      if (c + k < pieces) {
-        const float f = weight(m[k], top, 1.0f);
-        r.l = fmaf(f, l[k], r.l);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) r.o[w] = fmaf(f, o[k][w], r.o[w]);
-      }
-    r.m = top;
-  }
-  const float inv = r.l == 0.0f ? 0.0f : 1.0f / r.l;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) r.o[w] *= inv;
-  r.l = ldexpf(r.l, -g.up);
-  return r;
-}
-
-// As finish, joined with the prefix's part. Both averages come in over their own sums: what joins them is an
-// average of the two, so finite values cannot leave the type's range on the way.
-template <int DT, int DP>
-__device__ inline void finish_shared(const AttnParams& p, int64_t b, int head, int e, f32x4 o, float m,
-                                     float l, int up) {
-  const Share s = prefix_share<DP>(p, b, head, e);
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  // (the prefix's maximum is in base 2, the other in unit()s of it)
-  const float top = fmaxf(m * unit(p), s.m);
-  const float mine = m == -INFINITY ? l : ldexpf(l, -up) * __builtin_amdgcn_exp2f(fmaf(m, unit(p), -top));
-  const float other = s.l * weight(s.m, top, 1.0f);
-  const float sum = mine + other;
-  const float a = sum == 0.0f ? 0.0f : mine / sum, c = sum == 0.0f ? 0.0f : other / sum;
-  float r[4];
-#pragma unroll
-  for (int w = 0; w < 4; ++w) r[w] = fmaf(o[w] * inv, a, s.o[w] * c);
-  typedef u32x2 u32x2_any __attribute__((aligned(2)));
-  *reinterpret_cast<u32x2_any*>(p.out + b * p.o_batch + (int64_t)head * p.o_head + e) =
-      u32x2{T16<DT>::pack(r[0], r[1]), T16<DT>::pack(r[2], r[3])};
-  if (e == 0 && p.lse)
-    p.lse[b * p.q_heads + head] =
-        sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.69314718055994531f;
-}
-
 template <int CTRL, int ROWS>
 __device__ inline uint32_t add_from(uint32_t x) {
   return x + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xf, false);
@@ -633,16 +552,21 @@ __device__ inline uint32_t wave_sum(uint32_t x) {
 }
 
 // Elements e .. e + 3 of a row: o over the row's sum l, and the row's lse with element 0.
-template <int DT, int DP, bool EXT>
+template <int DT, int DP, int WAY>
 __device__ inline void finish(const AttnParams& p, int64_t b, int head, int e, f32x4 o, float m,
                               float l, int up) {
-  if constexpr (EXT) {
-    if (p.prefix.groups != 0) {
-      finish_shared<DT, DP>(p, b, head, e, o, m, l, up);
-      return;
-    }
-  }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;  // 0: nothing was attended to
+  if constexpr (WAY == kPieces) {
+    const int64_t row = b * p.q_heads + head;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) o[w] *= inv;
+    *reinterpret_cast<f32x4*>(p.prefix.own + row * DP + e) = o;
+    if (e == 0) {
+      p.prefix.own_stats[2 * row] = m;
+      p.prefix.own_stats[2 * row + 1] = ldexpf(l, -up);
+    }
+    return;
+  }
   typedef u32x2 u32x2_any __attribute__((aligned(2)));
   *reinterpret_cast<u32x2_any*>(p.out + b * p.o_batch + (int64_t)head * p.o_head + e) =
       u32x2{T16<DT>::pack(o[0] * inv, o[1] * inv), T16<DT>::pack(o[2] * inv, o[3] * inv)};
@@ -662,7 +586,7 @@ struct Piece {
 // Joins `count` partial results of a head: of workgroups wg0, wg0 + stride, ..., the one of the
 // workgroup where the head begins in slot 1 and the others in slot 0. final: the output; else a
 // partial result again, in the place of the first.
-template <int DT, int DP, bool EXT, int NW>
+template <int DT, int DP, int WAY, int NW>
 __device__ inline void join(const AttnParams& p, Shared<DP, NW>& sh, const Piece& h, uint32_t wg0,
                             uint32_t stride, uint32_t count, bool final) {
   auto slot = [&](uint32_t i) {
@@ -704,7 +628,7 @@ __device__ inline void join(const AttnParams& p, Shared<DP, NW>& sh, const Piece
       m = top;
     }
     if (final) {
-      finish<DT, DP, EXT>(p, h.b, h.head0 + row, e, o, m, l, h.up);
+      finish<DT, DP, WAY>(p, h.b, h.head0 + row, e, o, m, l, h.up);
     } else {
 #pragma unroll
       for (int w = 0; w < 4; ++w) sh.acc[0][row][e + w] = o[w];
@@ -744,7 +668,7 @@ __device__ inline void settle() {
 
 // The waves' results of tokens of one head, put together: the output if that was all of the head,
 // else a partial result in the workgroup's slot.
-template <int DT, int ST, int DP, bool CAP, bool EXT, int NW>
+template <int DT, int ST, int DP, bool CAP, int WAY, int NW>
 __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP, CAP>& w,
                                Shared<DP, NW>& sh, const Piece& h,
                                uint32_t me) {
@@ -787,7 +711,7 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP, CAP>&
       for (int k = 0; k < 4; ++k) o[k] += sh.acc[i][row][e + k];
     }
     if (whole) {
-      finish<DT, DP, EXT>(p, h.b, h.head0 + row, e, o, rm, rl, h.up);
+      finish<DT, DP, WAY>(p, h.b, h.head0 + row, e, o, rm, rl, h.up);
     } else {
       store_shared(slot + row * DP + e, o);
       if (e == 0) store_shared2(slot + p.rows * DP + 2 * row, rm, rl);
@@ -798,7 +722,7 @@ __device__ inline void combine(const AttnParams& p, const Wave<DT, ST, DP, CAP>&
 
 // The run of tiles of worker `me` of `wgs` (NW = 4: workgroups, NW = 1: waves), out of the `total` tiles
 // of all sequences and heads.
-template <int DT, int ST, int DP, bool CAP, bool EXT, int NW>
+template <int DT, int ST, int DP, bool CAP, int WAY, int NW>
 __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me, uint32_t wgs,
                             uint32_t total, uint32_t least, uint32_t whole) {
   typedef Wave<DT, ST, DP, CAP> W;
@@ -852,7 +776,7 @@ __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me
 
     W w;
     w.start(p, b, h.head0, h.n);
-    const int32_t* table = p.table + (int64_t)b * p.table_row + (EXT ? kv * p.table_head : 0);
+    const int32_t* table = p.table + (int64_t)b * p.table_row + (WAY == kHeads ? kv * p.table_head : 0);
     int64_t(*at)[2] = sh.at[wave];
     // The page of token base + lane; past the end, the last token's.
     auto page_of = [&](int64_t base) {
@@ -926,7 +850,7 @@ __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me
         }
       }
     }
-    combine<DT, ST, DP, CAP, EXT>(p, w, sh, h, me);
+    combine<DT, ST, DP, CAP, WAY>(p, w, sh, h, me);
     if (h.pieces > 1) (h.begin == me ? part[1] : part[0]) = h;
 
     cur = stop;
@@ -970,7 +894,7 @@ __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me
     uint32_t first = final ? h.begin : h.begin + g * kJoin, stride = 1;
     uint32_t count = final ? h.pieces : min((uint32_t)kJoin, h.pieces - g * kJoin);
     while (true) {
-      join<DT, DP, EXT>(p, sh, h, first, stride, count, final);
+      join<DT, DP, WAY>(p, sh, h, first, stride, count, final);
       if (final) break;
       settle<NW>();
       if (tid == 0) sh.last[i] = count_in(p.counters + h.begin, groups);
@@ -985,16 +909,12 @@ __device__ inline void work(const AttnParams& p, Shared<DP, NW>& sh, uint32_t me
   }
 }
 
-// EXT: a page table for each kv head, and prefixes that sequences share (agmm_long.h). Kernels of their
-// own, so that the others' code does not change with them.
-template <int DT, int ST, int DP, bool CAP, bool EXT>
-__global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(AttnParams p) {
-  __shared__ union {
-    Shared<DP, 4> together;
-    Shared<DP, 1> alone[4];
-  } sh;
+// What the lengths say about the work: tiles of one head; sequences with one or two, with three, with any.
+struct Census {
+  uint32_t tiles, short_ones, threes, sequences;
+};
+__device__ inline Census census(const AttnParams& p) {
   const int lane = threadIdx.x & 63;
-  // tiles; sequences with one or two; with three; with any
   uint32_t sum = 0, few = 0, mid = 0, some = 0;
   for (int b = lane; b < p.batch; b += 64) {
     const uint32_t t = tiles_of(p, p.lens[b]);
@@ -1003,66 +923,86 @@ __global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(Att
     mid += t == 3 ? 1 : 0;
     some += t ? 1 : 0;
   }
+  return Census{wave_sum(sum), wave_sum(few), wave_sum(mid), wave_sum(some)};
+}
+
+template <int DP>
+union AttnShared {
+  Shared<DP, 4> together;
+  Shared<DP, 1> alone[4];
+};
+
+// The share of workgroup `me` of `wgs`.
+template <int DT, int ST, int DP, bool CAP, int WAY>
+__device__ inline void share_of(const AttnParams& p, AttnShared<DP>& sh, const Census& c, uint32_t me,
+                                uint32_t wgs) {
   const uint32_t heads = (uint32_t)(p.c.kv_heads * p.q_groups);
-  const uint32_t tiles = wave_sum(sum), short_ones = wave_sum(few), threes = wave_sum(mid),
-                 sequences = wave_sum(some);
-  for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
-    if (tiles_of(p, p.lens[b]) == 0) {
-      const int d4 = p.c.head_dim / 4;
-      for (int i = threadIdx.x; i < p.q_heads * d4; i += kThreads) {
-        const int h = i / d4;
-        finish<DT, DP, EXT>(p, b, h, (i - h * d4) * 4, f32x4{0, 0, 0, 0}, EXT ? -INFINITY : 0.0f, 0.0f, 0);
-      }
-    }
   // Heads that all have 2 or all have 3 tiles are not cut: one workgroup's second step costs less than
   // joining (300 tokens, bf16 8.6 us, cut 9.5; 200 7.6, 9.5). With 4 tiles neither wins (9.7, 9.6). All
   // shares are alike, so none leaves heads of 2 and of 3 tiles whole both: those are cut as any others.
-  const bool twos = short_ones == sequences && tiles == 2 * sequences;
-  const uint32_t whole = threes == sequences ? 3 : twos ? 2 : 1;
+  const bool twos = c.short_ones == c.sequences && c.tiles == 2 * c.sequences;
+  const uint32_t whole = c.threes == c.sequences ? 3 : twos ? 2 : 1;
   // Where many heads have but a tile or two, a workgroup's waves would wait for each other at every
   // one of them: each wave works by itself then, on two tiles or more unless no head has more than one.
   // 96 ragged sequences (8 kv heads, e2m1, window) 26.5 us, together 45; 256 of 50 tokens (bf16) 15 us,
   // together 20. Else together: 64 of 512 (e2m1) 12 us, by themselves 17; 64 of 8192 (bf16) 355, 376;
   // and where the compute units suffice for a workgroup each: 32 of 200 (bf16, 8 kv heads) 8.0, 13.5.
-  if (tiles * heads > kCus * whole && 3 * short_ones * heads >= gridDim.x) {
+  // (Behind a shared prefix `wgs` are part of the chip's: where each has a tile at most they work together.)
+  const uint32_t enough = WAY == kPieces ? max(wgs, kCus * whole) : kCus * whole;
+  if (c.tiles * heads > enough && 3 * c.short_ones * heads >= wgs) {
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-    work<DT, ST, DP, CAP, EXT, 1>(p, sh.alone[wave], 4 * blockIdx.x + wave, 4 * gridDim.x, tiles * heads,
-                             tiles == sequences ? 1 : 2, 1);
+    work<DT, ST, DP, CAP, WAY, 1>(p, sh.alone[wave], 4 * me + wave, 4 * wgs, c.tiles * heads,
+                                  c.tiles == c.sequences ? 1 : 2, 1);
   } else {
-    work<DT, ST, DP, CAP, EXT, 4>(p, sh.together, blockIdx.x, gridDim.x, tiles * heads,
-                             tiles > kLong * sequences ? kLeast : 1, whole);
+    work<DT, ST, DP, CAP, WAY, 4>(p, sh.together, me, wgs, c.tiles * heads,
+                                  c.tiles > kLong * c.sequences ? kLeast : 1, whole);
   }
+}
+
+template <int DT, int ST, int DP, bool CAP, int WAY>
+__global__ __launch_bounds__(kThreads, attn_per_cu(ST, DP)) void attn_kernel(AttnParams p) {
+  __shared__ AttnShared<DP> sh;
+  const Census c = census(p);
+  for (int b = blockIdx.x; b < p.batch; b += gridDim.x)
+    if (tiles_of(p, p.lens[b]) == 0) {
+      const int d4 = p.c.head_dim / 4;
+      for (int i = threadIdx.x; i < p.q_heads * d4; i += kThreads) {
+        const int h = i / d4;
+        finish<DT, DP, WAY>(p, b, h, (i - h * d4) * 4, f32x4{0, 0, 0, 0}, 0.0f, 0.0f, 0);
+      }
+    }
+  share_of<DT, ST, DP, CAP, WAY>(p, sh, c, blockIdx.x, gridDim.x);
 }
 
 // Kernels with a cap are their own: its code in the others' way costs a call of one token 0.3 us of 5.7, and
 // ragged sequences to 9000, f16, 39.6 us instead of 39.2.
-template <int DT, int ST, int DP, bool EXT>
+template <int DT, int ST, int DP, int WAY>
 void by_cap(const AttnParams& p, int grid, hipStream_t s) {
   if (p.cap != 0.0f)
-    attn_kernel<DT, ST, DP, true, EXT><<<grid, kThreads, 0, s>>>(p);
+    attn_kernel<DT, ST, DP, true, WAY><<<grid, kThreads, 0, s>>>(p);
   else
-    attn_kernel<DT, ST, DP, false, EXT><<<grid, kThreads, 0, s>>>(p);
+    attn_kernel<DT, ST, DP, false, WAY><<<grid, kThreads, 0, s>>>(p);
 }
 
-template <int DT, int ST, bool EXT>
+template <int DT, int ST, int WAY>
 void by_width(const AttnParams& p, int grid, hipStream_t s) {
   const int dp = attn_padded(p.c.head_dim);
   if (dp == 64)
-    by_cap<DT, ST, 64, EXT>(p, grid, s);
+    by_cap<DT, ST, 64, WAY>(p, grid, s);
   else if (dp == 128)
-    by_cap<DT, ST, 128, EXT>(p, grid, s);
+    by_cap<DT, ST, 128, WAY>(p, grid, s);
   else
-    by_cap<DT, ST, 256, EXT>(p, grid, s);
+    by_cap<DT, ST, 256, WAY>(p, grid, s);
 }
 
-template <int DT, bool EXT>
+template <int DT, int WAY>
 void by_storage(const AttnParams& p, int storage, int grid, hipStream_t s) {
   if (storage == AG_KV_16BIT)
-    by_width<DT, AG_KV_16BIT, EXT>(p, grid, s);
+    by_width<DT, AG_KV_16BIT, WAY>(p, grid, s);
   else if (storage == AG_KV_MXFP8)
-    by_width<DT, AG_KV_MXFP8, EXT>(p, grid, s);
+    by_width<DT, AG_KV_MXFP8, WAY>(p, grid, s);
   else
-    by_width<DT, AG_KV_MXFP4, EXT>(p, grid, s);
+    by_width<DT, AG_KV_MXFP4, WAY>(p, grid, s);
 }
 
 }  // namespace

@@ -161,44 +161,54 @@ __global__ __launch_bounds__(kThreads) void score_kernel(IndexParams p) {
   int32_t j0 = (int32_t)(split * 4 + wave) * kPages;
   if (j0 >= end) return;
 
-  const bool in = 2 * c < 2 * blocks;   // a chunk of 16 codes is two blocks of 8
-  const uint16_t* q = p.q + b * p.q_batch + (int64_t)kv * p.group * p.q_head;
-  float most = 0.0f;
-  for (int h = 0; h < p.group; ++h)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int block = 2 * c + k;
-      if (!in) continue;
-      const u32x4 x = load16(q + h * p.q_head + 8 * (block < blocks ? block : block - blocks));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float f = fabsf(value_of<DT>(x[i / 2], i % 2));
-        most = fmaxf(most, f < INFINITY ? f : 0.0f);
-      }
-    }
-  const float unit = one_over(least_exponent(max_over_lanes<LC>(most)));
-  uint32_t w0[4] = {0, 0, 0, 0}, w1[4] = {0, 0, 0, 0};
+  const bool in = c < blocks;   // a chunk of 16 codes is two blocks of 8
+  // the elements that this lane's codes are multiplied by, 8 heads' loads in flight together
+  const uint16_t* q[2];
+  bool upper[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    int sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    const int block = 2 * c + k;
-    const bool upper = block < blocks;
-    if (in)
-      for (int h = 0; h < p.group; ++h) {
-        const u32x4 x = load16(q + h * p.q_head + 8 * (upper ? block : block - blocks));
+    const int block = in ? 2 * c + k : 0;
+    upper[k] = block < blocks;
+    q[k] = p.q + b * p.q_batch + (int64_t)kv * p.group * p.q_head + 8 * (upper[k] ? block : block - blocks);
+  }
+  constexpr int kHeads = 8;
+  u32x4 x[kHeads][2];
+  auto load = [&](int h0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float f = value_of<DT>(x[i / 2], i % 2);
-          const int code = fabsf(f) < INFINITY ? (int)rintf(f * unit) : 0;
-          sum[i] += upper ? max(code, 0) : min(code, 0);
-        }
+    for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) x[h][k] = load16(q[k] + min(h0 + h, p.group - 1) * p.q_head);
+  };
+  float most = 0.0f;
+  for (int h0 = 0; h0 < p.group; h0 += kHeads) {   // (the last head again past the end)
+    load(h0);
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float f = fabsf(value_of<DT>(x[h][i / 8][i % 8 / 2], i % 2));
+        most = fmaxf(most, f < INFINITY ? f : 0.0f);
       }
+  }
+  const float unit = one_over(least_exponent(max_over_lanes<LC>(in ? most : 0.0f)));
+  int sum[16] = {};
+  for (int h0 = 0; h0 < p.group; h0 += kHeads) {
+    if (p.group > kHeads) load(h0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int hi = sum[i] / 128, lo = sum[i] - 128 * hi;
-      w1[2 * k + i / 4] |= (uint32_t)(hi & 255) << (8 * (i % 4));
-      w0[2 * k + i / 4] |= (uint32_t)(lo & 255) << (8 * (i % 4));
-    }
+    for (int h = 0; h < kHeads; ++h)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float f = value_of<DT>(x[h][i / 8][i % 8 / 2], i % 2);
+        const int code = fabsf(f) < INFINITY && h0 + h < p.group ? (int)rintf(f * unit) : 0;
+        sum[i] += upper[i / 8] ? max(code, 0) : min(code, 0);
+      }
+  }
+  uint32_t w0[4] = {0, 0, 0, 0}, w1[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int s = in ? sum[i] : 0, hi = s / 128, lo = s - 128 * hi;
+    w1[i / 4] |= (uint32_t)(hi & 255) << (8 * (i % 4));
+    w0[i / 4] |= (uint32_t)(lo & 255) << (8 * (i % 4));
   }
   const int32_t* table = p.table + b * p.table_row;
   for (; j0 < end; j0 += kUnroll * step) {

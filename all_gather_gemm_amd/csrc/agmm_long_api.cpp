@@ -18,11 +18,11 @@ constexpr int64_t kHeads = 1 << 21;  // sequences times kv heads: each has a wor
 // ---- prefixes ----
 
 struct Scratch {
-  int64_t slots, sums, stats, bytes;  // offsets behind the groups
+  int64_t slots, sums, stats, own, own_stats, bytes;  // offsets behind the groups
 };
 
 int prefix_wgs(const ag_attn_desc& d) {
-  return d.num_wgs ? d.num_wgs : prefix_per_cu(attn_padded(d.head_dim)) * kCompute;
+  return d.num_wgs ? std::max(2, d.num_wgs) : prefix_per_cu(attn_padded(d.head_dim)) * kCompute;
 }
 
 // A strip for every 128 rows of a kv head, and an unfilled one for each group; a piece for each strip and for
@@ -33,10 +33,14 @@ int scratch_of(const ag_attn_desc& d, int64_t batch, int64_t groups, Scratch* s)
   if (batch >= kWide || groups >= kWide || (double)batch * group >= (double)kWide) return AGMM_ERR_UNSUPPORTED;
   const int64_t strips = batch * group / kPrefixRows + std::min(batch, groups);
   if ((double)strips * d.kv_heads >= (double)kWide / 2) return AGMM_ERR_UNSUPPORTED;
+  // (threads of the joining: numbers of 32 bits)
+  if ((double)batch * d.q_heads * (d.head_dim / 4) >= (double)kWide) return AGMM_ERR_UNSUPPORTED;
   s->slots = strips * d.kv_heads + prefix_wgs(d);
   s->sums = align256(groups * (int64_t)sizeof(PrefixGroup));
   s->stats = s->sums + s->slots * kPrefixRows * attn_padded(d.head_dim) * 4;
-  s->bytes = s->stats + align256(s->slots * kPrefixRows * 2 * 4);
+  s->own = s->stats + align256(s->slots * kPrefixRows * 2 * 4);
+  s->own_stats = s->own + batch * d.q_heads * attn_padded(d.head_dim) * 4;
+  s->bytes = align256(s->own_stats + batch * d.q_heads * 2 * 4);
   return AGMM_OK;
 }
 
@@ -119,33 +123,38 @@ int ag_prefix_run(ag_attn_handle* h, const ag_kv_cache* cache, const void* q, in
   Scratch s;
   rc = scratch_of(d, batch, groups, &s);
   if (rc != AGMM_OK) return rc;
-  if (groups > 0) {
-    if (!aligned(prefix_lens, 4) || (prefix_pages > 0 && !aligned(prefix_table, 4)) ||
-        (starts ? !aligned(starts, 4) : groups != 1) || !aligned(scratch, 256) || scratch_bytes < s.bytes)
-      return AGMM_ERR_INVALID_ARG;
-    if (prefix_pages >= kWide || prefix_pages * cache->page_size >= kWide) return AGMM_ERR_UNSUPPORTED;
-    PrefixParams p;
-    memset(&p, 0, sizeof(p));
-    a.prefix.info = (PrefixGroup*)scratch;
-    a.prefix.sums = (float*)((char*)scratch + s.sums);
-    a.prefix.stats = (float*)((char*)scratch + s.stats);
-    a.prefix.groups = (uint32_t)groups;
-    p.a = a;
-    p.a.table = prefix_table;
-    p.a.table_row = prefix_row;
-    p.a.capacity = cache->num_pages > 0 ? (int32_t)(prefix_pages * cache->page_size) : 0;
-    p.lens = prefix_lens;
-    p.starts = starts;
-    p.groups = (uint32_t)groups;
-    p.least = 2;
-    const int64_t tokens = 8192 / attn_padded(d.head_dim);
-    const int64_t strips = s.slots - prefix_wgs(d);
-    const int64_t tiles = (p.a.capacity + tokens - 1) / tokens;
-    if ((double)tiles * strips >= (double)kWide) return AGMM_ERR_UNSUPPORTED;
-    const int wgs = (int)std::min<int64_t>(prefix_wgs(d), std::max<int64_t>(1, tiles * strips));
-    ATTN_HIP(launch_prefix(p, d.dtype, d.storage, wgs, (hipStream_t)hip_stream));
+  if (groups == 0) {
+    ATTN_HIP(launch_attn(a, d.dtype, d.storage, grid, (hipStream_t)hip_stream));
+    return AGMM_OK;
   }
-  ATTN_HIP(launch_attn_ext(a, d.dtype, d.storage, grid, (hipStream_t)hip_stream));
+  if (!aligned(prefix_lens, 4) || (prefix_pages > 0 && !aligned(prefix_table, 4)) ||
+      (starts ? !aligned(starts, 4) : groups != 1) || !aligned(scratch, 256) || scratch_bytes < s.bytes)
+    return AGMM_ERR_INVALID_ARG;
+  if (prefix_pages >= kWide || prefix_pages * cache->page_size >= kWide) return AGMM_ERR_UNSUPPORTED;
+  PrefixParams p;
+  memset(&p, 0, sizeof(p));
+  a.prefix.info = (PrefixGroup*)scratch;
+  a.prefix.sums = (float*)((char*)scratch + s.sums);
+  a.prefix.stats = (float*)((char*)scratch + s.stats);
+  a.prefix.own = (float*)((char*)scratch + s.own);
+  a.prefix.own_stats = (float*)((char*)scratch + s.own_stats);
+  a.prefix.groups = (uint32_t)groups;
+  p.own = a;
+  p.table = prefix_table;
+  p.table_row = prefix_row;
+  p.capacity = cache->num_pages > 0 ? (int32_t)(prefix_pages * cache->page_size) : 0;
+  p.lens = prefix_lens;
+  p.starts = starts;
+  p.least = 2;
+  const int64_t tokens = 8192 / attn_padded(d.head_dim);
+  const int64_t strips = s.slots - prefix_wgs(d);
+  const int64_t tiles = (p.capacity + tokens - 1) / tokens;
+  if ((double)tiles * strips >= (double)kWide) return AGMM_ERR_UNSUPPORTED;
+  p.own_wgs = (uint32_t)attn_workgroups(h);   // that their workspace is for
+  const int wgs = (int)std::min<int64_t>(prefix_wgs(d), std::max<int64_t>(2, tiles * strips + grid));
+  ATTN_HIP(d.dtype == AGMM_F16 ? launch_prefix_f16(p, d.storage, wgs, (hipStream_t)hip_stream)
+                               : launch_prefix_bf16(p, d.storage, wgs, (hipStream_t)hip_stream));
+  ATTN_HIP(launch_prefix_join(p, d.dtype, (hipStream_t)hip_stream));
   return AGMM_OK;
 }
 
@@ -160,7 +169,7 @@ int ag_attn_run_heads(ag_attn_handle* h, const ag_kv_cache* cache, const void* q
   if (rc != AGMM_OK || grid == 0) return rc;
   a.table_head = table_head;
   const ag_attn_desc& d = attn_desc(h);
-  ATTN_HIP(launch_attn_ext(a, d.dtype, d.storage, grid, (hipStream_t)hip_stream));
+  ATTN_HIP(launch_attn_heads(a, d.dtype, d.storage, grid, (hipStream_t)hip_stream));
   return AGMM_OK;
 }
 
@@ -216,7 +225,7 @@ int ag_index_select(const ag_kv_cache* cache, const ag_page_index* index, const 
   p.group = (int32_t)(q_heads / cache->kv_heads);
   p.keys = (uint32_t*)scratch;
   const int64_t at_once = 64 / (attn_padded(cache->head_dim) / 8);
-  p.splits = splits_of(4 * kCompute, heads, (table_len + at_once - 1) / at_once);
+  p.splits = splits_of(16 * kCompute, heads, (table_len + at_once - 1) / at_once);
   if (p.pages > 0) ATTN_HIP(launch_index_score(p, cache->dtype, batch, (hipStream_t)hip_stream));
   ChooseParams c;
   memset(&c, 0, sizeof(c));

@@ -7,15 +7,20 @@
 namespace agmm {
 
 struct PrefixParams {
-  AttnParams a;            // table and capacity of the prefixes; prefix: where the pieces go
+  AttnParams own;          // the sequences' own tokens; prefix: where the pieces go
+  const int32_t* table;    // of the prefixes
+  int64_t table_row;
+  int32_t capacity;        // tokens that it reaches
   const int32_t* lens;     // of the prefixes
   const int32_t* starts;   // or nullptr: one group
-  uint32_t groups;
   uint32_t least;          // tiles of a workgroup's run
+  uint32_t own_wgs;        // workgroups on own tokens, at most
 };
-// Workgroups of the prefixes' kernel that share a compute unit, by its registers
+// Workgroups that share a compute unit, by their registers
 constexpr int prefix_per_cu(int padded) { return padded == 256 ? 1 : 2; }
-hipError_t launch_prefix(const PrefixParams& p, int dtype, int storage, int grid, hipStream_t s);
+hipError_t launch_prefix_f16(const PrefixParams& p, int storage, int grid, hipStream_t s);
+hipError_t launch_prefix_bf16(const PrefixParams& p, int storage, int grid, hipStream_t s);
+hipError_t launch_prefix_join(const PrefixParams& p, int dtype, hipStream_t s);
 
 struct IndexParams {
   CacheView c;

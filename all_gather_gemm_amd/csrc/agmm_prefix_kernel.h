@@ -23,6 +23,8 @@
 // sums of weights in the scratch; the kernel of the sequences' own tokens joins them, in the order of the
 // pieces, with those (finish_shared in agmm_attn_kernel.h). Consecutive runs go to workgroups of one XCD, so that
 // strips of one kv head find its tiles in one L2.
+#pragma once
+
 #include "agmm_attn_kernel.h"
 #include "agmm_long_internal.h"
 
@@ -64,7 +66,7 @@ struct Tile {
 };
 
 template <int DP>
-struct PrefixShared {
+struct TileShared {
   char k[2][Tile<DP>::kBytes], v[2][Tile<DP>::kBytes];
   int64_t at[4][Tile<DP>::kTokens][2];  // the tokens' places: data and scale offsets, for each wave
 };
@@ -103,14 +105,14 @@ template <int DP>
 __device__ inline PrefixScan scan_groups(const PrefixParams& p, uint32_t base, PrefixCarry& c) {
   const int lane = threadIdx.x & 63;
   const uint32_t g = base + lane;
-  const AttnParams& a = p.a;
+  const AttnParams& a = p.own;
   PrefixScan r = {};
   // A group ends where the next begins, and none begins before another's end: whatever `starts` holds,
   // sequences are in one group at most.
   int32_t end = 0;
-  if (g < p.groups) {
+  if (g < a.prefix.groups) {
     end = p.starts ? max(0, min(p.starts[g + 1], a.batch)) : a.batch;
-    r.len = max(0, min(p.lens[g], a.capacity));
+    r.len = max(0, min(p.lens[g], p.capacity));
   }
   int32_t run = end;  // the largest end up to this lane
 #pragma unroll
@@ -124,7 +126,7 @@ __device__ inline PrefixScan scan_groups(const PrefixParams& p, uint32_t base, P
   const int32_t lowest = max(c.last, floor0);
   r.first = max(before, lowest);
   r.end = max(run, lowest);
-  if (g < p.groups && r.len > 0 && r.end > r.first) {
+  if (g < a.prefix.groups && r.len > 0 && r.end > r.first) {
     r.tiles = (uint32_t)((r.len + Tile<DP>::kTokens - 1) / Tile<DP>::kTokens);
     r.row_tiles = ((uint32_t)(r.end - r.first) * a.group + kPrefixRows - 1) / kPrefixRows;
     r.strips = r.row_tiles * a.c.kv_heads;
@@ -132,7 +134,7 @@ __device__ inline PrefixScan scan_groups(const PrefixParams& p, uint32_t base, P
   const uint32_t s = wave_scan(r.strips), t = wave_scan(r.strips * r.tiles);
   r.strip0 = c.strips + s - r.strips;
   r.tile0 = c.tiles + t - r.strips * r.tiles;
-  c.last = max(c.last, __shfl(r.end, 63));
+  c.last = max(c.last, (int32_t)last_lane((uint32_t)r.end));
   c.strips += last_lane(s);
   c.tiles += last_lane(t);
   return r;
@@ -388,7 +390,7 @@ struct PrefixWave {
   // The piece's sums, maxima and sums of weights.
   __device__ inline void leave(const PrefixParams& p, uint32_t slot, int row) const {
     const int h = (threadIdx.x & 63) >> 5;
-    float* to = p.a.prefix.sums + (int64_t)slot * kPrefixRows * DP;
+    float* to = p.own.prefix.sums + (int64_t)slot * kPrefixRows * DP;
 #pragma unroll
     for (int i = 0; i < kParts; ++i)
 #pragma unroll
@@ -399,52 +401,33 @@ struct PrefixWave {
                                                     __builtin_bit_cast(uint32_t, l), false, false);
     const float sum = __builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]);
     if (h == 0) {
-      float* s = p.a.prefix.stats + ((int64_t)slot * kPrefixRows + row) * 2;
+      float* s = p.own.prefix.stats + ((int64_t)slot * kPrefixRows + row) * 2;
       s[0] = m;
       s[1] = sum;
     }
   }
 };
 
+// The share of workgroup `me` of those that work on prefixes, of which each has a run of `quota` of all tiles.
 template <int DT, int ST, int DP, bool CAP, bool DMA>
-__global__ __launch_bounds__(kThreads, prefix_per_cu(DP)) void prefix_kernel(PrefixParams p) {
+__device__ inline void prefix_share(const PrefixParams& p, TileShared<DP>& sh, const PrefixScan* scan0,
+                                    const PrefixCarry& carry0, uint32_t me, uint32_t total, uint32_t quota) {
   typedef Tile<DP> T;
   typedef PrefixWave<DT, ST, DP, CAP, DMA> W;
-  __shared__ PrefixShared<DP> sh;
-  const AttnParams& a = p.a;
+  const AttnParams& a = p.own;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const uint32_t wgs = gridDim.x;
-  // consecutive numbers to the workgroups of an XCD, which are 8 apart
-  const uint32_t xcd = blockIdx.x % 8, each = wgs / 8, more = wgs % 8;
-  const uint32_t me = xcd * each + min(xcd, more) + blockIdx.x / 8;
-
-  PrefixCarry c = {0, 0, 0};
-  for (uint32_t g = 0; g < p.groups; g += 64) scan_groups<DP>(p, g, c);
-  const uint32_t total = c.tiles;
-  // runs of p.least tiles at least, as long as every compute unit gets one
-  const uint32_t quota = max(max((total + wgs - 1) / wgs, 1u),
-                             min(p.least, (total + kCus - 1) / kCus));
-  if (me == 0 && wave == 0) {
-    c = {0, 0, 0};
-    for (uint32_t g = 0; g < p.groups; g += 64) {
-      const PrefixScan r = scan_groups<DP>(p, g, c);
-      if (g + lane < p.groups)
-        a.prefix.info[g + lane] =
-            PrefixGroup{r.first, r.end, r.tiles, r.row_tiles, r.strip0, r.tile0, head_of<DT>(r.len), quota};
-    }
-  }
   uint32_t cur = me * quota;
   if (cur >= total) return;
   const uint32_t end = min(cur + quota, total);
 
   while (cur < end) {
     // the group and strip of tile `cur`
-    c = {0, 0, 0};
     PrefixScan r = {};
     uint32_t group = 0;
-    for (uint32_t g = 0; g < p.groups; g += 64) {
-      const PrefixScan s = scan_groups<DP>(p, g, c);
+    PrefixCarry c = carry0;
+    for (uint32_t g = 0; g < a.prefix.groups; g += 64) {
+      const PrefixScan s = g == 0 ? scan0[lane] : scan_groups<DP>(p, g, c);
       const uint64_t hit = __ballot(s.strips * s.tiles != 0 && cur >= s.tile0 &&
                                     cur < s.tile0 + s.strips * s.tiles);
       if (hit) {
@@ -470,7 +453,7 @@ __global__ __launch_bounds__(kThreads, prefix_per_cu(DP)) void prefix_kernel(Pre
     const int32_t first = __builtin_amdgcn_readfirstlane(r.first);
     const int32_t rows = (__builtin_amdgcn_readfirstlane(r.end) - first) * a.group;
     const int32_t len = __builtin_amdgcn_readfirstlane(r.len);
-    const int32_t* table = a.table + (int64_t)group * a.table_row;
+    const int32_t* table = p.table + (int64_t)group * p.table_row;
     const int up = head_of<DT>(len);
     for (uint32_t strip = (cur - tile0) / tiles; strip < strips && cur < end; ++strip) {
       const uint32_t begin = tile0 + strip * tiles, stop = min(end, begin + tiles);
@@ -555,9 +538,76 @@ __global__ __launch_bounds__(kThreads, prefix_per_cu(DP)) void prefix_kernel(Pre
   }
 }
 
+// The length of the runs that prefixes' `total` tiles are cut into, so that the workgroups that are left for the
+// `own` tiles take as long. Each lane works out one length: a prefix's tile takes 3.15 us where two workgroups share
+// a compute unit (128 rows against 64 tokens of 128 elements), an own one some 3.5. Runs have at least `least` tiles,
+// as long as every compute unit gets one.
+__device__ inline uint32_t run_length(uint32_t total, uint32_t own, uint32_t wgs, uint32_t least) {
+  constexpr float kTile = 0.8f;
+  const uint32_t lane = threadIdx.x & 63;
+  const uint32_t shortest = max(max(1u, min(least, (total + kCus - 1) / kCus)), (total + wgs - 1) / wgs);
+  // (the last lane's is all of it in one run: that always leaves a workgroup)
+  const uint32_t quota = lane < 63 ? shortest + lane * max(1u, shortest / 64) : max(shortest, total);
+  const uint32_t x = (total + quota - 1) / quota;
+  float t = (float)quota * kTile;
+  if (own) t = x < wgs ? fmaxf(t, (float)((own + wgs - x - 1) / max(wgs - x, 1u))) : INFINITY;
+  float best = t;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) best = fminf(best, __shfl_xor(best, d));
+  const int at = __builtin_ctzll(__ballot(t == best));
+  return (uint32_t)__builtin_amdgcn_readlane((int)quota, at);
+}
+
+// Prefixes and own tokens in one launch, so that the products of the ones run beside the loads of the others: of the
+// workgroups, which are all on the chip at once, each part has as many as its share of the work, in every XCD alike.
+template <int DT, int ST, int DP, bool CAP, bool DMA>
+__global__ __launch_bounds__(kThreads, prefix_per_cu(DP)) void prefix_kernel(PrefixParams p) {
+  __shared__ union {
+    TileShared<DP> tiles;
+    AttnShared<DP> own;
+  } sh;
+  __shared__ PrefixScan scan0[64];
+  const AttnParams& a = p.own;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  // (what the first 64 groups' scan gives is kept: most calls have no more)
+  PrefixCarry carry0 = {0, 0, 0};
+  scan0[lane] = scan_groups<DP>(p, 0, carry0);   // (every wave writes the same)
+  __syncthreads();
+  PrefixCarry c = carry0;
+  for (uint32_t g = 64; g < a.prefix.groups; g += 64) scan_groups<DP>(p, g, c);
+  const uint32_t total = c.tiles;
+  const Census own = census(a);
+  const uint32_t own_tiles = own.tiles * (uint32_t)(a.c.kv_heads * a.q_groups);
+  const uint32_t wgs = gridDim.x;
+  const uint32_t quota = run_length(total, own_tiles, wgs, p.least);
+  const uint32_t x = (total + quota - 1) / quota;   // workgroups that have a run
+  if (blockIdx.x == 0 && wave == 0) {
+    c = carry0;
+    for (uint32_t g = 0; g < a.prefix.groups; g += 64) {
+      const PrefixScan r = g == 0 ? scan0[lane] : scan_groups<DP>(p, g, c);
+      if (g + lane < a.prefix.groups)
+        a.prefix.info[g + lane] =
+            PrefixGroup{r.first, r.end, r.tiles, r.row_tiles, r.strip0, r.tile0, head_of<DT>(r.len), quota};
+    }
+  }
+  // Consecutive numbers to the workgroups of an XCD, which are 8 apart, so that strips of one kv head find its
+  // tiles in one L2; the first of each XCD's are the prefixes'.
+  const uint32_t xcd = blockIdx.x % 8, local = blockIdx.x / 8;
+  const uint32_t from = xcd * (wgs / 8) + min(xcd, wgs % 8), size = wgs / 8 + (xcd < wgs % 8 ? 1 : 0);
+  const uint32_t first = (uint32_t)((uint64_t)x * from / wgs);
+  const uint32_t mine = (uint32_t)((uint64_t)x * (from + size) / wgs) - first;
+  if (local < mine) {
+    prefix_share<DT, ST, DP, CAP, DMA>(p, sh.tiles, scan0, carry0, first + local, total, quota);
+  } else {
+    const uint32_t other = from - first + local - mine, others = min(wgs - x, p.own_wgs);
+    if (other < others) share_of<DT, ST, DP, CAP, kPieces>(a, sh.own, own, other, others);
+  }
+}
+
 template <int DT, int ST, int DP, bool DMA>
 void prefix_by_cap(const PrefixParams& p, int grid, hipStream_t s) {
-  if (p.a.cap != 0.0f)
+  if (p.own.cap != 0.0f)
     prefix_kernel<DT, ST, DP, true, DMA><<<grid, kThreads, 0, s>>>(p);
   else
     prefix_kernel<DT, ST, DP, false, DMA><<<grid, kThreads, 0, s>>>(p);
@@ -566,7 +616,7 @@ void prefix_by_cap(const PrefixParams& p, int grid, hipStream_t s) {
 template <int DT, int ST, int DP>
 void prefix_by_rows(const PrefixParams& p, int grid, hipStream_t s) {
   if constexpr (ST == AG_KV_16BIT) {
-    if (p.a.c.head_dim == DP) {
+    if (p.own.c.head_dim == DP) {
       prefix_by_cap<DT, ST, DP, true>(p, grid, s);
       return;
     }
@@ -576,7 +626,7 @@ void prefix_by_rows(const PrefixParams& p, int grid, hipStream_t s) {
 
 template <int DT, int ST>
 void prefix_by_width(const PrefixParams& p, int grid, hipStream_t s) {
-  const int dp = attn_padded(p.a.c.head_dim);
+  const int dp = attn_padded(p.own.c.head_dim);
   if (dp == 64)
     prefix_by_rows<DT, ST, 64>(p, grid, s);
   else if (dp == 128)
@@ -586,23 +636,15 @@ void prefix_by_width(const PrefixParams& p, int grid, hipStream_t s) {
 }
 
 template <int DT>
-void prefix_by_storage(const PrefixParams& p, int storage, int grid, hipStream_t s) {
+hipError_t prefix_by_storage(const PrefixParams& p, int storage, int grid, hipStream_t s) {
   if (storage == AG_KV_16BIT)
     prefix_by_width<DT, AG_KV_16BIT>(p, grid, s);
   else if (storage == AG_KV_MXFP8)
     prefix_by_width<DT, AG_KV_MXFP8>(p, grid, s);
   else
     prefix_by_width<DT, AG_KV_MXFP4>(p, grid, s);
-}
-
-}  // namespace
-
-hipError_t launch_prefix(const PrefixParams& p, int dtype, int storage, int grid, hipStream_t s) {
-  if (dtype == AGMM_F16)
-    prefix_by_storage<AGMM_F16>(p, storage, grid, s);
-  else
-    prefix_by_storage<AGMM_BF16>(p, storage, grid, s);
   return hipGetLastError();
 }
 
+}  // namespace
 }  // namespace agmm

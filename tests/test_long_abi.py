@@ -57,12 +57,13 @@ def desc(L, **kw):
 
 def test_prefix_scratch(L):
     # the groups' plans; for each strip of 128 rows, unfilled one of a group and workgroup a piece of 128 padded
-    # rows, with their maxima and sums
+    # rows, with their maxima and sums; and the same of each row for the own tokens
     al = lambda x: (x + 255) & ~255  # noqa: E731
     for dim, padded, wgs in ((64, 64, 512), (80, 128, 512), (256, 256, 256)):
         for batch, groups, q, kv in ((1, 1, 8, 1), (100, 3, 64, 8), (7, 20, 6, 2), (0, 0, 4, 4), (300, 300, 1, 1)):
             slots = kv * (batch * (q // kv) // 128 + min(batch, groups)) + wgs
             want = al(32 * groups) + slots * 128 * padded * 4 + al(slots * 1024)
+            want = al(want + batch * q * (padded + 2) * 4)
             d = desc(L, head_dim=dim, q_heads=q, kv_heads=kv)
             assert L.lib.ag_prefix_scratch_bytes(ctypes.byref(d), batch, groups) == want
     d = ctypes.byref(desc(L))
