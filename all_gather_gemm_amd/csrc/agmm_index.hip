@@ -141,75 +141,94 @@ __device__ inline uint32_t order_key(float x) {
   return w >> 31 ? ~w : w | 0x80000000u;
 }
 
-// The scores of a sequence's pages for one kv head. The sum over the q heads is taken first: a page's codes are
-// multiplied by a_d = sum of the positive codes of element d, and by that of the negative ones, which are
-// within 127 * 128; in two parts of 8 bits, 128 x + y, they go through v_dot4_i32_i8. LC lanes have 16 codes each.
+template <int LC>
+struct ScoreShared {
+  int sum[2][8 * LC];   // of the elements' positive codes, and of the negative ones
+  float most[kThreads / 64];
+};
+
+// What a page's codes are multiplied by, for one sequence and kv head: the sums over the q heads of the positive
+// codes of each element, and of the negative ones. The workgroup makes them together, a thread some heads of one
+// element; a lane gets its 16 in two parts of 8 bits, 128 x + y, for v_dot4_i32_i8 (they are within 127 * 128).
+template <int DT, int LC>
+__device__ inline void weights_of(const IndexParams& p, int64_t b, int kv, ScoreShared<LC>& sh,
+                                  uint32_t (&w0)[4], uint32_t (&w1)[4]) {
+  constexpr int kDim = 8 * LC, kPer = kThreads / kDim, kIn = 4;
+  const int tid = threadIdx.x, e = tid % kDim, part = tid / kDim, hd = p.c.head_dim;
+  const uint16_t* q = p.q + b * p.q_batch + (int64_t)kv * p.group * p.q_head + (e < hd ? e : 0);
+  uint16_t x[kIn];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < kIn; ++i) x[i] = q[(int64_t)min(h0 + i * kPer, p.group - 1) * p.q_head];
+  };
+  auto value = [&](int h, int i) {
+    const float f = value_of<DT>(x[i], 0);
+    return fabsf(f) < INFINITY && h < p.group && e < hd ? f : 0.0f;
+  };
+  float most = 0.0f;
+  for (int h0 = part; h0 < p.group; h0 += kIn * kPer) {
+    load(h0);
+#pragma unroll
+    for (int i = 0; i < kIn; ++i) most = fmaxf(most, fabsf(value(h0 + i * kPer, i)));
+  }
+  most = max_over_lanes<32>(most);
+  most = fmaxf(most, __shfl_xor(most, 32));
+  if (tid < kDim) sh.sum[0][e] = sh.sum[1][e] = 0;
+  if ((tid & 63) == 0) sh.most[tid >> 6] = most;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kThreads / 64; ++i) most = fmaxf(most, sh.most[i]);
+  const float unit = one_over(least_exponent(most));
+  int up = 0, down = 0;
+  for (int h0 = part; h0 < p.group; h0 += kIn * kPer) {
+    if (p.group > kIn * kPer) load(h0);
+#pragma unroll
+    for (int i = 0; i < kIn; ++i) {
+      const int code = (int)rintf(value(h0 + i * kPer, i) * unit);
+      up += max(code, 0);
+      down += min(code, 0);
+    }
+  }
+  if (e < hd) {
+    atomicAdd(&sh.sum[0][e], up);
+    atomicAdd(&sh.sum[1][e], down);
+  }
+  __syncthreads();
+  const int c = (tid & 63) % LC;   // chunk: 16 of the 2 * hd codes, two blocks of 8
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w0[i] = w1[i] = 0;
+  if (c >= hd / 8) return;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int at = 16 * c + i;
+    const int s = at < hd ? sh.sum[0][at] : sh.sum[1][at - hd], hi = s / 128, lo = s - 128 * hi;
+    w1[i / 4] |= (uint32_t)(hi & 255) << (8 * (i % 4));
+    w0[i / 4] |= (uint32_t)(lo & 255) << (8 * (i % 4));
+  }
+}
+
+// The scores of a sequence's pages for one kv head, LC lanes to a page.
 template <int DT, int LC>
 __global__ __launch_bounds__(kThreads) void score_kernel(IndexParams p) {
   constexpr int kPages = 64 / LC, kUnroll = 4;
+  __shared__ ScoreShared<LC> sh;
   const int lane = threadIdx.x & 63, c = lane % LC, r0 = lane / LC;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const uint32_t bh = blockIdx.x / (uint32_t)p.splits, split = blockIdx.x - bh * (uint32_t)p.splits;
   const int64_t b = bh / (uint32_t)p.c.kv_heads;
   const int kv = (int)(bh - (uint32_t)b * p.c.kv_heads);
-  const int32_t ps = (int32_t)p.c.page_size.d, hd = p.c.head_dim, blocks = hd / 8;
+  const int32_t ps = (int32_t)p.c.page_size.d, hd = p.c.head_dim;
   const int64_t len = min((int64_t)max(p.lens[b], 0), (int64_t)p.pages * ps);
   const int32_t end = (int32_t)((len + ps - 1) / ps);
   const int32_t stride = (p.pages + 3) & ~3;
   uint32_t* keys = p.keys + (int64_t)bh * stride;
   const int32_t step = (int32_t)p.splits * 4 * kPages;
   int32_t j0 = (int32_t)(split * 4 + wave) * kPages;
-  if (j0 >= end) return;
+  if ((int32_t)split * 4 * kPages >= end) return;   // (nothing for the whole workgroup)
 
-  const bool in = c < blocks;   // a chunk of 16 codes is two blocks of 8
-  // the elements that this lane's codes are multiplied by, 8 heads' loads in flight together
-  const uint16_t* q[2];
-  bool upper[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int block = in ? 2 * c + k : 0;
-    upper[k] = block < blocks;
-    q[k] = p.q + b * p.q_batch + (int64_t)kv * p.group * p.q_head + 8 * (upper[k] ? block : block - blocks);
-  }
-  constexpr int kHeads = 8;
-  u32x4 x[kHeads][2];
-  auto load = [&](int h0) {
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h)
-#pragma unroll
-      for (int k = 0; k < 2; ++k) x[h][k] = load16(q[k] + min(h0 + h, p.group - 1) * p.q_head);
-  };
-  float most = 0.0f;
-  for (int h0 = 0; h0 < p.group; h0 += kHeads) {   // (the last head again past the end)
-    load(h0);
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float f = fabsf(value_of<DT>(x[h][i / 8][i % 8 / 2], i % 2));
-        most = fmaxf(most, f < INFINITY ? f : 0.0f);
-      }
-  }
-  const float unit = one_over(least_exponent(max_over_lanes<LC>(in ? most : 0.0f)));
-  int sum[16] = {};
-  for (int h0 = 0; h0 < p.group; h0 += kHeads) {
-    if (p.group > kHeads) load(h0);
-#pragma unroll
-    for (int h = 0; h < kHeads; ++h)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float f = value_of<DT>(x[h][i / 8][i % 8 / 2], i % 2);
-        const int code = fabsf(f) < INFINITY && h0 + h < p.group ? (int)rintf(f * unit) : 0;
-        sum[i] += upper[i / 8] ? max(code, 0) : min(code, 0);
-      }
-  }
-  uint32_t w0[4] = {0, 0, 0, 0}, w1[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int s = in ? sum[i] : 0, hi = s / 128, lo = s - 128 * hi;
-    w1[i / 4] |= (uint32_t)(hi & 255) << (8 * (i % 4));
-    w0[i / 4] |= (uint32_t)(lo & 255) << (8 * (i % 4));
-  }
+  uint32_t w0[4], w1[4];
+  weights_of<DT, LC>(p, b, kv, sh, w0, w1);
+  const bool in = c < hd / 8;
   const int32_t* table = p.table + b * p.table_row;
   for (; j0 < end; j0 += kUnroll * step) {
     int32_t page[kUnroll];
@@ -253,7 +272,7 @@ template <int T>
 struct ChooseShared {
   uint32_t hist[2048];
   uint32_t waves[T / 64];
-  uint32_t bin, left;
+  uint32_t bin, left, held;
 };
 
 // Sum over the workgroup's threads in front of this one, and over all.
@@ -276,8 +295,10 @@ __device__ inline uint32_t block_scan(uint32_t x, uint32_t* waves, uint32_t& all
 }
 
 // One workgroup chooses for one sequence and head: the keys of all items, the `budget`-th largest found by
-// three histograms of 11, 11 and 10 bits, then the chosen items written in order. A thread has K consecutive
-// items, in registers where the workgroup has all of them at once.
+// histograms of 11, 11 and 10 bits (as many as it takes), then the chosen items written in order. A thread has K
+// consecutive items, in registers where the workgroup has all of them at once.
+//
+// One workgroup's time is what counts, and of that the instructions for each item.
 template <int T, int K, bool TOKENS>
 __global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
   __shared__ ChooseShared<T> sh;
@@ -291,27 +312,36 @@ __global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
   const uint32_t* keys = TOKENS ? nullptr : p.keys + (int64_t)blockIdx.x * p.key_stride;
   const float* mass = TOKENS ? p.mass + b * p.mass_batch + head * p.mass_head : nullptr;
   auto there = [&](int32_t page) { return (uint32_t)page < (uint32_t)p.num_pages; };
+  constexpr int kBins = 2048 / T;
 
   uint32_t k[K];
   auto load = [&](int32_t base) {
     const int32_t i0 = base + tid * K;
     if constexpr (TOKENS) {
       typedef f32x4 f32x4_any __attribute__((aligned(4)));
+      f32x4 x[K / 4];
 #pragma unroll
       for (int i = 0; i < K; i += 4) {
-        f32x4 x = {0, 0, 0, 0};
+        x[i / 4] = f32x4{0, 0, 0, 0};
         if (i0 + i + 4 <= n)
-          x = *reinterpret_cast<const f32x4_any*>(mass + i0 + i);
+          x[i / 4] = *reinterpret_cast<const f32x4_any*>(mass + i0 + i);
         else
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            if (i0 + i + u < n) x[u] = mass[i0 + i + u];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) k[i + u] = order_key(x[u]);
+            if (i0 + i + u < n) x[i / 4][u] = mass[i0 + i + u];
       }
+      if (ps >= K) {   // a thread's tokens are in two pages at most
+        const uint32_t j = (uint32_t)min(i0, n - 1) / p.page_size;   // (n > 0)
+        const int32_t left = (int32_t)(j + 1) * ps - i0;   // tokens of the first
+        const bool ok0 = there(table[j]), ok1 = i0 + left < n && there(table[min((int32_t)j + 1, p.pages - 1)]);
 #pragma unroll
-      for (int i = 0; i < K; ++i)
-        if (i0 + i >= n || !there(table[(uint32_t)(i0 + i) / p.page_size])) k[i] = 0;
+        for (int i = 0; i < K; ++i)
+          k[i] = i0 + i < n && (i < left ? ok0 : ok1) ? order_key(x[i / 4][i % 4]) : 0u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+          k[i] = i0 + i < n && there(table[(uint32_t)(i0 + i) / p.page_size]) ? order_key(x[i / 4][i % 4]) : 0u;
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < K; i += 4) {
@@ -321,62 +351,66 @@ __global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
         for (int u = 0; u < 4; ++u) k[i + u] = i0 + i + u < n ? x[u] : 0;
       }
     }
+    if (i0 < p.sink || i0 + K > n - p.recent)
 #pragma unroll
-    for (int i = 0; i < K; ++i)
-      if (k[i] != 0 && (i0 + i < p.sink || i0 + i >= n - p.recent)) k[i] = kForced;
+      for (int i = 0; i < K; ++i)
+        if (k[i] != 0 && (i0 + i < p.sink || i0 + i >= n - p.recent)) k[i] = kForced;
   };
   const bool once = n <= T * K;
-  if (once) load(0);
-  uint32_t present = 0;
-  for (int32_t base = 0; base < n; base += T * K) {
-    if (!once) load(base);
-    uint32_t mine = 0, all = 0;
 #pragma unroll
-    for (int i = 0; i < K; ++i) mine += k[i] != 0;
-    block_scan<T>(mine, sh.waves, all);
-    present += all;
-  }
-  const uint32_t keep = min((uint32_t)p.budget, present);
-  uint32_t least = 0, ties = 0;   // chosen: keys above `least`, and the first `ties` that equal it
-  if (keep < present) {
-    uint32_t left = keep;
+  for (int i = 0; i < kBins; ++i) sh.hist[tid + i * T] = 0;
+  if (once && n > 0) load(0);   // (nothing may be read of a sequence without a token)
+  __syncthreads();
+  // Chosen: keys above `least`, and the first `ties` that equal it. What cannot be chosen, key 0, has bin 0 of the
+  // first histogram to itself (the least other key, minus infinity's, is in bin 3).
+  uint32_t least = 0, ties = 0, keep = (uint32_t)p.budget, left = 0;
 #pragma unroll
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-      for (int i = tid; i < 2048; i += T) sh.hist[i] = 0;
-      __syncthreads();
-      for (int32_t base = 0; base < n; base += T * K) {
-        if (!once) load(base);
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
+    for (int32_t base = 0; base < n; base += T * K) {
+      if (!once) load(base);
 #pragma unroll
-        for (int i = 0; i < K; ++i)
-          if (k[i] != 0 && (pass == 0 || k[i] >> (shift + bits) == least >> (shift + bits)))
-            atomicAdd(&sh.hist[k[i] >> shift & ((1u << bits) - 1)], 1u);
-      }
-      __syncthreads();
-      constexpr int kBins = 2048 / T;
-      const int top = (1 << bits) - 1;
-      uint32_t h[kBins], mine = 0, all = 0;
-#pragma unroll
-      for (int i = 0; i < kBins; ++i) {   // from the largest down
-        const int bin = top - (tid * kBins + i);
-        h[i] = bin >= 0 ? sh.hist[bin] : 0;
-        mine += h[i];
-      }
-      uint32_t before = block_scan<T>(mine, sh.waves, all);
-#pragma unroll
-      for (int i = 0; i < kBins; ++i) {
-        if (before < left && left <= before + h[i]) {
-          sh.bin = (uint32_t)(top - (tid * kBins + i));
-          sh.left = left - before;
-        }
-        before += h[i];
-      }
-      __syncthreads();
-      least |= sh.bin << shift;
-      left = sh.left;
-      __syncthreads();
+      for (int i = 0; i < K; ++i)
+        if (pass == 0 || (k[i] ^ least) >> (shift + bits) == 0)
+          atomicAdd(&sh.hist[k[i] >> shift & ((1u << bits) - 1)], 1u);
     }
-    ties = left;
+    __syncthreads();
+    const int top = (1 << bits) - 1;
+    uint32_t h[kBins], mine = 0, all = 0;
+#pragma unroll
+    for (int i = 0; i < kBins; ++i) {   // from the largest down
+      const int bin = top - (tid * kBins + i);
+      h[i] = bin >= 0 && (pass != 0 || bin > 0) ? sh.hist[bin] : 0;
+      mine += h[i];
+    }
+    uint32_t before = block_scan<T>(mine, sh.waves, all);
+    if (pass == 0) {   // all: what can be chosen
+      if (all <= keep) {
+        keep = all;
+        break;
+      }
+      left = keep;
+    }
+#pragma unroll
+    for (int i = 0; i < kBins; ++i) {
+      if (before < left && left <= before + h[i]) {
+        sh.bin = (uint32_t)(top - (tid * kBins + i));
+        sh.left = left - before;
+        sh.held = h[i];
+      }
+      before += h[i];
+      sh.hist[tid + i * T] = 0;   // (block_scan's barriers are behind every read)
+    }
+    __syncthreads();
+    least |= sh.bin << shift;
+    left = sh.left;
+    const bool whole = left == sh.held;
+    __syncthreads();
+    if (whole) {   // all of the bin's
+      least -= 1;   // (no bin is 0: keys above this are those of the bin and more)
+      break;
+    }
+    if (pass == 2) ties = left;
   }
   int32_t* out = p.out + (int64_t)blockIdx.x * p.budget;
   float* out_mass = TOKENS && p.out_mass ? p.out_mass + (int64_t)blockIdx.x * p.budget : nullptr;
@@ -385,12 +419,12 @@ __global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
     if (!once) load(base);
     uint32_t mine = 0, all = 0;
 #pragma unroll
-    for (int i = 0; i < K; ++i) mine += (k[i] > least ? 1u : 0u) + (k[i] == least && least ? 0x10000u : 0u);
+    for (int i = 0; i < K; ++i) mine += (k[i] > least ? 1u : 0u) + (k[i] == least ? 0x10000u : 0u);
     const uint32_t before = block_scan<T>(mine, sh.waves, all);
     uint32_t a = above + (before & 0xffffu), e = equal + (before >> 16);
 #pragma unroll
     for (int i = 0; i < K; ++i) {
-      const bool more = k[i] > least, same = least && k[i] == least;
+      const bool more = k[i] > least, same = k[i] == least;
       if (more || (same && e < ties)) {
         const int32_t item = base + tid * K + i;
         const uint32_t at = a + min(e, ties);

@@ -225,7 +225,7 @@ int ag_index_select(const ag_kv_cache* cache, const ag_page_index* index, const 
   p.group = (int32_t)(q_heads / cache->kv_heads);
   p.keys = (uint32_t*)scratch;
   const int64_t at_once = 64 / (attn_padded(cache->head_dim) / 8);
-  p.splits = splits_of(16 * kCompute, heads, (table_len + at_once - 1) / at_once);
+  p.splits = splits_of(8 * kCompute, heads, (table_len + at_once - 1) / at_once);
   if (p.pages > 0) ATTN_HIP(launch_index_score(p, cache->dtype, batch, (hipStream_t)hip_stream));
   ChooseParams c;
   memset(&c, 0, sizeof(c));
