@@ -314,37 +314,42 @@ __global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
   auto there = [&](int32_t page) { return (uint32_t)page < (uint32_t)p.num_pages; };
   constexpr int kBins = 2048 / T;
 
-  uint32_t k[K];
+  // a thread's keys, and what it writes with the chosen ones: tokens' masses or the pages' numbers
+  uint32_t k[K], with[K];
   auto load = [&](int32_t base) {
+    typedef u32x4 u32x4_four __attribute__((aligned(4)));
     const int32_t i0 = base + tid * K;
-    if constexpr (TOKENS) {
-      typedef f32x4 f32x4_any __attribute__((aligned(4)));
-      f32x4 x[K / 4];
+    const uint32_t* from = TOKENS ? reinterpret_cast<const uint32_t*>(mass) : reinterpret_cast<const uint32_t*>(table);
+    if (i0 + K <= n) {
 #pragma unroll
       for (int i = 0; i < K; i += 4) {
-        x[i / 4] = f32x4{0, 0, 0, 0};
-        if (i0 + i + 4 <= n)
-          x[i / 4] = *reinterpret_cast<const f32x4_any*>(mass + i0 + i);
-        else
+        const u32x4 x = *reinterpret_cast<const u32x4_four*>(from + i0 + i);
 #pragma unroll
-          for (int u = 0; u < 4; ++u)
-            if (i0 + i + u < n) x[i / 4][u] = mass[i0 + i + u];
-      }
-      if (ps >= K) {   // a thread's tokens are in two pages at most
-        const uint32_t j = (uint32_t)min(i0, n - 1) / p.page_size;   // (n > 0)
-        const int32_t left = (int32_t)(j + 1) * ps - i0;   // tokens of the first
-        const bool ok0 = there(table[j]), ok1 = i0 + left < n && there(table[min((int32_t)j + 1, p.pages - 1)]);
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-          k[i] = i0 + i < n && (i < left ? ok0 : ok1) ? order_key(x[i / 4][i % 4]) : 0u;
-      } else {
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-          k[i] = i0 + i < n && there(table[(uint32_t)(i0 + i) / p.page_size]) ? order_key(x[i / 4][i % 4]) : 0u;
+        for (int u = 0; u < 4; ++u) with[i + u] = x[u];
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < K; i += 4) {
+      for (int i = 0; i < K; ++i) with[i] = i0 + i < n ? from[i0 + i] : 0u;
+    }
+    if constexpr (TOKENS) {
+      if (ps >= K) {   // a thread's tokens are in two pages at most
+        const uint32_t j = (uint32_t)min(i0, n - 1) / p.page_size;   // (n > 0)
+        const int32_t left = (int32_t)(j + 1) * ps - i0;   // tokens of the first
+        const int32_t p0 = table[j], p1 = table[min((int32_t)j + 1, p.pages - 1)];
+        const bool ok0 = there(p0), ok1 = there(p1);
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+          k[i] = i0 + i < n && (i < left ? ok0 : ok1) ? order_key(as_f(with[i])) : 0u;
+      } else {
+#pragma unroll
+        for (int i = 0; i < K; ++i) {
+          const int32_t page = table[(uint32_t)min(i0 + i, n - 1) / p.page_size];
+          k[i] = i0 + i < n && there(page) ? order_key(as_f(with[i])) : 0u;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < K; i += 4) {   // (the keys' rows are filled up to fours)
         u32x4 x = {0, 0, 0, 0};
         if (i0 + i < n) x = *reinterpret_cast<const u32x4*>(keys + i0 + i);
 #pragma unroll
@@ -428,8 +433,8 @@ __global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
       if (more || (same && e < ties)) {
         const int32_t item = base + tid * K + i;
         const uint32_t at = a + min(e, ties);
-        out[at] = TOKENS ? item : table[item];
-        if (TOKENS && out_mass) out_mass[at] = mass[item];
+        out[at] = TOKENS ? item : (int32_t)with[i];
+        if (TOKENS && out_mass) out_mass[at] = as_f(with[i]);
       }
       a += more ? 1 : 0;
       e += same ? 1 : 0;
