@@ -207,25 +207,14 @@ __device__ inline void weights_of(const IndexParams& p, int64_t b, int kv, Score
   }
 }
 
-// The scores of a sequence's pages for one kv head, LC lanes to a page.
-template <int DT, int LC>
-__global__ __launch_bounds__(kThreads) void score_kernel(IndexParams p) {
-  constexpr int kPages = 64 / LC, kUnroll = 4;
-  __shared__ ScoreShared<LC> sh;
+// The keys of pages j0, j0 + 1 .. and so on in steps of `step` for one sequence and kv head, LC lanes to a page:
+// put(page, key).
+template <int DT, int LC, class F>
+__device__ inline void score(const IndexParams& p, int64_t b, int kv, ScoreShared<LC>& sh, int32_t j0, int32_t step,
+                             int32_t end, F put) {
+  constexpr int kUnroll = 4;
   const int lane = threadIdx.x & 63, c = lane % LC, r0 = lane / LC;
-  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const uint32_t bh = blockIdx.x / (uint32_t)p.splits, split = blockIdx.x - bh * (uint32_t)p.splits;
-  const int64_t b = bh / (uint32_t)p.c.kv_heads;
-  const int kv = (int)(bh - (uint32_t)b * p.c.kv_heads);
-  const int32_t ps = (int32_t)p.c.page_size.d, hd = p.c.head_dim;
-  const int64_t len = min((int64_t)max(p.lens[b], 0), (int64_t)p.pages * ps);
-  const int32_t end = (int32_t)((len + ps - 1) / ps);
-  const int32_t stride = (p.pages + 3) & ~3;
-  uint32_t* keys = p.keys + (int64_t)bh * stride;
-  const int32_t step = (int32_t)p.splits * 4 * kPages;
-  int32_t j0 = (int32_t)(split * 4 + wave) * kPages;
-  if ((int32_t)split * 4 * kPages >= end) return;   // (nothing for the whole workgroup)
-
+  const int32_t hd = p.c.head_dim;
   uint32_t w0[4], w1[4];
   weights_of<DT, LC>(p, b, kv, sh, w0, w1);
   const bool in = c < hd / 8;
@@ -260,10 +249,32 @@ __global__ __launch_bounds__(kThreads) void score_kernel(IndexParams p) {
       if (c == 0 && j < end) {
         const bool ok = (uint32_t)page[u] < (uint32_t)p.num_pages;
         const uint32_t key = s[u] == 255u ? kMost : order_key((float)total * as_f(s[u] << 23));
-        keys[j] = ok ? key : 0u;
+        put(j, ok ? key : 0u);
       }
     }
   }
+}
+
+// Pages with tokens of sequence b.
+__device__ inline int32_t pages_of(const IndexParams& p, int64_t b) {
+  const int32_t ps = (int32_t)p.c.page_size.d;
+  const int64_t len = min((int64_t)max(p.lens[b], 0), (int64_t)p.pages * ps);
+  return (int32_t)((len + ps - 1) / ps);
+}
+
+template <int DT, int LC>
+__global__ __launch_bounds__(kThreads) void score_kernel(IndexParams p) {
+  constexpr int kPages = 64 / LC;
+  __shared__ ScoreShared<LC> sh;
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const uint32_t bh = blockIdx.x / (uint32_t)p.splits, split = blockIdx.x - bh * (uint32_t)p.splits;
+  const int64_t b = bh / (uint32_t)p.c.kv_heads;
+  const int kv = (int)(bh - (uint32_t)b * p.c.kv_heads);
+  const int32_t end = pages_of(p, b);
+  if ((int32_t)split * 4 * kPages >= end) return;   // (nothing for the whole workgroup)
+  uint32_t* keys = p.keys + (int64_t)bh * ((p.pages + 3) & ~3);
+  score<DT, LC>(p, b, kv, sh, (int32_t)(split * 4 + wave) * kPages, (int32_t)p.splits * 4 * kPages, end,
+                [&](int32_t j, uint32_t key) { keys[j] = key; });
 }
 
 // ---------------------------------------------------------------- choosing
@@ -299,9 +310,9 @@ __device__ inline uint32_t block_scan(uint32_t x, uint32_t* waves, uint32_t& all
 // consecutive items, in registers where the workgroup has all of them at once.
 //
 // One workgroup's time is what counts, and of that the instructions for each item.
+// keys: in global memory or, K = 1, in LDS.
 template <int T, int K, bool TOKENS>
-__global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
-  __shared__ ChooseShared<T> sh;
+__device__ inline void choose_items(const ChooseParams& p, ChooseShared<T>& sh, const uint32_t* keys) {
   const int tid = threadIdx.x;
   const int64_t b = blockIdx.x / (uint32_t)p.heads;
   const int head = (int)(blockIdx.x - (uint32_t)b * p.heads);
@@ -309,7 +320,6 @@ __global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
   const int64_t len = min((int64_t)max(p.lens[b], 0), (int64_t)p.pages * ps);
   const int32_t n = TOKENS ? (int32_t)min(len, (int64_t)p.items) : (int32_t)((len + ps - 1) / ps);
   const int32_t* table = p.table + b * p.table_row;
-  const uint32_t* keys = TOKENS ? nullptr : p.keys + (int64_t)blockIdx.x * p.key_stride;
   const float* mass = TOKENS ? p.mass + b * p.mass_batch + head * p.mass_head : nullptr;
   auto there = [&](int32_t page) { return (uint32_t)page < (uint32_t)p.num_pages; };
   constexpr int kBins = 2048 / T;
@@ -320,9 +330,9 @@ __global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
     typedef u32x4 u32x4_four __attribute__((aligned(4)));
     const int32_t i0 = base + tid * K;
     const uint32_t* from = TOKENS ? reinterpret_cast<const uint32_t*>(mass) : reinterpret_cast<const uint32_t*>(table);
-    if (i0 + K <= n) {
+    if (K > 1 && i0 + K <= n) {
 #pragma unroll
-      for (int i = 0; i < K; i += 4) {
+      for (int i = 0; i < K / 4 * 4; i += 4) {
         const u32x4 x = *reinterpret_cast<const u32x4_four*>(from + i0 + i);
 #pragma unroll
         for (int u = 0; u < 4; ++u) with[i + u] = x[u];
@@ -347,6 +357,8 @@ __global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
           k[i] = i0 + i < n && there(page) ? order_key(as_f(with[i])) : 0u;
         }
       }
+    } else if constexpr (K == 1) {
+      k[0] = i0 < n ? keys[i0] : 0u;
     } else {
 #pragma unroll
       for (int i = 0; i < K; i += 4) {   // (the keys' rows are filled up to fours)
@@ -457,6 +469,30 @@ __global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
   }
 }
 
+template <int T, int K, bool TOKENS>
+__global__ __launch_bounds__(T) void choose_kernel(ChooseParams p) {
+  __shared__ ChooseShared<T> sh;
+  choose_items<T, K, TOKENS>(p, sh, TOKENS ? nullptr : p.keys + (int64_t)blockIdx.x * p.key_stride);
+}
+
+// Scores and choice in one launch, for tables of up to kFew pages: the keys stay in LDS.
+template <int DT, int LC>
+__global__ __launch_bounds__(kThreads) void select_kernel(IndexParams p, ChooseParams c) {
+  constexpr int kPages = 64 / LC;
+  __shared__ union {
+    ScoreShared<LC> score;
+    ChooseShared<kThreads> choose;
+  } sh;
+  __shared__ uint32_t keys[kFew];
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int64_t b = blockIdx.x / (uint32_t)p.c.kv_heads;
+  const int kv = (int)(blockIdx.x - (uint32_t)b * p.c.kv_heads);
+  score<DT, LC>(p, b, kv, sh.score, wave * kPages, 4 * kPages, pages_of(p, b),
+                [&](int32_t j, uint32_t key) { keys[j] = key; });
+  __syncthreads();
+  choose_items<kThreads, 1, false>(c, sh.choose, keys);
+}
+
 // ---------------------------------------------------------------- moving
 
 // A thread moves one 16-byte chunk of a row's keys and of its values; the first ones also the scales.
@@ -509,6 +545,17 @@ void update_by_storage(const IndexParams& p, int storage, int grid, hipStream_t 
 }
 
 template <int DT>
+void select_by_width(const IndexParams& p, const ChooseParams& c, int grid, hipStream_t s) {
+  const int dp = attn_padded(p.c.head_dim);
+  if (dp == 64)
+    select_kernel<DT, 8><<<grid, kThreads, 0, s>>>(p, c);
+  else if (dp == 128)
+    select_kernel<DT, 16><<<grid, kThreads, 0, s>>>(p, c);
+  else
+    select_kernel<DT, 32><<<grid, kThreads, 0, s>>>(p, c);
+}
+
+template <int DT>
 void score_by_width(const IndexParams& p, int grid, hipStream_t s) {
   const int dp = attn_padded(p.c.head_dim);
   if (dp == 64)
@@ -546,6 +593,15 @@ hipError_t launch_index_score(const IndexParams& p, int dtype, int64_t batch, hi
     score_by_width<AGMM_F16>(p, grid, s);
   else
     score_by_width<AGMM_BF16>(p, grid, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_select(const IndexParams& p, const ChooseParams& c, int dtype, int64_t batch, hipStream_t s) {
+  const int grid = (int)(batch * p.c.kv_heads);
+  if (dtype == AGMM_F16)
+    select_by_width<AGMM_F16>(p, c, grid, s);
+  else
+    select_by_width<AGMM_BF16>(p, c, grid, s);
   return hipGetLastError();
 }
 

@@ -195,7 +195,7 @@ int64_t ag_index_scratch_bytes(const ag_kv_cache* cache, int64_t table_len, int6
   if (rc != AGMM_OK) return rc;
   if (table_len < 0 || batch < 0) return AGMM_ERR_INVALID_ARG;
   if (table_len >= kWide || batch > kHeads / cache->kv_heads) return AGMM_ERR_UNSUPPORTED;
-  return batch * cache->kv_heads * key_stride(table_len) * 4;
+  return table_len <= kFew ? 0 : batch * cache->kv_heads * key_stride(table_len) * 4;
 }
 
 int ag_index_select(const ag_kv_cache* cache, const ag_page_index* index, const void* q, int64_t q_batch,
@@ -226,7 +226,6 @@ int ag_index_select(const ag_kv_cache* cache, const ag_page_index* index, const 
   p.keys = (uint32_t*)scratch;
   const int64_t at_once = 64 / (attn_padded(cache->head_dim) / 8);
   p.splits = splits_of(8 * kCompute, heads, (table_len + at_once - 1) / at_once);
-  if (p.pages > 0) ATTN_HIP(launch_index_score(p, cache->dtype, batch, (hipStream_t)hip_stream));
   ChooseParams c;
   memset(&c, 0, sizeof(c));
   c.keys = p.keys;
@@ -243,6 +242,11 @@ int ag_index_select(const ag_kv_cache* cache, const ag_page_index* index, const 
   c.recent = (int32_t)recent;
   c.out = out_table;
   c.out_lens = out_lens;
+  if (table_len <= kFew) {
+    ATTN_HIP(launch_select(p, c, cache->dtype, batch, (hipStream_t)hip_stream));
+    return AGMM_OK;
+  }
+  if (p.pages > 0) ATTN_HIP(launch_index_score(p, cache->dtype, batch, (hipStream_t)hip_stream));
   ATTN_HIP(launch_choose_pages(c, batch, (hipStream_t)hip_stream));
   return AGMM_OK;
 }

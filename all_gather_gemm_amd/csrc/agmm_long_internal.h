@@ -58,6 +58,9 @@ struct ChooseParams {
   float* out_mass;           // or nullptr
   int32_t* out_lens;
 };
+// Tables that one workgroup scores and chooses from in one launch
+constexpr int kFew = 256;
+hipError_t launch_select(const IndexParams& p, const ChooseParams& c, int dtype, int64_t batch, hipStream_t s);
 hipError_t launch_choose_pages(const ChooseParams& p, int64_t batch, hipStream_t s);
 hipError_t launch_choose_tokens(const ChooseParams& p, int64_t batch, hipStream_t s);
 

@@ -55,6 +55,10 @@ _declare()
 
 
 def _table(t, name, rows, device):
+    shape = t.shape
+    if t.dtype is torch.int32 and len(shape) == 2 and shape[0] == rows and t.device == device and \
+            (shape[1] < 2 or t.stride(1) == 1):
+        return t
     return _tensor(t, name, torch.int32, (rows, t.shape[1] if t.dim() == 2 else None), device)
 
 
@@ -171,13 +175,13 @@ class PageIndex:
             n = lib.ag_index_scratch_bytes(cache._ref, pages, batch)
             _checked(min(n, 0), "ag_index_scratch_bytes")
             self._scratch[batch, pages] = n
-        scratch = _empty(q, (n,), torch.uint8, stream)
+        scratch = _empty(q, (n,), torch.uint8, stream) if n else None
         table = _empty(lens, (batch, cache.kv_heads, budget), torch.int32, stream)
         tokens = _like(lens, stream)
         rc = lib.ag_index_select(cache._ref, self._ref, q.data_ptr(), q.stride(0), q.stride(1), q.shape[1],
                                  page_table.data_ptr(), page_table.stride(0), pages, lens.data_ptr(), batch,
-                                 budget, sink, recent, table.data_ptr(), tokens.data_ptr(), scratch.data_ptr(),
-                                 n, where)
+                                 budget, sink, recent, table.data_ptr(), tokens.data_ptr(),
+                                 scratch.data_ptr() if n else None, n, where)
         _checked(rc, "ag_index_select")
         return table, tokens
 
@@ -238,46 +242,60 @@ class Evictor:
     def choose(self, cache: PagedCache, page_table, lens, mass, stream=None):
         """(lens, kept, mass): kept int32 [batch, kv_heads, budget], the tokens that are kept, in order, and -1
         behind them; their masses, float32, and 0 behind them; lens int32 [batch], how many they are."""
-        batch, device = lens.shape[0], cache.device
-        _table(page_table, "page_table", batch, device)
-        _tensor(lens, "lens", torch.int32, (batch,), device)
-        shape = (batch, cache.kv_heads, mass.shape[2] if mass.dim() == 3 else None)
-        _tensor(mass, "mass", torch.float32, shape, device)
-        where = _stream(stream, device.index)
-        kept = _empty(lens, (batch, cache.kv_heads, self.budget), torch.int32, stream)
-        new = _empty(mass, kept.shape, torch.float32, stream)
-        tokens = _like(lens, stream)
-        rc = lib.ag_evict_choose(cache._ref, mass.data_ptr(), mass.stride(0), mass.stride(1), mass.shape[2],
-                                 page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
-                                 lens.data_ptr(), batch, self.budget, self.sink, self.recent,
-                                 kept.data_ptr(), new.data_ptr(), tokens.data_ptr(), where)
-        _checked(rc, "ag_evict_choose")
-        return tokens, kept, new
+        return self._choose(cache, page_table, lens, mass, stream, self._where(cache, page_table, lens, stream))
 
     def move(self, cache: PagedCache, page_table, kept, lens, to_table, to: Optional[PagedCache] = None,
              stream=None):
         """Row j of each sequence and kv head in the pages of to_table int32 [batch, pages] of `to` (the same
         cache if None) becomes the row of token kept[..., j]. No page may be both read and written."""
-        to = cache if to is None else to
-        batch, device = lens.shape[0], cache.device
-        _table(page_table, "page_table", batch, device)
-        _table(to_table, "to_table", batch, device)
-        _tensor(lens, "lens", torch.int32, (batch,), device)
-        _dense(_tensor(kept, "kept", torch.int32, (batch, cache.kv_heads, kept.shape[2] if kept.dim() == 3
-                                                   else None), device), "kept")
-        if to.device != device:
-            raise ValueError("both caches must be on one GPU")
-        if to.desc.k == cache.desc.k and to_table.data_ptr() == page_table.data_ptr() and batch:
-            raise ValueError("rows cannot be moved within the pages that they are read from")
-        rc = lib.ag_evict_move(cache._ref, page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
-                               to._ref, to_table.data_ptr(), to_table.stride(0), to_table.shape[1],
-                               kept.data_ptr(), kept.shape[2], lens.data_ptr(), batch,
-                               _stream(stream, device.index))
-        _checked(rc, "ag_evict_move")
+        to = self._destination(cache, page_table, lens, to_table, to)
+        where = self._where(cache, page_table, lens, stream)
+        _dense(_tensor(kept, "kept", torch.int32, (lens.shape[0], cache.kv_heads, kept.shape[2] if kept.dim() == 3
+                                                   else None), cache.device), "kept")
+        self._move(cache, page_table, kept, lens, to_table, to, where)
 
     def run(self, cache: PagedCache, page_table, lens, mass, to_table, to: Optional[PagedCache] = None,
             stream=None):
         """choose and move in one call: (lens, kept, mass) of the moved sequences."""
-        tokens, kept, new = self.choose(cache, page_table, lens, mass, stream=stream)
-        self.move(cache, page_table, kept, tokens, to_table, to=to, stream=stream)
+        to = self._destination(cache, page_table, lens, to_table, to)
+        where = self._where(cache, page_table, lens, stream)
+        tokens, kept, new = self._choose(cache, page_table, lens, mass, stream, where)
+        self._move(cache, page_table, kept, tokens, to_table, to, where)
         return tokens, kept, new
+
+    @staticmethod
+    def _where(cache, page_table, lens, stream):
+        _table(page_table, "page_table", lens.shape[0], cache.device)
+        _tensor(lens, "lens", torch.int32, (lens.shape[0],), cache.device)
+        return _stream(stream, cache.device.index)
+
+    @staticmethod
+    def _destination(cache, page_table, lens, to_table, to):
+        to = cache if to is None else to
+        _table(to_table, "to_table", lens.shape[0], cache.device)
+        if to.device != cache.device:
+            raise ValueError("both caches must be on one GPU")
+        if to.desc.k == cache.desc.k and to_table.data_ptr() == page_table.data_ptr() and lens.shape[0]:
+            raise ValueError("rows cannot be moved within the pages that they are read from")
+        return to
+
+    def _choose(self, cache, page_table, lens, mass, stream, where):
+        batch = lens.shape[0]
+        shape = (batch, cache.kv_heads, mass.shape[2] if mass.dim() == 3 else None)
+        _tensor(mass, "mass", torch.float32, shape, cache.device)
+        kept = _empty(lens, (batch, cache.kv_heads, self.budget), torch.int32, stream)
+        new = _empty(mass, kept.shape, torch.float32, stream)
+        tokens = _like(lens, stream)
+        ms = mass.stride()
+        rc = lib.ag_evict_choose(cache._ref, mass.data_ptr(), ms[0], ms[1], mass.shape[2], page_table.data_ptr(),
+                                 page_table.stride(0), page_table.shape[1], lens.data_ptr(), batch, self.budget,
+                                 self.sink, self.recent, kept.data_ptr(), new.data_ptr(), tokens.data_ptr(), where)
+        _checked(rc, "ag_evict_choose")
+        return tokens, kept, new
+
+    @staticmethod
+    def _move(cache, page_table, kept, lens, to_table, to, where):
+        rc = lib.ag_evict_move(cache._ref, page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
+                               to._ref, to_table.data_ptr(), to_table.stride(0), to_table.shape[1],
+                               kept.data_ptr(), kept.shape[2], lens.data_ptr(), lens.shape[0], where)
+        _checked(rc, "ag_evict_move")

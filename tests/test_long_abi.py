@@ -119,8 +119,8 @@ def select(L, c=None, x=None, q=64, heads=8, table=64, pages=2, lens=64, batch=1
     (INVALID, dict(sink=4)), (INVALID, dict(recent=5)), (INVALID, dict(sink=1 << 62, recent=1 << 62)),
     (INVALID, dict(heads=3)), (INVALID, dict(heads=0)), (UNSUPPORTED, dict(heads=258)),
     (UNSUPPORTED, dict(budget=1 << 31)), (INVALID, dict(q=63)), (INVALID, dict(table=None)), (INVALID, dict(lens=62)),
-    (INVALID, dict(out=None)), (INVALID, dict(out_lens=66)), (INVALID, dict(scratch=72)), (INVALID, dict(bytes=31)),
-    (INVALID, dict(scratch=None)), (UNSUPPORTED, dict(batch=(1 << 20) + 1)), (UNSUPPORTED, dict(pages=1 << 27)),
+    (INVALID, dict(out=None)), (INVALID, dict(out_lens=66)), (INVALID, dict(scratch=72, pages=300)),
+    (INVALID, dict(bytes=2399, pages=300)), (INVALID, dict(scratch=None, pages=300)), (UNSUPPORTED, dict(batch=(1 << 20) + 1)), (UNSUPPORTED, dict(pages=1 << 27)),
     (0, dict(batch=0, q=None, table=None, lens=None, out=None, out_lens=None, scratch=None)),
 ])
 def test_select_refusals(L, rc, kw):
@@ -129,8 +129,9 @@ def test_select_refusals(L, rc, kw):
 
 def test_index_scratch(L):
     c = ctypes.byref(cache(L))
-    for pages, batch in ((0, 3), (1, 1), (5, 7), (1000, 64)):
-        assert L.lib.ag_index_scratch_bytes(c, pages, batch) == 4 * 2 * batch * (-(-pages // 4) * 4)
+    for pages, batch in ((0, 3), (1, 1), (256, 7), (257, 7), (1001, 64)):   # (up to 256 there is none)
+        assert L.lib.ag_index_scratch_bytes(c, pages, batch) == \
+            (4 * 2 * batch * (-(-pages // 4) * 4) if pages > 256 else 0)
     assert L.lib.ag_index_scratch_bytes(c, -1, 1) == INVALID
     assert L.lib.ag_index_scratch_bytes(c, 1, -1) == INVALID
     assert L.lib.ag_index_scratch_bytes(c, 1 << 31, 1) == UNSUPPORTED
