@@ -98,7 +98,11 @@ def test_types_and_widths(T, L, dtype, storage, dim):
     p = Problem(T, L, EDGES, 6, 2, dim, 16, storage, dtype)
     for b in p.runs:
         check_entries(p.pool, p.index, b)
-    p.check(p.select(9), 9)
+    got = p.select(9)
+    p.check(got, 9)
+    # tables past 256 pages take another way to the same
+    wide = p.index.select(p.q, p.pool.table(p.runs, extra=300), p.lens, 9)
+    assert all(torch.equal(x, y) for x, y in zip(wide, got))
     # what belongs to no sequence is left as it was
     free = p.pool.free
     assert (p.index.codes[free] == 77).all() and (p.index.scales[free] == 77).all()
