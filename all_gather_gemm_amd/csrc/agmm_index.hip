@@ -42,10 +42,22 @@ __device__ inline uint32_t least_exponent(float most) {
 // 2^(127 - s), that is 1 / 2^e, exactly: s is 1..248.
 __device__ inline float one_over(uint32_t s) { return as_f((254u - s) << 23); }
 
-// A wave makes one entry at a time: LC = padded dim / 8 lanes on 8 elements each, 64 / LC rows at once.
+// Pairs of 16-bit floats as pairs of 16-bit whole numbers of the same order, and back. What is past infinity is NaN.
+typedef short s16x2 __attribute__((ext_vector_type(2)));
+__device__ inline s16x2 ordered(uint32_t w) {
+  const s16x2 x = __builtin_bit_cast(s16x2, w);
+  return x ^ ((x >> 15) & (short)0x7fff);
+}
+__device__ inline s16x2 larger(s16x2 a, s16x2 b) { return __builtin_elementwise_max(a, b); }
+__device__ inline s16x2 smaller(s16x2 a, s16x2 b) { return __builtin_elementwise_min(a, b); }
+
+// A wave makes one entry at a time: LC = padded dim / 8 lanes on 8 elements each, 64 / LC rows at once. Largest and
+// least are found among 16-bit whole numbers, two at once; ~x turns the order round, so both are maxima. The rows are
+// put together by exchanges of registers that leave the largest to the lower half of the wave and the least to the
+// upper, and (LC < 32) half of the elements to every other 16 lanes: each lane then has kLeft words of the result.
 template <int DT, int ST, int LC>
 __global__ __launch_bounds__(kThreads) void update_kernel(IndexParams p) {
-  constexpr int kRows = 64 / LC, kUnroll = 4;
+  constexpr int kRows = 64 / LC, kUnroll = 4, kLeft = LC == 32 ? 4 : 2;
   const int lane = threadIdx.x & 63, c = lane % LC, r0 = lane / LC;
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const uint32_t bh = blockIdx.x / (uint32_t)p.splits, split = blockIdx.x - bh * (uint32_t)p.splits;
@@ -60,25 +72,28 @@ __global__ __launch_bounds__(kThreads) void update_kernel(IndexParams p) {
   const int e = in ? 8 * c : 0;
   const int bytes = ST == AG_KV_16BIT ? 2 * e : ST == AG_KV_MXFP8 ? e : e / 2;
   constexpr int kWords = ST == AG_KV_16BIT ? 4 : ST == AG_KV_MXFP8 ? 2 : 1;
-  for (uint32_t j = first + split * 4 + wave; j < end; j += 4 * p.splits) {
-    const int32_t page = p.table[b * p.table_row + j];
-    if ((uint32_t)page >= (uint32_t)p.num_pages) continue;
+  const bool upper = lane >= 32;                                  // has the least
+  const int part = LC == 32 ? 0 : (lane >> 4) & 1;                // and which elements of its 8
+  const int32_t* table = p.table + b * p.table_row;
+  uint32_t j = first + split * 4 + wave;
+  const uint32_t step = 4 * p.splits;
+  int32_t page = j < end ? table[j] : -1;
+  for (; j < end; j += step) {
+    const int32_t now = page;
+    page = j + step < end ? table[j + step] : -1;
+    if ((uint32_t)now >= (uint32_t)p.num_pages) continue;
     const int used = (int)min((int64_t)ps, len - (int64_t)j * ps);
-    float hi[8], lo[8];
-    bool odd = false;
+    s16x2 hi[4], lo[4];   // lo: the largest of ~x
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      hi[k] = -INFINITY;
-      lo[k] = INFINITY;
-    }
+    for (int k = 0; k < 4; ++k) hi[k] = lo[k] = s16x2{-0x8000, -0x8000};
     for (int r = r0; r - r0 < used; r += kUnroll * kRows) {
       uint32_t w[kUnroll][kWords], s[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {   // (past the last row: the last again)
         const uint32_t row = (uint32_t)min(r + u * kRows, used - 1);
-        load_words<kWords>(w[u], p.c.k + kv * p.c.head + row_at(p.c, page, row) + bytes);
+        load_words<kWords>(w[u], p.c.k + kv * p.c.head + row_at(p.c, now, row) + bytes);
         if (ST != AG_KV_16BIT)
-          s[u] = *(const uint8_t*)(p.c.ks + kv * p.c.s_head + scales_at(p.c, page, row) + e / 32);
+          s[u] = *(const uint8_t*)(p.c.ks + kv * p.c.s_head + scales_at(p.c, now, row) + e / 32);
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
@@ -90,41 +105,69 @@ __global__ __launch_bounds__(kThreads) void update_kernel(IndexParams p) {
         else
           x = from_fp4x8<DT>(w[u][0], scale_of(s[u]));
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float f = value_of<DT>(x[k / 2], k % 2);
-          odd = odd || !(fabsf(f) < INFINITY);
-          hi[k] = fmaxf(hi[k], f);
-          lo[k] = fminf(lo[k], f);
+        for (int k = 0; k < 4; ++k) {
+          const s16x2 o = ordered(x[k]);
+          hi[k] = larger(hi[k], o);
+          lo[k] = larger(lo[k], ~o);
         }
       }
     }
-    float most = 0.0f;
+    if constexpr (LC == 8) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-#pragma unroll
-      for (int d = LC; d < 64; d *= 2) {
-        hi[k] = fmaxf(hi[k], __shfl_xor(hi[k], d));
-        lo[k] = fminf(lo[k], __shfl_xor(lo[k], d));
+      for (int k = 0; k < 4; ++k) {   // lanes 8 apart
+        const int x = __builtin_bit_cast(int, hi[k]), y = __builtin_bit_cast(int, lo[k]);
+        hi[k] = larger(hi[k], __builtin_bit_cast(s16x2, __builtin_amdgcn_update_dpp(0, x, 0x128, 0xf, 0xf, true)));
+        lo[k] = larger(lo[k], __builtin_bit_cast(s16x2, __builtin_amdgcn_update_dpp(0, y, 0x128, 0xf, 0xf, true)));
       }
-      most = fmaxf(most, fmaxf(fabsf(hi[k]), fabsf(lo[k])));
+    }
+    s16x2 v[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const auto x = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, hi[k]),
+                                                      __builtin_bit_cast(uint32_t, lo[k]), false, false);
+      v[k] = larger(__builtin_bit_cast(s16x2, (uint32_t)x[0]), __builtin_bit_cast(s16x2, (uint32_t)x[1]));
+    }
+    if constexpr (LC < 32) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const auto x = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v[k]),
+                                                        __builtin_bit_cast(uint32_t, v[k + 2]), false, false);
+        v[k] = larger(__builtin_bit_cast(s16x2, (uint32_t)x[0]), __builtin_bit_cast(s16x2, (uint32_t)x[1]));
+      }
+    }
+    float f[2 * kLeft], most = 0.0f;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < kLeft; ++i) {
+      const uint32_t w = __builtin_bit_cast(uint32_t, ordered(__builtin_bit_cast(uint32_t, upper ? ~v[i] : v[i])));
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float x = value_of<DT>(w, h);
+        odd = odd || !(fabsf(x) < INFINITY);
+        most = fmaxf(most, fabsf(x));
+        f[2 * i + h] = upper ? -x : x;   // (rounded up, either)
+      }
     }
     const bool bad = __ballot(odd && in) != 0;
-    const uint32_t s = bad ? 255u : least_exponent(max_over_lanes<LC>(in ? most : 0.0f));
+    most = max_over_lanes<16>(in ? most : 0.0f);
+    const uint32_t s = bad ? 255u : least_exponent(across_max(most));
     const float unit = bad ? 0.0f : one_over(s);
-    uint32_t up[2] = {0, 0}, down[2] = {0, 0};
+    uint32_t code[kLeft / 2];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      // (a product that underflows is still above 0, or below)
-      int h = max((int)ceilf(hi[k] * unit), hi[k] > 0.0f ? 1 : -128);
-      int l = min((int)floorf(lo[k] * unit), lo[k] < 0.0f ? -1 : 128);
-      if (bad) h = l = 0;
-      up[k / 4] |= (uint32_t)(h & 255) << (8 * (k % 4));
-      down[k / 4] |= (uint32_t)(l & 255) << (8 * (k % 4));
+    for (int i = 0; i < kLeft / 2; ++i) code[i] = 0;
+#pragma unroll
+    for (int k = 0; k < 2 * kLeft; ++k) {
+      // (a product that underflows is still above 0)
+      const int h = bad ? 0 : max((int)ceilf(f[k] * unit), f[k] > 0.0f ? 1 : -128);
+      code[k / 4] |= (uint32_t)((upper ? -h : h) & 255) << (8 * (k % 4));
     }
-    const int64_t entry = (int64_t)page * p.c.kv_heads + kv;
-    if (in && r0 == 0) {
-      *reinterpret_cast<u32x2*>(p.codes + entry * 2 * hd + e) = u32x2{up[0], up[1]};
-      *reinterpret_cast<u32x2*>(p.codes + entry * 2 * hd + hd + e) = u32x2{down[0], down[1]};
+    const int64_t entry = (int64_t)now * p.c.kv_heads + kv;
+    int8_t* to = p.codes + entry * 2 * hd + (upper ? hd : 0) + e + 4 * part;
+    if (in && (LC != 8 || !(lane & 8))) {
+      if constexpr (LC == 32)
+        *reinterpret_cast<u32x2*>(to) = u32x2{code[0], code[kLeft / 2 - 1]};
+      else
+        *reinterpret_cast<uint32_t*>(to) = code[0];
     }
     if (lane == 0) p.scales[entry] = (uint8_t)s;
   }

@@ -185,7 +185,7 @@ int ag_index_update(const ag_kv_cache* cache, const ag_page_index* index, const 
   IndexParams p = index_params(*cache, *index, page_table, table_row, table_len, lens);
   p.starts = starts;
   const int64_t heads = batch * cache->kv_heads;
-  p.splits = splits_of(4 * kCompute, heads, table_len);
+  p.splits = splits_of(8 * kCompute, heads, table_len);
   ATTN_HIP(launch_index_update(p, cache->dtype, cache->storage, batch, (hipStream_t)hip_stream));
   return AGMM_OK;
 }
