@@ -77,8 +77,8 @@ struct PrefixGroup {
   uint32_t tiles;           // of a strip
   uint32_t row_tiles;       // strips of a kv head
   uint32_t strip0, tile0;   // the first strip and tile
-  int32_t up;               // head of the weights
   uint32_t quota;
+  uint32_t reserved;        // (two loads of 16 bytes)
 };
 struct PrefixView {
   PrefixGroup* info;        // [groups]

@@ -120,6 +120,7 @@ int ag_prefix_run(ag_attn_handle* h, const ag_kv_cache* cache, const void* q, in
   int rc = attn_params(h, cache, q, q_batch, q_head, page_table, table_row, table_len, lens, batch, out,
                        o_batch, o_head, lse, &a, &grid);
   if (rc != AGMM_OK || grid == 0) return rc;
+  if (a.cap == 0.0f && a.scale > 0x1p64f) return AGMM_ERR_UNSUPPORTED;
   Scratch s;
   rc = scratch_of(d, batch, groups, &s);
   if (rc != AGMM_OK) return rc;

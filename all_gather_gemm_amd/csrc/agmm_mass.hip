@@ -48,7 +48,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void mass_kernel(MassP
   if (base >= n) return;
 
   W w;
-  float lse[4];
+  float lse[4], rest[4];   // in base 2, and what its rounding leaves
   auto heads = [&](int group) {
     const int head0 = kv * p.group + 16 * group, count = min(16, p.group - 16 * group);
     w.start(p, b, head0, count);
@@ -56,7 +56,9 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void mass_kernel(MassP
     for (int j = 0; j < 4; ++j) {
       const int h = 4 * g + j;
       const float x = h < count ? m.lse[(int64_t)b * p.q_heads + head0 + h] : -INFINITY;
-      lse[j] = x == -INFINITY ? INFINITY : x * 1.44269504088896340736f;
+      const float log2e = 1.44269504088896340736f;
+      lse[j] = x == -INFINITY ? INFINITY : x * log2e;
+      rest[j] = fabsf(lse[j]) < INFINITY ? fmaf(x, log2e, -lse[j]) + x * 1.92596299e-8f : 0.0f;
     }
   };
   // Puts the places of a tile's tokens into LDS; bit t: token base + t is attended to. Loads of tiles without
@@ -97,7 +99,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void mass_kernel(MassP
             s = capped<false>(p, s);
             scale = 1.0f;
           }
-          sum[t] += __builtin_amdgcn_exp2f(fmaf(s, scale, -lse[j]));
+          sum[t] += __builtin_amdgcn_exp2f(fmaf(s, scale, -lse[j]) - rest[j]);
         }
     };
     f32x4 st[R::kSub];

@@ -34,7 +34,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(PrefixParams p, FastDiv 
   }
   const u32x4 g0 = *reinterpret_cast<const u32x4*>(&x.info[lo]);
   const u32x4 g1 = *(reinterpret_cast<const u32x4*>(&x.info[lo]) + 1);
-  const PrefixGroup g = {(int32_t)g0[0], (int32_t)g0[1], g0[2], g0[3], g1[0], g1[1], (int32_t)g1[2], g1[3]};
+  const PrefixGroup g = {(int32_t)g0[0], (int32_t)g0[1], g0[2], g0[3], g1[0], g1[1], g1[2], 0};
   const uint32_t r = (b - g.first) * a.group + (head - kv * a.group);
   const uint32_t strip = kv * g.row_tiles + r / kPrefixRows, row = r % kPrefixRows;
   const uint32_t start = g.tile0 + strip * g.tiles, begin = start / g.quota;
@@ -79,11 +79,10 @@ __global__ __launch_bounds__(kThreads) void join_kernel(PrefixParams p, FastDiv 
     own_l = 0.0f;
   }
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-  const float sum = shares ? ldexpf(l, -g.up) : 0.0f;
   // (the prefix's reference is in base 2, the other in unit()s of it)
   const float u = unit(a), top = fmaxf(own_m * u, m);
   const float ours = own_m == -INFINITY ? own_l : own_l * __builtin_amdgcn_exp2f(fmaf(own_m, u, -top));
-  const float theirs = sum * weight(m, top, 1.0f);
+  const float theirs = l * weight(m, top, 1.0f);
   const float all = ours + theirs;
   const float fo = all == 0.0f ? 0.0f : ours / all, fp = all == 0.0f ? 0.0f : theirs / all;
   float y[4];

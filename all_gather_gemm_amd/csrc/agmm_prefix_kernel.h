@@ -155,7 +155,7 @@ struct PrefixWave {
 
   u32x4 q[kSteps];
   f32x16 acc[kParts];
-  float m, l;  // of this lane's row: reference of the weights, a whole number, base 2; l of this lane's tokens
+  float m, l;  // of this lane's row: weights are 2^(score - m), base 2; their sum over this lane's tokens
   uint32_t k_at[kKeys], v_at[kValues];  // LDS bytes of this lane's operands
 
   __device__ inline void start(const AttnParams& p, int32_t first, int kv, int row, int rows) {
@@ -321,11 +321,15 @@ struct PrefixWave {
                                                       __builtin_bit_cast(uint32_t, top), false, false);
       top = fmaxf(__builtin_bit_cast(float, (uint32_t)x[0]), __builtin_bit_cast(float, (uint32_t)x[1]));
     }
-    // Weights are 2^(score - m + head) with a whole number m: scaling by one multiply-add is then exact up to the
-    // exponent's own rounding however large the scores are, and what is summed is rescaled by powers of 2.
+    // Weights are 2^(score - m) with a whole number m, `up` below the largest score so far (or less: it is raised
+    // only when that is left behind by 2^kRaise). One multiply-add then gives an exponent that is off by its own
+    // rounding alone, however large the scores are, and what is summed is rescaled by powers of 2. Past 2^23 not
+    // every whole number is a 32-bit float: there m is the score itself. (One past the range of floats gives NaN.)
     top *= scale;
-    if (__any(top - m > (float)kRaise)) {
-      const float raised = fmaxf(m, ceilf(top));
+    const float head = (float)up;
+    if (__any(top - m > (float)kRaise + head)) {
+      const float whole = fminf(ceilf(top), 0x1.fffffep127f);
+      const float raised = fmaxf(m, fabsf(whole) < 0x1p23f ? whole - head : whole);
       const float f = weight(m, raised, 1.0f);
 #pragma unroll
       for (int i = 0; i < kParts; ++i)
@@ -334,7 +338,7 @@ struct PrefixWave {
       l *= f;
       m = raised;
     }
-    const float less = (float)up - (m == -INFINITY ? 0.0f : m);
+    const float less = m == -INFINITY ? 0.0f : -m;
     // 16 tokens at a time; the weights of the next ones are made between the products of these.
     constexpr int kTimes = 2 * T::kSub, kVector = 56 / (2 * kParts);
     u32x4 hi[2], lo[2], value[2][kParts];
@@ -588,7 +592,7 @@ __global__ __launch_bounds__(kThreads, prefix_per_cu(DP)) void prefix_kernel(Pre
       const PrefixScan r = g == 0 ? scan0[lane] : scan_groups<DP>(p, g, c);
       if (g + lane < a.prefix.groups)
         a.prefix.info[g + lane] =
-            PrefixGroup{r.first, r.end, r.tiles, r.row_tiles, r.strip0, r.tile0, head_of<DT>(r.len), quota};
+            PrefixGroup{r.first, r.end, r.tiles, r.row_tiles, r.strip0, r.tile0, quota, 0};
     }
   }
   // Consecutive numbers to the workgroups of an XCD, which are 8 apart, so that strips of one kv head find its

@@ -34,7 +34,8 @@ extern "C" {
 /* Device bytes of a run's scratch, or a negative code. Host only. */
 int64_t ag_prefix_scratch_bytes(const ag_attn_desc* desc, int64_t batch, int64_t groups);
 
-/* One run of a handle of ag_attn_create whose desc has no window.
+/* One run of a handle of ag_attn_create whose desc has no window, and a cap or a scale of 2^63 at most (else
+ * UNSUPPORTED). Scores of 2^127 and more, without a cap, count as infinite.
  *   prefix_table: device int32 [groups], entry (g, j) at g * prefix_row + j, j < prefix_pages;
  *   prefix_lens:  device int32 [groups]; < 0 counts as 0, tokens past the table are left out;
  *   starts:       device int32 [groups + 1], or NULL with one group: all of the batch. Numbers outside [0,

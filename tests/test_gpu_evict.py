@@ -72,8 +72,9 @@ class Masses:
                 with np.errstate(invalid="ignore", over="ignore"):
                     p = np.where(seen[:, None], np.exp(s - x), 0.0)
                 want = self.decay * old[b, h, :n] + p.sum(1)
-                err = np.where(seen[:, None], p * (2 * (q.shape[2] + 8) * 2.0 ** -24 * w +
-                                                   2.0 ** -22 * (np.abs(s) + np.abs(x)) + 2.0 ** -20), 0.0).sum(1)
+                with np.errstate(invalid="ignore"):
+                    err = np.where(seen[:, None], p * (2 * (q.shape[2] + 8) * 2.0 ** -24 * w +
+                                                       2.0 ** -22 * (np.abs(s) + np.abs(x)) + 2.0 ** -20), 0.0).sum(1)
                 tol = err + (group + 2) * 2.0 ** -24 * np.abs(want)
                 assert (np.abs(got[b, h, :n] - want) <= tol).all(), (b, h)
 

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+import attention_reference as ref
 import long_reference as lr
 
 pytestmark = pytest.mark.gpu
@@ -185,6 +186,34 @@ def test_large_values_stay_finite(T, L):
     assert (out.float() <= top).all() and (out.float() >= top * (1 - 2.0 ** -7)).all()
 
 
+@pytest.mark.parametrize("power", [10, 20, 22, 23, 24])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_large_scores(T, L, power, dtype):
+    """Scores of 2^power and a little, growing from tile to tile, so that the maximum is raised again and again.
+
+    Products are exact: one large element that all keys share and one small one, whose product is a multiple of half
+    `step` and so of 2^(power - 23), the last bit of a 32-bit float at 2^power. So scores differ by what the small
+    elements say, off by 2^-24 of it for the scale's rounding, and the exponent's own rounding is 2^-19 at 2^5 and less:
+    a weight is within 2^-17 of itself. out: half an ulp, and A * (2^-16 + 2^-11 [f16: parts] or 2^-15)."""
+    n, dim, step = 640, 64, 2.0 ** max(0, power - 22)
+    k = torch.zeros((n + 40, 1, dim))
+    k[..., 0] = 2.0 ** (power - 10)
+    k[:, 0, 1] = step * (torch.arange(n + 40) // 20 + 2.0 * (torch.arange(n + 40) % 3))
+    p = Problem(T, L, [(n, [30, 10])], 4, 1, dim, 16, "16bit", dtype, k=k, scale=1.0)
+    p.q.zero_()
+    p.q[..., 0] = 2.0 ** 10
+    p.q[..., 1] = 0.5
+    out, lse = p.run()
+    q, out, lse = (x.double().cpu().numpy() for x in (p.q, out, lse))
+    part = 2.0 ** -11 if dtype == "f16" else 2.0 ** -15
+    for b in range(2):
+        kk, vv = p.tokens(b)
+        o, s, a, _ = ref.attention(q[b], kk, vv, 1.0)
+        assert (np.abs(out[b] - o) <= ref.HALF_ULP[dtype] * np.abs(o) + a * (2.0 ** -16 + part)).all(), b
+        # lse: 2^-24 for each of three roundings at its magnitude, and the scale's
+        assert (np.abs(lse[b] - s) <= 2.0 ** -21 * (1 + np.abs(s))).all()
+
+
 def test_repeats_are_equal(T, L):
     p = Problem(T, L, [(3000, [100] * 9), (500, [9, 8])], 16, 2, 128, 16, "mxfp8", "bf16")
     a = p.run()
@@ -231,6 +260,31 @@ def test_strided_out(T, L):
     out, lse = p.run(out=wide[:, 1:7])
     p.check(out, lse)
     assert (wide[:, 0] == 7).all() and (wide[:, 7] == 7).all()
+
+
+def test_scales_past_the_range(T, L):
+    """Scores would leave the range of 32-bit floats: refused, unless they are capped."""
+    for cap in (0.0, 5.0):
+        p = Problem(T, L, [(40, [4, 0])], 4, 1, 64, 16, "16bit", "bf16", scale=2.0 ** 64, cap=cap)
+        if cap:
+            p.run()
+        else:
+            with pytest.raises(T.AgmmError) as e:
+                p.run()
+            assert e.value.code == -2
+
+
+def test_infinite_scores(T, L):
+    """A score past the range of floats, as an infinite one, gives NaN for its sequences and no others."""
+    p = Problem(T, L, [(100, [6, 7]), (100, [5])], 4, 1, 64, 16, "16bit", "bf16")
+    page, row = p.pool.pages[0][2], 5
+    for k in (math.inf, 3.0e38):
+        p.pool.cache.k[page, 0, row] = k
+        p.q.fill_(3.0e38 if k < math.inf else 1.0)
+        out, lse = p.run()
+        assert torch.isnan(out[:2]).all()
+        if k == math.inf:
+            assert torch.isfinite(out[2]).all() and torch.isfinite(lse[2]).all()
 
 
 def test_nothing(T, L):
