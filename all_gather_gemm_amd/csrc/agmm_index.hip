@@ -2,6 +2,11 @@
 //
 // All of them read a stream of bytes and compute little on each, so many pages or tokens are bound by memory
 // bandwidth and few by the chain of a launch, the length, the page and its rows.
+//
+// Measured, warm: entries of a prompt of 16384 tokens (8 kv heads of 128, bf16, pages of 16) 7.6 us, 4.7 TB/s; scores of
+// 32 sequences of up to 32768 tokens, 8 kv heads: 14 us, of one of 131072 tokens, one kv head, pages of 64: 5.0; choosing
+// from 2048 pages 6.5 us, from 16384 tokens (one workgroup each, 256 of them) 26; moving 4096 rows of 32 sequences and 8
+// kv heads 217 us, 4.9 TB/s of reads and writes (a copy of 4 GiB runs at 4.7; four rows to a thread: 220).
 #include "agmm_attn_kernel.h"
 #include "agmm_long_internal.h"
 
