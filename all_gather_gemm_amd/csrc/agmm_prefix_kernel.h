@@ -12,8 +12,8 @@
 //    P^T's operands for O^T, in the order of tokens {16 s + 4 h ..+3, 16 s + 8 + 4 h ..+3} for lane half h, so
 //    P never moves between lanes. V^T's operands in that order are two transposing reads of LDS each.
 //  - Weights enter the product in two parts of the 16-bit type, as in the attention of single tokens, so that
-//    a shared prefix gives what its tokens give unshared. One rounded part alone would take 390 us for 455 (256
-//    sequences behind 32768 tokens), and where values average out be off by 1.4 times as much.
+//    a shared prefix gives what its tokens give unshared. One rounded part alone: 390 us against 472 (256 sequences
+//    behind 32768 tokens, one run), and where values average out 1.4 times as far off, bf16's own rounding counted in.
 //  - 16-bit rows of whole padded width go from memory to LDS directly; others, and codes, through registers, where
 //    they become values of the 16-bit type, so all storages share the rest.
 //  - The next tile is under way to the other half of LDS while one is worked on: one barrier a tile.
@@ -26,7 +26,7 @@
 // own tokens (agmm_attn_kernel.h) and leave theirs. A second kernel joins them all, in the order of the pieces, so
 // results do not depend on timing.
 //
-// Measured, warm, with the joining: 256 sequences behind 32768 tokens, 64/8 heads of 128, bf16: 455 us; the prefix by
+// Measured, with the joining: 256 sequences behind 32768 tokens, 64/8 heads of 128, bf16: 447 us; the prefix by
 // itself 393: 0.70 PFLOP/s counted once, 1.05 with both parts of the weights (the card's large products run at 1.2, at
 // its power limit; the clock is 1.9 GHz here). The matrix units are busy half of the cycles, the vector units 60%.
 // 64 sequences behind 8192 tokens: 51 us, of which launch, lengths and pages take 10, the pieces' 33 MB 8, the joining
