@@ -74,7 +74,7 @@ struct Tile {
 };
 
 template <int DP>
-struct TileShared {
+struct alignas(16) TileShared {
   char k[2][Tile<DP>::kBytes], v[2][Tile<DP>::kBytes];
   int64_t at[4][Tile<DP>::kTokens][2];  // the tokens' places: data and scale offsets, for each wave
 };
