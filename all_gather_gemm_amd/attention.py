@@ -295,7 +295,7 @@ class PagedCache:
             c.scale_page, c.scale_head, c.scale_row = k_scale.stride()[:3]
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.desc, self._ref = c, ctypes.byref(c)
-        self.storage, self.device = storage, k.device
+        self.storage, self.device, self.index = storage, k.device, k.device.index
         self.kv_heads, self.head_dim, self.page_size = c.kv_heads, c.head_dim, c.page_size
 
     @staticmethod

@@ -54,12 +54,21 @@ def _declare():
 _declare()
 
 
-def _table(t, name, rows, device):
-    shape = t.shape
-    if t.dtype is torch.int32 and len(shape) == 2 and shape[0] == rows and t.device == device and \
-            (shape[1] < 2 or t.stride(1) == 1):
+# Arguments' checks are most of a small call's time: what is right is seen with few attributes, and whatever is not goes
+# to attention._tensor, which says why.
+def _is(t, name, dtype, shape, cache):
+    """A tensor of this type and shape on the cache's GPU whose last dimension is dense."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == cache.index and t.stride(-1) == 1:
         return t
-    return _tensor(t, name, torch.int32, (rows, t.shape[1] if t.dim() == 2 else None), device)
+    return _tensor(t, name, dtype, shape, cache.device)
+
+
+def _table(t, name, rows, cache):
+    shape = t.shape
+    if t.dtype is torch.int32 and len(shape) == 2 and shape[0] == rows and t.get_device() == cache.index and \
+            t.stride(1) == 1:
+        return t
+    return _tensor(t, name, torch.int32, (rows, shape[1] if len(shape) == 2 else None), cache.device)
 
 
 def _dense(t, name):
@@ -88,27 +97,29 @@ class PrefixAttention(DecodeAttention):
         if n is None:
             n = lib.ag_prefix_scratch_bytes(ctypes.byref(self.desc), batch, groups)
             _checked(min(n, 0), "ag_prefix_scratch_bytes")
+            if len(self._scratch) >= 4096:
+                self._scratch.clear()
             self._scratch[batch, groups] = n
         return n
 
     def run(self, q, cache: PagedCache, prefix_table, prefix_lens, page_table, lens, starts=None, out=None,
             return_lse: bool = False, stream=None):
-        batch, device = q.shape[0], cache.device
-        _tensor(q, "q", self.torch_dtype, (batch, self.q_heads, self.head_dim), device)
+        batch = q.shape[0]
+        _is(q, "q", self.torch_dtype, (batch, self.q_heads, self.head_dim), cache)
         groups = prefix_lens.shape[0]
-        _tensor(prefix_lens, "prefix_lens", torch.int32, (groups,), device)
-        _table(prefix_table, "prefix_table", groups, device)
-        _table(page_table, "page_table", batch, device)
-        _tensor(lens, "lens", torch.int32, (batch,), device)
+        _is(prefix_lens, "prefix_lens", torch.int32, (groups,), cache)
+        _table(prefix_table, "prefix_table", groups, cache)
+        _table(page_table, "page_table", batch, cache)
+        _is(lens, "lens", torch.int32, (batch,), cache)
         if starts is not None:
-            _tensor(starts, "starts", torch.int32, (groups + 1,), device)
+            _is(starts, "starts", torch.int32, (groups + 1,), cache)
         elif groups != 1:
             raise ValueError("several groups need starts")
-        where = _stream(stream, device.index)
+        where = _stream(stream, cache.index)
         if out is None:
             out = _like(q, stream)
         else:
-            _tensor(out, "out", self.torch_dtype, q.shape, device)
+            _is(out, "out", self.torch_dtype, q.shape, cache)
         lse = _empty(q, (batch, self.q_heads), torch.float32, stream) if return_lse else None
         n = self._scratch_bytes(batch, groups)
         scratch = _empty(q, (n,), torch.uint8, stream)
@@ -147,14 +158,14 @@ class PageIndex:
     def update(self, page_table, lens, starts=None, stream=None):
         """Makes the entries of the pages that hold tokens starts[b] (0 without starts) to lens[b] - 1 of
         the sequences of page_table int32 [batch, pages]; starts and lens int32 [batch]."""
-        batch, device = lens.shape[0], self.cache.device
-        _table(page_table, "page_table", batch, device)
-        _tensor(lens, "lens", torch.int32, (batch,), device)
+        cache, batch = self.cache, lens.shape[0]
+        _table(page_table, "page_table", batch, cache)
+        _is(lens, "lens", torch.int32, (batch,), cache)
         if starts is not None:
-            _tensor(starts, "starts", torch.int32, (batch,), device)
-        rc = lib.ag_index_update(self.cache._ref, self._ref, page_table.data_ptr(), page_table.stride(0),
+            _is(starts, "starts", torch.int32, (batch,), cache)
+        rc = lib.ag_index_update(cache._ref, self._ref, page_table.data_ptr(), page_table.stride(0),
                                  page_table.shape[1], None if starts is None else starts.data_ptr(),
-                                 lens.data_ptr(), batch, _stream(stream, device.index))
+                                 lens.data_ptr(), batch, _stream(stream, cache.index))
         _checked(rc, "ag_index_update")
 
     def select(self, q, page_table, lens, budget: int, sink: int = 1, recent: int = 2, stream=None):
@@ -162,18 +173,20 @@ class PageIndex:
         q_heads, head_dim] attend to (the sequence's first `sink`, its last `recent`, and those with the
         highest scores), in order, and -1 behind them; tokens int32 [batch], how many they hold.
         DecodeAttention.run takes both as its page table and lengths."""
-        cache, batch, device = self.cache, q.shape[0], self.cache.device
-        _tensor(q, "q", cache.torch_dtype, (batch, q.shape[1] if q.dim() == 3 else None, cache.head_dim), device)
-        _table(page_table, "page_table", batch, device)
-        _tensor(lens, "lens", torch.int32, (batch,), device)
+        cache, batch = self.cache, q.shape[0]
+        _is(q, "q", cache.torch_dtype, (batch, q.shape[1] if q.dim() == 3 else None, cache.head_dim), cache)
+        _table(page_table, "page_table", batch, cache)
+        _is(lens, "lens", torch.int32, (batch,), cache)
         if budget < 1:
             raise ValueError("budget must be at least 1")
-        where = _stream(stream, device.index)
+        where = _stream(stream, cache.index)
         pages = page_table.shape[1]
         n = self._scratch.get((batch, pages))
         if n is None:
             n = lib.ag_index_scratch_bytes(cache._ref, pages, batch)
             _checked(min(n, 0), "ag_index_scratch_bytes")
+            if len(self._scratch) >= 4096:
+                self._scratch.clear()
             self._scratch[batch, pages] = n
         scratch = _empty(q, (n,), torch.uint8, stream) if n else None
         table = _empty(lens, (batch, cache.kv_heads, budget), torch.int32, stream)
@@ -209,18 +222,18 @@ class AttentionMass:
 
     def add(self, mass, q, lse, cache: PagedCache, page_table, lens, decay: float = 1.0, out=None,
             stream=None):
-        batch, device = q.shape[0], cache.device
-        _tensor(q, "q", self.torch_dtype, (batch, self.q_heads, self.head_dim), device)
+        batch = q.shape[0]
+        _is(q, "q", self.torch_dtype, (batch, self.q_heads, self.head_dim), cache)
         shape = (batch, self.kv_heads, mass.shape[2] if mass.dim() == 3 else None)
-        _tensor(mass, "mass", torch.float32, shape, device)
-        _dense(_tensor(lse, "lse", torch.float32, (batch, self.q_heads), device), "lse")
-        _table(page_table, "page_table", batch, device)
-        _tensor(lens, "lens", torch.int32, (batch,), device)
-        where = _stream(stream, device.index)
+        _is(mass, "mass", torch.float32, shape, cache)
+        _dense(_is(lse, "lse", torch.float32, (batch, self.q_heads), cache), "lse")
+        _table(page_table, "page_table", batch, cache)
+        _is(lens, "lens", torch.int32, (batch,), cache)
+        where = _stream(stream, cache.index)
         if out is None:
             out = _empty(mass, mass.shape, torch.float32, stream)
         else:
-            _tensor(out, "out", torch.float32, mass.shape, device)
+            _is(out, "out", torch.float32, mass.shape, cache)
         ms, os, qs = mass.stride(), out.stride(), q.stride()
         rc = lib.ag_mass_add(self._ref, cache._ref, q.data_ptr(), qs[0], qs[1], lse.data_ptr(),
                              page_table.data_ptr(), page_table.stride(0), page_table.shape[1],
@@ -265,14 +278,14 @@ class Evictor:
 
     @staticmethod
     def _where(cache, page_table, lens, stream):
-        _table(page_table, "page_table", lens.shape[0], cache.device)
-        _tensor(lens, "lens", torch.int32, (lens.shape[0],), cache.device)
-        return _stream(stream, cache.device.index)
+        _table(page_table, "page_table", lens.shape[0], cache)
+        _is(lens, "lens", torch.int32, (lens.shape[0],), cache)
+        return _stream(stream, cache.index)
 
     @staticmethod
     def _destination(cache, page_table, lens, to_table, to):
         to = cache if to is None else to
-        _table(to_table, "to_table", lens.shape[0], cache.device)
+        _table(to_table, "to_table", lens.shape[0], cache)
         if to.device != cache.device:
             raise ValueError("both caches must be on one GPU")
         if to.desc.k == cache.desc.k and to_table.data_ptr() == page_table.data_ptr() and lens.shape[0]:
@@ -282,7 +295,7 @@ class Evictor:
     def _choose(self, cache, page_table, lens, mass, stream, where):
         batch = lens.shape[0]
         shape = (batch, cache.kv_heads, mass.shape[2] if mass.dim() == 3 else None)
-        _tensor(mass, "mass", torch.float32, shape, cache.device)
+        _is(mass, "mass", torch.float32, shape, cache)
         kept = _empty(lens, (batch, cache.kv_heads, self.budget), torch.int32, stream)
         new = _empty(mass, kept.shape, torch.float32, stream)
         tokens = _like(lens, stream)

@@ -27,6 +27,9 @@ class F(Fake):
     def new_empty(self, shape, dtype=None):
         return F(shape, dtype or self.dtype, self.device)
 
+    def get_device(self):
+        return self.device.index
+
     def numel(self):
         return self.shape.numel()
 
