@@ -13,6 +13,7 @@ namespace {
 
 constexpr int kCompute = 256;  // compute units
 constexpr int64_t kWide = (int64_t)1 << 31;
+constexpr int64_t kReach = kWide - (1 << 20);  // of a table: loops go past their ends, in 32 bits
 constexpr int64_t kHeads = 1 << 21;  // sequences times kv heads: each has a workgroup of up to 1024 threads
 
 // ---- prefixes ----
@@ -52,7 +53,7 @@ int check_tables(const ag_kv_cache& c, const int32_t* table, int64_t table_len, 
   if (batch < 0 || table_len < 0) return AGMM_ERR_INVALID_ARG;
   if (batch == 0) return AGMM_OK;
   if (!aligned(lens, 4) || (table_len > 0 && !aligned(table, 4))) return AGMM_ERR_INVALID_ARG;
-  if (batch >= kWide || table_len >= kWide || table_len * c.page_size >= kWide ||
+  if (batch >= kWide || table_len >= kWide || table_len * c.page_size >= kReach ||
       batch > kHeads / c.kv_heads)
     return AGMM_ERR_UNSUPPORTED;
   return AGMM_OK;
@@ -131,7 +132,7 @@ int ag_prefix_run(ag_attn_handle* h, const ag_kv_cache* cache, const void* q, in
   if (!aligned(prefix_lens, 4) || (prefix_pages > 0 && !aligned(prefix_table, 4)) ||
       (starts ? !aligned(starts, 4) : groups != 1) || !aligned(scratch, 256) || scratch_bytes < s.bytes)
     return AGMM_ERR_INVALID_ARG;
-  if (prefix_pages >= kWide || prefix_pages * cache->page_size >= kWide) return AGMM_ERR_UNSUPPORTED;
+  if (prefix_pages >= kWide || prefix_pages * cache->page_size >= kReach) return AGMM_ERR_UNSUPPORTED;
   PrefixParams p;
   memset(&p, 0, sizeof(p));
   a.prefix.info = (PrefixGroup*)scratch;

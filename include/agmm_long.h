@@ -11,7 +11,8 @@
  *
  * Types, strides, devices, codes and threading are those of agmm_attn.h. No call here waits for the device;
  * all of them may be captured into a HIP graph and replayed. At most 2^21 sequences times kv heads, but for
- * ag_prefix_run and ag_attn_run_heads, whose limits are ag_attn_run's. Page numbers and lengths are read on
+ * ag_prefix_run and ag_attn_run_heads, whose limits are ag_attn_run's, and less than 2^31 - 2^20 tokens in a table's
+ * pages, but for the own tables of those two. Page numbers and lengths are read on
  * the device and checked there: nothing is read or written at a page outside [0, num_pages).
  */
 #ifndef AGMM_LONG_H

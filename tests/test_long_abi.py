@@ -197,6 +197,13 @@ def test_move_refusals(L, rc, kw):
     assert move(L, **kw) == rc
 
 
+def test_tables_near_31_bits(L):
+    """Pages of 16: tables of 2^31 - 2^20 tokens and more are refused, before anything is launched."""
+    for pages in ((1 << 27) - (1 << 16), (1 << 27) - 1):
+        assert select(L, pages=pages) == add(L, pages=pages) == choose(L, pages=pages) == UNSUPPORTED
+        assert move(L, pages=pages) == move(L, to_pages=pages) == UNSUPPORTED
+
+
 def test_move_between_unlike_caches(L):
     for kw in (dict(dtype=0), dict(storage=1), dict(head_dim=64), dict(kv_heads=1)):
         assert move(L, to=cache(L, **kw)) == INVALID
