@@ -1,0 +1,165 @@
+"""The operators for long contexts at the ends of what the documentation allows: pages past 2^32 bytes, several
+captured graphs and streams, one page in many places."""
+import math
+
+import pytest
+import torch
+
+import attention_reference as ref
+import long_reference as lr
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def T():
+    import all_gather_gemm_amd.attention
+    return all_gather_gemm_amd.attention
+
+
+@pytest.fixture(scope="module")
+def L():
+    import all_gather_gemm_amd.long_context
+    return all_gather_gemm_amd.long_context
+
+
+class Far:
+    """The same sequences in a small cache and in one whose pages are past 2^32 bytes from each other."""
+
+    def __init__(self, T, storage="16bit"):
+        self.lens = [300, 40, 200]
+        self.page, self.heads, self.dim = 16, 2, 128
+        near = lr.Pool(T, self.lens, self.heads, self.dim, self.page, storage, "bf16", spare=16)
+        pages = near.cache.k.shape[0]
+        row = near.cache.k.shape[3]
+        size = near.cache.k.element_size()
+        # every page 2^28 bytes and a bit behind the one before: the last past 2^32
+        step = ((1 << 28) + 4096) // size
+        shape, strides = (pages, self.heads, self.page, row), (step, self.page * row, row, 1)
+        kind = near.cache.k.dtype
+        far = [torch.as_strided(torch.empty(pages * step, dtype=kind, device=lr.DEV), shape, strides) for _ in "kv"]
+        far[0].copy_(near.cache.k)
+        far[1].copy_(near.cache.v)
+        self.caches = near.cache, T.PagedCache(*far, near.cache.k_scale, near.cache.v_scale, storage=storage)
+        assert (pages - 1) * step * size > 1 << 32
+        self.table, self.n = near.table(range(3)), near.lengths(range(3))
+        self.free, self.q = near.free, near.q(3, 8)
+
+
+@pytest.mark.parametrize("storage", ["16bit", "mxfp8"])
+def test_pages_past_32_bits(T, L, storage):
+    f = Far(T, storage)
+    prefix, plain = (c(8, 2, 128, storage=storage) for c in (L.PrefixAttention, T.DecodeAttention))
+    adder, evictor = L.AttentionMass(8, 2, 128, storage=storage), L.Evictor(64, sink=4, recent=16)
+    to_table = torch.tensor(f.free[:12], dtype=torch.int32, device=lr.DEV).view(3, 4)
+    slots = (to_table.long()[:, :, None] * 16 + torch.arange(16, device=lr.DEV)).flatten()
+    got = []
+    for cache in f.caches:
+        r = list(prefix.run(f.q, cache, f.table[:1], f.n[:1], f.table, f.n, return_lse=True))
+        index = L.PageIndex(cache)
+        index.update(f.table, f.n)
+        r += list(index.select(f.q, f.table, f.n, 6))
+        r += list(plain.run(f.q, cache, r[2], r[3], return_lse=True))
+        mass = adder.add(torch.zeros((3, 2, 320), device=lr.DEV), f.q, plain.run(f.q, cache, f.table, f.n,
+                                                                                return_lse=True)[1], cache, f.table, f.n)
+        r += [mass] + list(evictor.run(cache, f.table, f.n, mass, to_table))
+        r += list(cache.read(slots[:64])) + list(cache.read(slots[128:168]))
+        got.append(r + [index.codes[f.table[0, :19].long()], index.scales[f.table[0, :19].long()]])
+    for x, y in zip(*got):
+        assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+
+
+def test_graphs_of_one_handle(T, L):
+    """Two captured graphs and eager calls of one handle, in turns."""
+    pool = lr.Pool(T, [500, 300, 40, 70, 3], 2, 64, 16, "16bit", "bf16")
+    attn = L.PrefixAttention(8, 2, 64)
+    calls = []
+    for runs, batch in ((range(2, 4), 2), (range(2, 5), 3)):
+        q = pool.q(batch, 8, seed=batch)
+        a = (q, pool.cache, pool.table([batch - 2]), pool.lengths([batch - 2]), pool.table(runs), pool.lengths(runs))
+        calls.append(lambda a=a: attn.run(*a, return_lse=True))
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(c())
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1):
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs[i], want[i]))
+        got = calls[1 - i]()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want[1 - i]))
+
+
+def test_two_handles_at_once(T, L):
+    """Two handles on two streams, each with its own scratch, at the same time."""
+    pool = lr.Pool(T, [3000, 300, 400, 700, 3], 2, 128, 16, "16bit", "bf16")
+    q = pool.q(3, 16)
+    args = (q, pool.cache, pool.table([0]), pool.lengths([0]), pool.table(range(2, 5)), pool.lengths(range(2, 5)))
+    handles = [L.PrefixAttention(16, 2, 128) for _ in "ab"]
+    want = handles[0].run(*args, return_lse=True)
+    streams = [torch.cuda.Stream() for _ in "ab"]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[h.run(*args, return_lse=True, stream=s) for h, s in zip(handles, streams)] for _ in range(20)]
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    for pair in got:
+        for r in pair:
+            assert all(torch.equal(x, y) for x, y in zip(r, want))
+
+
+def test_one_page_in_many_places(T, L):
+    """A prefix that is also a sequence's own tokens, and a page twice in one table."""
+    pool = lr.Pool(T, [48, 20], 1, 64, 16, "16bit", "bf16")
+    q = pool.q(2, 4)
+    twice = pool.table([0], extra=0)[:, [0, 1, 1, 2]].contiguous()
+    own = twice.expand(2, -1).contiguous()
+    n = torch.tensor([64, 33], dtype=torch.int32, device=lr.DEV)
+    attn = L.PrefixAttention(4, 1, 64)
+    out, lse = attn.run(q, pool.cache, twice, n[:1], own, n, return_lse=True)
+    k, v = pool.k[0], pool.v[0]
+    order = list(range(32)) + list(range(16, 48))
+    keys = [k[order + order], k[order + order[:33]]]
+    values = [v[order + order], v[order + order[:33]]]
+    lr.check_attention("bf16", q, out, lse, keys, values, 1 / math.sqrt(64))
+    index = L.PageIndex(pool.cache)
+    index.update(own, n)
+    table, tokens = index.select(q, own, n, 8)
+    assert tokens.tolist() == [64, 33]
+    assert table[0, 0].tolist()[:4] == own[0].tolist() and table[1, 0].tolist()[:3] == own[1].tolist()[:3]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_shared_and_unshared_agree(T, L, dtype):
+    """A prefix of whole pages, shared, against the same pages in front of each sequence's own table: both within
+    half an ulp and the sums' roundings of the same value."""
+    pool = lr.Pool(T, [640, 100, 7, 333], 2, 128, 16, "16bit", dtype)
+    q = pool.q(3, 8)
+    own = pool.table(range(1, 4))
+    got, lse = L.PrefixAttention(8, 2, 128, dtype=dtype).run(
+        q, pool.cache, pool.table([0]), pool.lengths([0]), own, pool.lengths(range(1, 4)), return_lse=True)
+    whole = torch.cat((pool.table([0], extra=0).expand(3, -1), own), 1).contiguous()
+    want, lse2 = T.DecodeAttention(8, 2, 128, dtype=dtype).run(q, pool.cache, whole, pool.lengths(range(1, 4)) + 640,
+                                                              return_lse=True)
+    k = [torch.cat((torch.from_numpy(pool.k[0]), torch.from_numpy(pool.k[b]))).numpy() for b in (1, 2, 3)]
+    v = [torch.cat((torch.from_numpy(pool.v[0]), torch.from_numpy(pool.v[b]))).numpy() for b in (1, 2, 3)]
+    lr.check_attention(dtype, q, got, lse, k, v, 1 / math.sqrt(128))
+    lr.check_attention(dtype, q, want, lse2, k, v, 1 / math.sqrt(128))
+    assert (lse - lse2).abs().max() < 2.0 ** -18
+    assert (ref.f64(got) != ref.f64(want)).mean() < 0.25
+
+
+def test_prefix_table_near_31_bits(T, L):
+    """Tables of prefixes with 2^31 - 2^20 tokens and more are refused on the host."""
+    pool = lr.Pool(T, [40, 3], 1, 64, 64, "16bit", "bf16")
+    q, n = pool.q(1, 1), pool.lengths([0])
+    long = torch.full((1, (1 << 25) - (1 << 14)), -1, dtype=torch.int32, device=lr.DEV)
+    attn = L.PrefixAttention(1, 1, 64)
+    with pytest.raises(RuntimeError):
+        attn.run(q, pool.cache, long, n, pool.table([1]), pool.lengths([1]))
+    attn.run(q, pool.cache, pool.table([0]), n, pool.table([1]), pool.lengths([1]))
