@@ -4,7 +4,7 @@
 // bandwidth and few by the chain of a launch, the length, the page and its rows.
 //
 // Measured, warm: entries of a prompt of 16384 tokens (8 kv heads of 128, bf16, pages of 16) 7.6 us, 4.7 TB/s; scores of
-// 32 sequences of up to 32768 tokens, 8 kv heads: 14 us, of one of 131072 tokens, one kv head, pages of 64: 5.0; choosing
+// 32 sequences of up to 32768 tokens, 8 kv heads: 12.3 us, of one of 131072 tokens, one kv head, pages of 64: 4.4; choosing
 // from 2048 pages 6.5 us, from 16384 tokens (one workgroup each, 256 of them) 26; moving 4096 rows of 32 sequences and 8
 // kv heads 217 us, 4.9 TB/s of reads and writes (a copy of 4 GiB runs at 4.7; four rows to a thread: 220).
 #include "agmm_attn_kernel.h"
@@ -190,17 +190,18 @@ __device__ inline uint32_t order_key(float x) {
 }
 
 template <int LC>
-struct ScoreShared {
-  int sum[2][8 * LC];   // of the elements' positive codes, and of the negative ones
+struct alignas(16) ScoreShared {
+  uint8_t code[2][16 * LC];   // the sums' low and high parts
+  int sum[16 * LC];           // of the elements' positive codes, and of the negative ones
   float most[kThreads / 64];
 };
 
 // What a page's codes are multiplied by, for one sequence and kv head: the sums over the q heads of the positive
-// codes of each element, and of the negative ones. The workgroup makes them together, a thread some heads of one
-// element; a lane gets its 16 in two parts of 8 bits, 128 x + y, for v_dot4_i32_i8 (they are within 127 * 128).
+// codes of each element, and of the negative ones, in two parts of 8 bits, 128 x + y, for v_dot4_i32_i8 (they are
+// within 127 * 128). The workgroup makes them together, a thread some heads of one element; a lane gets its 16.
 template <int DT, int LC>
 __device__ inline void weights_of(const IndexParams& p, int64_t b, int kv, ScoreShared<LC>& sh,
-                                  uint32_t (&w0)[4], uint32_t (&w1)[4]) {
+                                  u32x4& w0, u32x4& w1) {
   constexpr int kDim = 8 * LC, kPer = kThreads / kDim, kIn = 4;
   const int tid = threadIdx.x, e = tid % kDim, part = tid / kDim, hd = p.c.head_dim;
   const uint16_t* q = p.q + b * p.q_batch + (int64_t)kv * p.group * p.q_head + (e < hd ? e : 0);
@@ -221,7 +222,7 @@ __device__ inline void weights_of(const IndexParams& p, int64_t b, int kv, Score
   }
   most = max_over_lanes<32>(most);
   most = fmaxf(most, __shfl_xor(most, 32));
-  if (tid < kDim) sh.sum[0][e] = sh.sum[1][e] = 0;
+  for (int i = tid; i < 16 * LC; i += kThreads) sh.sum[i] = 0;
   if ((tid & 63) == 0) sh.most[tid >> 6] = most;
   __syncthreads();
 #pragma unroll
@@ -238,21 +239,19 @@ __device__ inline void weights_of(const IndexParams& p, int64_t b, int kv, Score
     }
   }
   if (e < hd) {
-    atomicAdd(&sh.sum[0][e], up);
-    atomicAdd(&sh.sum[1][e], down);
+    atomicAdd(&sh.sum[e], up);
+    atomicAdd(&sh.sum[hd + e], down);
   }
   __syncthreads();
-  const int c = (tid & 63) % LC;   // chunk: 16 of the 2 * hd codes, two blocks of 8
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w0[i] = w1[i] = 0;
-  if (c >= hd / 8) return;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int at = 16 * c + i;
-    const int s = at < hd ? sh.sum[0][at] : sh.sum[1][at - hd], hi = s / 128, lo = s - 128 * hi;
-    w1[i / 4] |= (uint32_t)(hi & 255) << (8 * (i % 4));
-    w0[i / 4] |= (uint32_t)(lo & 255) << (8 * (i % 4));
+  for (int i = tid; i < 16 * LC; i += kThreads) {   // (0 past 2 * hd)
+    const int s = sh.sum[i], hi = s / 128;
+    sh.code[0][i] = (uint8_t)(s - 128 * hi);
+    sh.code[1][i] = (uint8_t)hi;
   }
+  __syncthreads();
+  const int c = (tid & 63) % LC;   // chunk: 16 of the 2 * hd codes
+  w0 = *reinterpret_cast<const u32x4*>(sh.code[0] + 16 * c);
+  w1 = *reinterpret_cast<const u32x4*>(sh.code[1] + 16 * c);
 }
 
 // The keys of pages j0, j0 + 1 .. and so on in steps of `step` for one sequence and kv head, LC lanes to a page:
@@ -263,7 +262,7 @@ __device__ inline void score(const IndexParams& p, int64_t b, int kv, ScoreShare
   constexpr int kUnroll = 4;
   const int lane = threadIdx.x & 63, c = lane % LC, r0 = lane / LC;
   const int32_t hd = p.c.head_dim;
-  uint32_t w0[4], w1[4];
+  u32x4 w0, w1;
   weights_of<DT, LC>(p, b, kv, sh, w0, w1);
   const bool in = c < hd / 8;
   const int32_t* table = p.table + b * p.table_row;

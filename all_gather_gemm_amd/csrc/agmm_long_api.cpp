@@ -227,6 +227,7 @@ int ag_index_select(const ag_kv_cache* cache, const ag_page_index* index, const 
   p.group = (int32_t)(q_heads / cache->kv_heads);
   p.keys = (uint32_t*)scratch;
   const int64_t at_once = 64 / (attn_padded(cache->head_dim) / 8);
+  // (32 sequences of up to 32768 tokens, 8 kv heads: 17.4 us with 4 a compute unit, 12.3 with 8, 13.6 with 16)
   p.splits = splits_of(8 * kCompute, heads, (table_len + at_once - 1) / at_once);
   ChooseParams c;
   memset(&c, 0, sizeof(c));
