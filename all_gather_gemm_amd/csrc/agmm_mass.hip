@@ -10,7 +10,7 @@
 // other, so each wave goes through its own; the next tile's keys are loaded as soon as the products have used
 // the last one's.
 //
-// Measured, warm: 32 sequences of 16384 tokens, 64/8 heads of 128, bf16: 203 us, 5.5 TB/s; one of 4096, 8/1 heads: 6.3 us
+// Measured, warm: 32 sequences of 16384 tokens, 64/8 heads of 128, bf16: 205 us, 5.5 TB/s; one of 4096, 8/1 heads: 6.3 us
 // (launch, length, page, keys, each waiting for the one before).
 #include "agmm_attn_kernel.h"
 #include "agmm_long_internal.h"
@@ -39,7 +39,6 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void mass_kernel(MassP
   const Range seq = range_of(p, len);            // tokens that are attended to
   const float* from = m.mass + b * m.mass_batch + kv * m.mass_head;
   float* to = m.out + b * m.out_batch + kv * m.out_head;
-  const int32_t n = m.out == m.mass ? held : m.tokens;
   const int32_t* table = p.table + (int64_t)b * p.table_row;
   const int64_t hoff = kv * p.c.head, shoff = kv * p.c.s_head;
   int64_t(*at)[2] = sh.at[wave];
@@ -48,7 +47,6 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void mass_kernel(MassP
   constexpr int kTile = R::kTokens;
   const int64_t step = (int64_t)m.splits * 4 * kTile;
   int64_t base = ((int64_t)split * 4 + wave) * kTile;
-  if (base >= n) return;
 
   W w;
   float lse[4], rest[4];   // in base 2, and what its rounding leaves
@@ -80,60 +78,74 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void mass_kernel(MassP
     __builtin_amdgcn_wave_barrier();
     return (uint64_t)__ballot(ok);
   };
-  heads(0);
-  R r;
-  uint64_t there = place(base);
-  if (there) W::load_k(r, p, at, hoff, shoff);
-  while (true) {
-    const int64_t tok = base + lane;
-    const bool mine = lane < kTile && tok < n;
-    const float old = mine ? from[tok] : 0.0f;
-    float sum[R::kSub];
+  heads(0);   // (in front of what waits for the length)
+  if (base < held) {
+    R r;
+    uint64_t there = place(base);
+    if (there) W::load_k(r, p, at, hoff, shoff);
+    while (true) {
+      const int64_t tok = base + lane;
+      const bool mine = lane < kTile && tok < held;
+      const float old = mine ? from[tok] : 0.0f;
+      float sum[R::kSub];
 #pragma unroll
-    for (int t = 0; t < R::kSub; ++t) sum[t] = 0.0f;
-    const uint64_t now = there;
-    auto add = [&](const f32x4 (&st)[R::kSub]) {
+      for (int t = 0; t < R::kSub; ++t) sum[t] = 0.0f;
+      const uint64_t now = there;
+      auto add = [&](const f32x4 (&st)[R::kSub]) {
 #pragma unroll
-      for (int t = 0; t < R::kSub; ++t)
+        for (int t = 0; t < R::kSub; ++t)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float s = st[t][j], scale = p.scale;
-          if constexpr (CAP) {
-            s = capped<false>(p, s);
-            scale = 1.0f;
+          for (int j = 0; j < 4; ++j) {
+            float s = st[t][j], scale = p.scale;
+            if constexpr (CAP) {
+              s = capped<false>(p, s);
+              scale = 1.0f;
+            }
+            sum[t] += __builtin_amdgcn_exp2f(fmaf(s, scale, -lse[j]) - rest[j]);
           }
-          sum[t] += __builtin_amdgcn_exp2f(fmaf(s, scale, -lse[j]) - rest[j]);
-        }
-    };
-    f32x4 st[R::kSub];
-    for (int group = 1; group < p.q_groups; ++group) {   // (more than 16 heads: the last groups first)
-      if (now == 0) break;
-      heads(group);
-      w.template scores<true>(r, p, sc, st);
-      add(st);
-    }
-    if (now != 0) {
-      if (p.q_groups > 1) heads(0);
-      w.template scores<true>(r, p, sc, st);
-    }
-    base += step;
-    there = 0;
-    if (base < n) {
-      there = place(base);
-      if (there) W::load_k(r, p, at, hoff, shoff);
-    }
-    float x = 0.0f;
-    if (now != 0) {
-      add(st);
-#pragma unroll
-      for (int t = 0; t < R::kSub; ++t) {
-        const float s = across_sum(sum[t]);
-        x = g == t ? s : x;
+      };
+      f32x4 st[R::kSub];
+      for (int group = 1; group < p.q_groups; ++group) {   // (more than 16 heads: the last groups first)
+        if (now == 0) break;
+        heads(group);
+        w.template scores<true>(r, p, sc, st);
+        add(st);
       }
-      x = now >> lane & 1 ? x : 0.0f;
+      if (now != 0) {
+        if (p.q_groups > 1) heads(0);
+        w.template scores<true>(r, p, sc, st);
+      }
+      base += step;
+      there = 0;
+      if (base < held) {
+        there = place(base);
+        if (there) W::load_k(r, p, at, hoff, shoff);
+      }
+      float x = 0.0f;
+      if (now != 0) {
+        add(st);
+#pragma unroll
+        for (int t = 0; t < R::kSub; ++t) {
+          const float s = across_sum(sum[t]);
+          x = g == t ? s : x;
+        }
+        x = now >> lane & 1 ? x : 0.0f;
+      }
+      if (mine) to[tok] = fmaf(m.decay, old, x);
+      if (base >= held) break;
     }
-    if (mine) to[tok] = tok < held ? fmaf(m.decay, old, x) : old;
-    if (base >= n) break;
+  }
+
+  // The entries behind the sequence, all threads over the row and 4 each, those without tiles first. (32 sequences of up
+  // to 16384 tokens, 62516 in all, in rows of 16384, 64/8 heads: 49 us, 63 with tiles of these as of the others.)
+  if (m.out == m.mass) return;
+  typedef f32x4 f32x4_any __attribute__((aligned(4)));
+  const int64_t each = (int64_t)4 * kThreads * m.splits;
+  for (int64_t t = held + each - 4 - 4 * (int64_t)(split * kThreads + threadIdx.x); t < m.tokens; t += each) {
+    if (t + 4 <= m.tokens)
+      *reinterpret_cast<f32x4_any*>(to + t) = *reinterpret_cast<const f32x4_any*>(from + t);
+    else
+      for (int64_t i = t; i < m.tokens; ++i) to[i] = from[i];
   }
 }
 

@@ -163,3 +163,28 @@ def test_prefix_table_near_31_bits(T, L):
     with pytest.raises(RuntimeError):
         attn.run(q, pool.cache, long, n, pool.table([1]), pool.lengths([1]))
     attn.run(q, pool.cache, pool.table([0]), n, pool.table([1]), pool.lengths([1]))
+
+
+@pytest.mark.parametrize("tokens", [1, 7, 130, 1027, 5003])
+def test_masses_behind_the_sequences(T, L, tokens):
+    """Rows of odd strides: entries from the length on are copied bit for bit, NaN too, and nothing else is written."""
+    pool = lr.Pool(T, [40, 3, 600, 0], 2, 64, 16, "16bit", "bf16")
+    q, table, n = pool.q(4, 8), pool.table(range(4)), pool.lengths(range(4))
+    lse = T.DecodeAttention(8, 2, 64).run(q, pool.cache, table, n, return_lse=True)[1]
+    old = torch.rand((4, 2, tokens + 6), device=lr.DEV)
+    old[:, :, 3::5] = math.nan
+    kept, into = old.clone(), torch.full((4, 2, tokens + 8), 7.0, device=lr.DEV)
+    adder = L.AttentionMass(8, 2, 64)
+    adder.add(old[:, :, 1:tokens + 1], q, lse, pool.cache, table, n, decay=0.5, out=into[:, :, 3:tokens + 3])
+    placed = kept[:, :, 1:tokens + 1]
+    adder.add(placed, q, lse, pool.cache, table, n, decay=0.5, out=placed)
+    bits = lambda x: x.contiguous().view(torch.int32)  # noqa: E731
+    got = into[:, :, 3:tokens + 3]
+    assert torch.equal(bits(got), bits(placed))
+    assert (into[:, :, :3] == 7.0).all() and (into[:, :, tokens + 3:] == 7.0).all()
+    for b in range(4):
+        m = min(int(n[b]), tokens)
+        assert torch.equal(bits(got[b, :, m:]), bits(old[b, :, m + 1:tokens + 1]))
+        assert (got[b, :, :m].isnan() == old[b, :, 1:m + 1].isnan()).all()
+    assert torch.equal(bits(kept[:, :, :1]), bits(old[:, :, :1])) and \
+        torch.equal(bits(kept[:, :, tokens + 1:]), bits(old[:, :, tokens + 1:]))
