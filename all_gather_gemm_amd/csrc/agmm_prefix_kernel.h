@@ -26,9 +26,10 @@
 // own tokens (agmm_attn_kernel.h) and leave theirs. A second kernel joins them all, in the order of the pieces, so
 // results do not depend on timing.
 //
-// Measured, with the joining: 256 sequences behind 32768 tokens, 64/8 heads of 128, bf16: 435 us (467 on another card); the prefix by
-// itself 393: 0.70 PFLOP/s counted once, 1.05 with both parts of the weights (the card's large products run at 1.2, at
-// its power limit; the clock is 1.9 GHz here). The matrix units are busy half of the cycles, the vector units 60%.
+// Measured, with the joining: 256 sequences behind 32768 tokens, 64/8 heads of 128, bf16: 435 us (467 on another
+// card); the prefix by itself 393: 0.70 PFLOP/s counted once, 1.05 with both parts of the weights (the card's large
+// products run at 1.2, at its power limit; the clock is 1.9 GHz here). The matrix units are busy half of the cycles,
+// the vector units 60%.
 // 64 sequences behind 8192 tokens: 51 us, of which launch, lengths and pages take 10, the pieces' 33 MB 8, the joining
 // 9; a call of 4 behind 2000 tokens 14 + the host.
 #pragma once
