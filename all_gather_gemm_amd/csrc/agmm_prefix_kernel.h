@@ -82,9 +82,10 @@ struct alignas(16) TileShared {
 
 // 16 bytes a lane from `from` into LDS at byte m0 + 16 * lane (m0 is wave-uniform). Written as inline asm so that
 // the compiler adds no waits for it: it cannot tell which half of LDS is written, and would wait before every
-// read of the other.
+// read of the other. (The load needs one wait state behind the write of m0, which the compiler does not keep in front
+// of inline asm.)
 __device__ inline void dma16(const char* from, uint32_t m0) {
-  asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(from), "{m0}"(m0) : "memory");
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "{m0}"(m0) : "memory");
 }
 __device__ inline void dma_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
