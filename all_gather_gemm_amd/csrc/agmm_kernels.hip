@@ -176,9 +176,10 @@ typedef __attribute__((address_space(3))) u32x2 lds_u32x2;
 // wave-uniform): buffer_load_dwordx4 ... lds, with the LDS base in M0. Written as inline
 // asm so that the compiler adds no waits of its own for it (it cannot tell which stage a
 // DMA in flight targets across the K loop's back edge and would drain every request); the
-// K loop waits for exactly the requests it needs with wait_vmcnt.
+// K loop waits for exactly the requests it needs with wait_vmcnt. (The load needs one wait state
+// behind the write of m0, which the compiler does not keep in front of inline asm.)
 __device__ inline void dma16(rsrc_t rs, uint32_t m0, uint32_t voff) {
-  asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rs), "{m0}"(m0)
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(voff), "s"(rs), "{m0}"(m0)
                : "memory");
 }
 

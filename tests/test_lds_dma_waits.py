@@ -77,7 +77,7 @@ def test_what_counts(code, found):
     assert len(without_wait(code)) == found
 
 
-@pytest.mark.parametrize("kernel", ["prefix_kernel<"])
+@pytest.mark.parametrize("kernel", ["prefix_kernel<", "agmm_persistent<", ""])
 def test_m0(kernels, kernel):
     mine = {n: c for n, c in kernels.items() if kernel in n}
     assert any(is_lds_load(x) for c in mine.values() for x in c)
