@@ -599,8 +599,16 @@ __device__ __attribute__((always_inline)) void gemm_tile(const KParams& p, int t
     else
       bd.issue(d - T::ADMA, r.rb, stage_off + T::A_CH * 16, wave_u, 0);
   };
+  // Resources that requests follow at once: the vector unit's write of a scalar register has to be 5 wait states
+  // old where a memory instruction reads it, and the compiler does not keep those in front of inline asm. (In the
+  // K loop there are products in between.)
+  auto settled = [&](int t) -> Req {
+    Req r = resources(t);
+    asm volatile("s_nop 4" : "+s"(r.ra), "+s"(r.rb));
+    return r;
+  };
   auto request = [&](int t, uint32_t stage_off) {
-    const Req r = resources(t);
+    const Req r = settled(t);
 #pragma unroll
     for (int d = 0; d < T::DMA_PER_TILE; ++d) issue(d, r, stage_off);
   };
@@ -688,7 +696,7 @@ __device__ __attribute__((always_inline)) void gemm_tile(const KParams& p, int t
       if (j < KT) request(j, st.off(j));
     });
     if (KT > NS - 1) {
-      const Req r = resources(NS - 1);
+      const Req r = settled(NS - 1);
 #pragma unroll
       for (int d = 0; d < T::ADMA; ++d) issue(d, r, st.off(NS - 1));
     }

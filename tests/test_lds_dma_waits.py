@@ -1,7 +1,8 @@
 """Wait states in front of the loads from memory to LDS, in the built gfx950 code (CPU: the code is only listed).
 
-Such a load takes its LDS address from m0 and needs one wait state behind the write of m0. The compiler keeps
-that where it makes the load itself; where the load is inline asm, as here, it does not look."""
+Such a load takes its LDS address from m0 and needs one wait state behind the write of m0, and 5 behind a vector
+instruction's write of a scalar register that it reads. The compiler keeps those where it makes the load itself; where
+the load is inline asm, as here, it does not look."""
 import os
 import re
 import shutil
@@ -66,6 +67,30 @@ def without_wait(code):
             if is_lds_load(b) and re.match(r"[sv]_\w+ m0\b", a)]
 
 
+def scalars(text):
+    out = {int(n) for n in re.findall(r"\bs(\d+)\b", text)}
+    for a, b in re.findall(r"\bs\[(\d+):(\d+)\]", text):
+        out |= set(range(int(a), int(b) + 1))
+    return out
+
+
+def too_young(code):
+    """Loads to LDS that read a scalar register less than 5 wait states behind a vector instruction's write of it."""
+    out = []
+    for i, x in enumerate(code):
+        if not is_lds_load(x):
+            continue
+        waits = 0
+        for y in reversed(code[max(0, i - 5):i]):
+            if waits >= 5:
+                break
+            if y.startswith("v_") and scalars(y.partition(" ")[2].split(",")[0]) & scalars(x):
+                out.append(f"{y} | {x}")
+                break
+            waits += int(y.split()[1]) + 1 if y.startswith("s_nop") else 1
+    return out
+
+
 @pytest.mark.parametrize("code, found", [
     (["s_mov_b32 m0, s9", "global_load_lds_dwordx4 v[4:5], off"], 1),
     (["s_add_i32 m0, s9, 0x8000", "s_nop 0", "global_load_lds_dwordx4 v[4:5], off"], 0),
@@ -82,3 +107,18 @@ def test_m0(kernels, kernel):
     mine = {n: c for n, c in kernels.items() if kernel in n}
     assert any(is_lds_load(x) for c in mine.values() for x in c)
     assert {n: w[:2] for n, w in ((n, without_wait(c)) for n, c in mine.items()) if w} == {}
+
+
+@pytest.mark.parametrize("code, found", [
+    (["v_readfirstlane_b32 s36, v20", "s_nop 0", "buffer_load_dwordx4 v26, s[36:39], 0 offen lds"], 1),
+    (["v_readlane_b32 s39, v20, 3", "s_nop 3", "buffer_load_dwordx4 v26, s[36:39], 0 offen lds"], 1),
+    (["v_readfirstlane_b32 s36, v20", "s_nop 4", "buffer_load_dwordx4 v26, s[36:39], 0 offen lds"], 0),
+    (["v_readfirstlane_b32 s40, v20", "s_nop 0", "buffer_load_dwordx4 v26, s[36:39], 0 offen lds"], 0),
+    (["v_add_u32_e32 v1, s36, v20", "s_nop 0", "buffer_load_dwordx4 v26, s[36:39], 0 offen lds"], 0),
+])
+def test_what_is_too_young(code, found):
+    assert len(too_young(code)) == found
+
+
+def test_scalars(kernels):
+    assert {n: w[:2] for n, w in ((n, too_young(c)) for n, c in kernels.items()) if w} == {}
