@@ -81,10 +81,10 @@ IndexParams index_params(const ag_kv_cache& c, const ag_page_index& x, const int
   return p;
 }
 
-// Workgroups for each sequence and head: `wgs` in all, as long as each has an item for its waves.
-int splits_of(int64_t wgs, int64_t heads, int64_t items) {
+// Workgroups for each of `n` sequences, or their heads: `wgs` in all, as long as each has an item for its waves.
+int splits_of(int64_t wgs, int64_t n, int64_t items) {
   const int64_t most = std::max<int64_t>(1, (items + 3) / 4);
-  int64_t n = std::min(std::max<int64_t>(1, wgs / std::max<int64_t>(1, heads)), most);
+  n = std::min(std::max<int64_t>(1, wgs / std::max<int64_t>(1, n)), most);
   return (int)n;
 }
 
@@ -186,8 +186,9 @@ int ag_index_update(const ag_kv_cache* cache, const ag_page_index* index, const 
   if (batch == 0 || table_len == 0 || cache->num_pages == 0) return AGMM_OK;
   IndexParams p = index_params(*cache, *index, page_table, table_row, table_len, lens);
   p.starts = starts;
-  const int64_t heads = batch * cache->kv_heads;
-  p.splits = splits_of(8 * kCompute, heads, table_len);
+  p.batch = fast_div((uint32_t)batch);
+  p.step = fast_div((uint32_t)(4 * splits_of(8 * kCompute, batch, table_len * cache->kv_heads)));
+  p.heads = fast_div((uint32_t)cache->kv_heads);
   ATTN_HIP(launch_index_update(p, cache->dtype, cache->storage, batch, (hipStream_t)hip_stream));
   return AGMM_OK;
 }

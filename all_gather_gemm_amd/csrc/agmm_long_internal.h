@@ -31,8 +31,10 @@ struct IndexParams {
   const int32_t* lens;
   int64_t table_row;
   int32_t num_pages, pages;  // of the cache; of a sequence's table
-  int32_t splits;            // workgroups of one sequence and head
+  // update
+  FastDiv batch, step, heads;  // step: entries of a sequence at once, 4 a workgroup; heads: kv heads
   // select
+  int32_t splits;            // workgroups of one sequence and head
   const uint16_t* q;
   int64_t q_batch, q_head;
   int32_t group;

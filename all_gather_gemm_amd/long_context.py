@@ -157,7 +157,8 @@ class PageIndex:
 
     def update(self, page_table, lens, starts=None, stream=None):
         """Makes the entries of the pages that hold tokens starts[b] (0 without starts) to lens[b] - 1 of
-        the sequences of page_table int32 [batch, pages]; starts and lens int32 [batch]."""
+        the sequences of page_table int32 [batch, pages]; starts and lens int32 [batch]. A page in several of
+        those places gets the entry of the one with the most of its tokens."""
         cache, batch = self.cache, lens.shape[0]
         _table(page_table, "page_table", batch, cache)
         _is(lens, "lens", torch.int32, (batch,), cache)
