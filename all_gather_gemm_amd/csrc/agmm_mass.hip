@@ -50,6 +50,7 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void mass_kernel(MassP
 
   W w;
   float lse[4], rest[4];   // in base 2, and what its rounding leaves
+  bool none[4];            // adds nothing, whatever its score: 0 * infinity in a row without a head is NaN
   auto heads = [&](int group) {
     const int head0 = kv * p.group + 16 * group, count = min(16, p.group - 16 * group);
     w.start(p, b, head0, count);
@@ -58,7 +59,8 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void mass_kernel(MassP
       const int h = 4 * g + j;
       const float x = h < count ? m.lse[(int64_t)b * p.q_heads + head0 + h] : -INFINITY;
       const float log2e = 1.44269504088896340736f;
-      lse[j] = x == -INFINITY ? INFINITY : x * log2e;
+      none[j] = x == -INFINITY;
+      lse[j] = none[j] ? 0.0f : x * log2e;
       rest[j] = fabsf(lse[j]) < INFINITY ? fmaf(x, log2e, -lse[j]) + x * 1.92596299e-8f : 0.0f;
     }
   };
@@ -101,7 +103,8 @@ __global__ __launch_bounds__(kThreads, DP == 256 ? 2 : 4) void mass_kernel(MassP
               s = capped<false>(p, s);
               scale = 1.0f;
             }
-            sum[t] += __builtin_amdgcn_exp2f(fmaf(s, scale, -lse[j]) - rest[j]);
+            const float w = __builtin_amdgcn_exp2f(fmaf(s, scale, -lse[j]) - rest[j]);
+            sum[t] += none[j] ? 0.0f : w;
           }
       };
       f32x4 st[R::kSub];
