@@ -114,8 +114,9 @@ int ag_prefix_run(ag_attn_handle* h, const ag_kv_cache* cache, const void* q, in
                   const int32_t* page_table, int64_t table_row, int64_t table_len, const int32_t* lens,
                   int64_t batch, void* out, int64_t o_batch, int64_t o_head, float* lse, void* scratch,
                   int64_t scratch_bytes, void* hip_stream) {
-  if (!h || attn_desc(h).window != 0 || groups < 0 || prefix_pages < 0) return AGMM_ERR_INVALID_ARG;
+  if (!h || groups < 0 || prefix_pages < 0) return AGMM_ERR_INVALID_ARG;
   const ag_attn_desc& d = attn_desc(h);
+  if (d.window != 0) return AGMM_ERR_UNSUPPORTED;
   AttnParams a;
   int grid = 0;
   int rc = attn_params(h, cache, q, q_batch, q_head, page_table, table_row, table_len, lens, batch, out,
