@@ -3,10 +3,10 @@
 // All of them read a stream of bytes and compute little on each, so many pages or tokens are bound by memory
 // bandwidth and few by the chain of a launch, the length, the page and its rows.
 //
-// Measured, warm: entries of a prompt of 16384 tokens (8 kv heads of 128, bf16, pages of 16) 7.6 us, 4.7 TB/s; scores of
-// 32 sequences of up to 32768 tokens, 8 kv heads: 12.3 us, of one of 131072 tokens, one kv head, pages of 64: 4.4; choosing
-// from 2048 pages 6.5 us, from 16384 tokens (one workgroup each, 256 of them) 26; moving 4096 rows of 32 sequences and 8
-// kv heads 217 us, 4.9 TB/s of reads and writes (a copy of 4 GiB runs at 4.7; four rows to a thread: 220).
+// Measured, warm: entries of a prompt of 16384 tokens (8 kv heads of 128, bf16, pages of 16) 7.8 us, 4.6 TB/s; scores of
+// 32 sequences of up to 32768 tokens, 8 kv heads: 12 us, of one of 131072 tokens, one kv head, pages of 64: 4.6; choosing
+// from 2048 pages 6.4 us, from 16384 tokens (one workgroup each, 256 of them) 26; moving 4096 rows of 32 sequences and 8
+// kv heads 216 us, 4.9 TB/s of reads and writes (a copy of 4 GiB runs at 4.7; four rows to a thread: 220).
 #include "agmm_attn_kernel.h"
 #include "agmm_long_internal.h"
 
@@ -434,7 +434,9 @@ __device__ inline uint32_t block_scan(uint32_t x, uint32_t* waves, uint32_t& all
 // histograms of 11, 11 and 10 bits (as many as it takes), then the chosen items written in order. A thread has K
 // consecutive items, in registers where the workgroup has all of them at once.
 //
-// One workgroup's time is what counts, and of that the instructions for each item.
+// One workgroup's time is what counts, and of that the instructions for each item. What is past T * K items is read again
+// for every histogram and for writing: 8 heads of 16384, 32768 and 131072 tokens take 14, 25 and 91 us, 256 of 16384 and 16400
+// 20 and 49 (in graphs).
 // keys: in global memory or, K = 1, in LDS.
 template <int T, int K, bool TOKENS>
 __device__ inline void choose_items(const ChooseParams& p, ChooseShared<T>& sh, const uint32_t* keys) {

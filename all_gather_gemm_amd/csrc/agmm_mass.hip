@@ -11,7 +11,8 @@
 // the last one's.
 //
 // Measured, warm: 32 sequences of 16384 tokens, 64/8 heads of 128, bf16: 205 us, 5.5 TB/s; one of 4096, 8/1 heads: 6.3 us
-// (launch, length, page, keys, each waiting for the one before).
+// (launch, length, page, keys, each waiting for the one before). Past 16 q heads to a kv head, q and log-sum-exp are read
+// again for every tile and group of 16: 32 sequences of 16384, one kv head, 16, 17, 32, 64 q heads 28, 34, 39, 53 us.
 #include "agmm_attn_kernel.h"
 #include "agmm_long_internal.h"
 

@@ -26,12 +26,15 @@
 // own tokens (agmm_attn_kernel.h) and leave theirs. A second kernel joins them all, in the order of the pieces, so
 // results do not depend on timing.
 //
-// Measured, with the joining: 256 sequences behind 32768 tokens, 64/8 heads of 128, bf16: 435 us (467 on another
-// card); the prefix by itself 393: 0.70 PFLOP/s counted once, 1.05 with both parts of the weights (the card's large
+// Measured, with the joining: 256 sequences behind 32768 tokens, 64/8 heads of 128, bf16: 429 to 467 us, from card to
+// card; the prefix by itself 393: 0.70 PFLOP/s counted once, 1.05 with both parts of the weights (the card's large
 // products run at 1.2, at its power limit; the clock is 1.9 GHz here). The matrix units are busy half of the cycles,
-// the vector units 60%.
-// 64 sequences behind 8192 tokens: 51 us, of which launch, lengths and pages take 10, the pieces' 33 MB 8, the joining
-// 9; a call of 4 behind 2000 tokens 14 + the host.
+// the vector units 60%, and 2192 MB are read, for 289 MB of prefix and own tokens, at 5 TB/s: every 128 rows read the
+// prefix again.
+// 64 sequences behind 8192 tokens: 51 us, of which products and weights take 28, launch, lengths and pages 10, the
+// writing of the pieces' 33 MB 8, the joining 8; a call of 4 behind 2000 tokens 14 + the host.
+// Kernels that spill registers, all of width 64 and 128: those with a cap 34 to 98 (64 sequences behind 8192 tokens, in a
+// graph: 64 us, 55.5 without), 16-bit rows through registers at width 128 10 and 11, e4m3's 6 and 7, e2m1's 1 or none.
 #pragma once
 
 #include "agmm_attn_kernel.h"
@@ -557,9 +560,11 @@ __device__ inline void prefix_share(const PrefixParams& p, TileShared<DP>& sh, c
 }
 
 // The length of the runs that prefixes' `total` tiles are cut into, so that the workgroups that are left for the
-// `own` tiles take as long. Each lane works out one length: a prefix's tile takes 3.15 us where two workgroups share
-// a compute unit (128 rows against 64 tokens of 128 elements), an own one some 3.5. Runs have at least `least` tiles,
-// as long as every compute unit gets one.
+// `own` tiles take as long. Each lane works out one length, with a prefix's tile at kTile of an own one, whatever the
+// width, the storage and the rows that the strip has. Runs have at least `least` tiles, as long as every compute unit
+// gets one.
+// kTile 0.65, 0.8, 0.9, 1.0, in graphs: 256 sequences behind 32768 tokens 435, 431, 432, 432 us; 64 of 2048 behind 8192
+// tokens, 64/8 heads, e4m3 61.6, 61.2, 60.5, 60.5, e2m1 61.0, 60.4, 60.2, 60.0; 32/8 heads of 256, 16 bits 105, 104, 111, 111.
 __device__ inline uint32_t run_length(uint32_t total, uint32_t own, uint32_t wgs, uint32_t least) {
   constexpr float kTile = 0.8f;
   const uint32_t lane = threadIdx.x & 63;
@@ -609,8 +614,9 @@ __global__ __launch_bounds__(kThreads, prefix_per_cu(DP)) void prefix_kernel(Pre
             PrefixGroup{r.first, r.end, r.tiles, r.row_tiles, r.strip0, r.tile0, quota, 0};
     }
   }
-  // Consecutive numbers to the workgroups of an XCD, which are 8 apart, so that strips of one kv head find its
-  // tiles in one L2; the first of each XCD's are the prefixes'.
+  // Consecutive numbers to the workgroups of an XCD, which are 8 apart, so that neighbouring runs share an L2 (strips of
+  // one kv head whose runs are a strip or so long read the same tiles; of a long prefix they are at other tokens);
+  // the first of each XCD's are the prefixes'.
   const uint32_t xcd = blockIdx.x % 8, local = blockIdx.x / 8;
   const uint32_t from = xcd * (wgs / 8) + min(xcd, wgs % 8), size = wgs / 8 + (xcd < wgs % 8 ? 1 : 0);
   const uint32_t first = (uint32_t)((uint64_t)x * from / wgs);

@@ -2,7 +2,7 @@
 (libagmm.so).
 
 `PrefixAttention` attends with one new token of every sequence where sequences share prefixes, which are
-read once for all that share one. `PageIndex` keeps bounds of every page's keys, and selects for each
+read once for every 128 rows (q heads of one kv head) of all that share one. `PageIndex` keeps bounds of every page's keys, and selects for each
 sequence and kv head the pages whose score is highest; DecodeAttention.run takes the table that it makes.
 `AttentionMass` adds up the weight that each cached token gets, `Evictor` keeps the tokens that got the
 most and moves their rows together. As in all of the package's modules, arguments are marshalled only: tensors'
@@ -82,7 +82,7 @@ class PrefixAttention(DecodeAttention):
 
     run(q, cache, prefix_table, prefix_lens, page_table, lens): q [batch, q_heads, head_dim]; prefix_table
     int32 [groups, pages] and prefix_lens int32 [groups]; page_table int32 [batch, pages] and lens int32
-    [batch] of the sequences' own tokens, the new one counted in. Group g has the sequences starts[g] to
+    [batch] of the sequences' own tokens, the new one counted in (no window). Group g has the sequences starts[g] to
     starts[g + 1] - 1 (starts int32 [groups + 1]); without starts there is one group, the whole batch.
     Returns out like q, or (out, lse) with lse float32 [batch, q_heads]. A handle serves one stream at a time."""
 
@@ -206,7 +206,7 @@ class AttentionMass:
 
     add(mass, q, lse, cache, page_table, lens) returns decay * mass plus, for each token, the softmax weights
     of the kv head's q heads: mass float32 [batch, kv_heads, tokens], q and lse [batch, q_heads] as the attention
-    took and gave them. Entries from lens on are copied. out may be mass itself."""
+    took and gave them, over one page table for all heads (not behind a shared prefix, nor over selected pages). Entries from lens on are copied. out may be mass itself."""
 
     def __init__(self, q_heads: int, kv_heads: int, head_dim: int, dtype: str = "bf16",
                  storage: str = "16bit", scale: float = 0.0, window: int = 0, soft_cap: float = 0.0):
@@ -261,7 +261,8 @@ class Evictor:
     def move(self, cache: PagedCache, page_table, kept, lens, to_table, to: Optional[PagedCache] = None,
              stream=None):
         """Row j of each sequence and kv head in the pages of to_table int32 [batch, pages] of `to` (the same
-        cache if None) becomes the row of token kept[..., j]. No page may be both read and written."""
+        cache if None) becomes the row of token kept[..., j]. No page may be both read and written, nor be in
+        two places of to_table."""
         to = self._destination(cache, page_table, lens, to_table, to)
         where = self._where(cache, page_table, lens, stream)
         _dense(_tensor(kept, "kept", torch.int32, (lens.shape[0], cache.kv_heads, kept.shape[2] if kept.dim() == 3

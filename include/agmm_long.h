@@ -3,7 +3,7 @@
  * the C ABI.
  *
  *   ag_prefix_*  attention of one new token of every sequence where sequences share prefixes, which are
- *                read once for all that share one;
+ *                read once for every 128 rows (q heads of one kv head) of all that share one;
  *   ag_index_*   an index of the cache's pages, the pages that its score selects for each sequence and kv
  *                head, and (ag_attn_run_heads) the attention over those;
  *   ag_mass_*    the attention weight that each cached token has got, added up step by step;
@@ -29,10 +29,12 @@ extern "C" {
  * < starts[g + 1]. Its tokens are the first prefix_lens[g] of the group's prefix and then its own, and its new
  * token attends to all of them, as in ag_attn_run. A sequence outside of all groups has its own tokens
  * alone. The prefixes' tokens and the own ones lie in one cache.
- * Two launches: all rows of a group (its sequences' q heads of one kv head) against the prefix, in pieces
- * that go to `scratch`, and then the own tokens, joined with those. Results do not depend on timing. */
+ * Two launches: all rows of a group (its sequences' q heads of one kv head) against the prefix and, beside them, the
+ * own tokens, in pieces that go to `scratch`; and then the pieces joined, in a fixed order. Results do not depend on
+ * timing. */
 
-/* Device bytes of a run's scratch, or a negative code. Host only. */
+/* Device bytes of a run's scratch, or a negative code. Host only. It has a piece for each workgroup that the chip holds,
+ * whatever the lengths: 17 MB for heads of up to 64 and 34 above, and 8 bytes for each element of a row. */
 int64_t ag_prefix_scratch_bytes(const ag_attn_desc* desc, int64_t batch, int64_t groups);
 
 /* One run of a handle of ag_attn_create whose desc has no window, and a cap or a scale of 2^63 at most (else
@@ -104,7 +106,9 @@ int ag_attn_run_heads(ag_attn_handle* h, const ag_kv_cache* cache, const void* q
                       int64_t table_len, const int32_t* lens, int64_t batch, void* out, int64_t o_batch,
                       int64_t o_head, float* lse, void* hip_stream);
 
-/* ---- eviction by accumulated attention weight ---- */
+/* ---- eviction by accumulated attention weight ----
+ * Weights come from the new tokens of ag_attn_run over one page table for all heads: not from a prompt's own q, behind
+ * a shared prefix or over selected pages. */
 
 /* For every sequence b, kv head h and token t < lens[b]:
  *     out[b][h][t] = decay * mass[b][h][t] + sum over h's q heads of exp(s_t - lse)
@@ -138,7 +142,7 @@ int ag_evict_choose(const ag_kv_cache* cache, const float* mass, int64_t mass_ba
 /* Moves kept tokens' rows together: row j of sequence b and kv head h in `to` is set to the row of token
  * kept[b][h][j] in `from`, for j < lens[b] and j < budget, keys, values and scales. Rows whose page is absent, in
  * either table, are left as they are. The two caches have one dtype, storage, head_dim and kv_heads; no page may be
- * both read and written.
+ * both read and written. A row that is written twice (a page in several places of to_table) is left undefined.
  *   kept: as above; lens: device int32 [batch].
  * Returns AGMM_OK, INVALID_ARG, UNSUPPORTED or HIP. */
 int ag_evict_move(const ag_kv_cache* from, const int32_t* from_table, int64_t from_row, int64_t from_len,
