@@ -26,7 +26,7 @@
 // own tokens (agmm_attn_kernel.h) and leave theirs. A second kernel joins them all, in the order of the pieces, so
 // results do not depend on timing.
 //
-// Measured, with the joining: 256 sequences behind 32768 tokens, 64/8 heads of 128, bf16: 429 to 467 us, from card to
+// Measured, with the joining: 256 sequences behind 32768 tokens, 64/8 heads of 128, bf16: 429 to 468 us, from card to
 // card; the prefix by itself 393: 0.70 PFLOP/s counted once, 1.05 with both parts of the weights (the card's large
 // products run at 1.2, at its power limit; the clock is 1.9 GHz here). The matrix units are busy half of the cycles,
 // the vector units 60%, and 2192 MB are read, for 289 MB of prefix and own tokens, at 5 TB/s: every 128 rows read the

@@ -76,7 +76,8 @@ typedef struct ag_page_index {
  *   page_table, table_row, table_len, lens: as for ag_attn_run;
  *   starts: device int32 [batch], < 0 counts as 0; NULL: 0 for all.
  * Absent pages are left out. A page in several of the places that are renewed gets the entry of the one with the most of
- * its tokens. (To find that, a sequence that ends inside a page reads the numbers of all pages that the call renews.)
+ * its tokens; places in front of starts[b] do not count. (To find that, a sequence that ends inside a page reads the
+ * numbers of all pages that the call renews.)
  * Returns AGMM_OK, INVALID_ARG, UNSUPPORTED or HIP. */
 int ag_index_update(const ag_kv_cache* cache, const ag_page_index* index, const int32_t* page_table,
                     int64_t table_row, int64_t table_len, const int32_t* starts, const int32_t* lens,
